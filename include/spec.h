@@ -46,6 +46,7 @@
 #ifndef SPEC_H
 #define SPEC_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -396,6 +397,134 @@ spec_status spec_trace_kinds(spec_handle h, int32_t* out, int32_t capacity, int3
  * at zero.  Asynchronous on cuda_stream (a cudaStream_t, NULL = default). */
 spec_status spec_accept_from_logits_noalloc(const float* d_logits, int32_t n, int32_t vocab, const int32_t* d_block,
                                             int32_t* d_argmax, int32_t* d_accept_len, void* cuda_stream);
+
+/* ---- a paged cache shared by many sequences ----
+ *
+ * The handle's own caches give every sequence a region of max_ctx positions.
+ * These calls serve a caller that runs its own projections and keeps many
+ * sequences of very different lengths in one pool of pages: the pages are
+ * handed out and taken back on the device as blocks of drafts are accepted
+ * and rejected (DFlash README: verify, accept, crop on rejection), so a
+ * verify cycle needs no host round trip:
+ *   spec_pages_step       crop every sequence, add its new block: tables, slots
+ *   spec_paged_append     the block's keys and values to their slots (per layer)
+ *   spec_paged_attention  the block's queries over the pages        (per layer)
+ * They need no handle.  They run on the current device, which must own every
+ * buffer, and enqueue on cuda_stream (a cudaStream_t, NULL = legacy default
+ * stream); the caller orders streams.  All are asynchronous, allocate nothing,
+ * keep nothing between calls and can be captured into a graph.
+ *
+ * Layout.  A page holds SPEC_PAGE positions.  Pools of keys and of values are
+ * bf16 [num_pages][n_kv_heads][SPEC_PAGE][head_dim], one pair per layer (all
+ * layers use the same tables); position t of sequence q is entry t % SPEC_PAGE
+ * of page d_tables[q][t / SPEC_PAGE]; its slot is page * SPEC_PAGE + t %
+ * SPEC_PAGE.  Sequence q of length len holds the first ceil(len / SPEC_PAGE)
+ * entries of its table row; what stands behind them is never read.
+ *
+ * Device values are checked on the device: a kernel that meets a bad one reads
+ * and writes nothing through it and puts one of the codes below into the error
+ * word, unless that already holds one.  The error word of spec_pages_step is
+ * d_pool[SPEC_POOL_ERROR]; the other calls take any int32 (that word too), or
+ * NULL. */
+#define SPEC_PAGE 64             /* positions per page                             */
+#define SPEC_MAX_SEQS 1024       /* sequences per call                             */
+#define SPEC_MAX_PAGES 33554431  /* pages of one pool (a slot fits int32)          */
+#define SPEC_MAX_TABLE 1048576   /* table entries per sequence                     */
+#define SPEC_POOL_HEADER 8       /* int32 words in front of the free stack         */
+#define SPEC_POOL_FREE 0         /* header word: number of free pages              */
+#define SPEC_POOL_ERROR 1        /* header word: error code, 0 = none              */
+enum {
+    SPEC_PAGED_BAD_LENGTH = 1, /* a length, keep or add out of range, or more pages than a table row holds */
+    SPEC_PAGED_BAD_ROWS = 2,   /* more new rows than the buffers hold, or row starts that are not rising   */
+    SPEC_PAGED_NO_PAGES = 3,   /* the pool has too few free pages                                          */
+    SPEC_PAGED_BAD_PAGE = 4,   /* a page or slot outside the pool                                          */
+    SPEC_PAGED_TIMEOUT = 5     /* a bounded device wait gave up                                            */
+};
+
+/* d_pool: int32[SPEC_POOL_HEADER + num_pages], CALLER-owned: a header, then
+ * the stack of free pages.  All pages become free; page 0 is handed out
+ * first.  1 <= num_pages <= SPEC_MAX_PAGES.  The header's other words belong
+ * to the library. */
+spec_status spec_pages_init(int32_t* d_pool, int32_t num_pages, void* cuda_stream);
+
+/* Crop every sequence to its first keep positions, then add `add` new ones.
+ *   d_tables  int32 [nseq][table_pages], updated: entries of pages taken now are
+ *             written, every other entry is left as it was;
+ *   d_len     int32 [nseq], updated: the length before the call, then keep + add;
+ *   d_keep    int32 [nseq], 0 <= keep <= length.  After a verify of n tokens at
+ *             length p + n that accepted k drafts: p + k + 1.  0 takes every
+ *             page of the sequence back.  May be d_len itself (crops nothing);
+ *   d_add     int32 [nseq], >= 0; 0 leaves a sequence idle;
+ *   d_row_start int32 [nseq + 1], written: sequence q's new positions are the
+ *             rows row_start[q] .. row_start[q+1]-1 of the call's row order;
+ *   d_slots   int32 [row_cap], written: the slot of each new row; entries from
+ *             row_start[nseq] on are left as they were.
+ * Order: pages that crops leave over are put on the free stack in (sequence,
+ * page) order, then new pages are taken from its top in (sequence, page) order.
+ * All or nothing: with a bad length, more than row_cap rows or too few free
+ * pages the call sets d_pool[SPEC_POOL_ERROR] and d_row_start to zeros (later
+ * calls of the cycle then find no rows) and changes nothing else.
+ * 0 <= nseq <= SPEC_MAX_SEQS (0: nothing is done); 1 <= table_pages <=
+ * SPEC_MAX_TABLE; row_cap >= 0 (d_slots may be NULL when 0).  Calls on one pool
+ * must not overlap.  Errors: SPEC_ERR_INVALID_ARG, nothing enqueued. */
+spec_status spec_pages_step(int32_t* d_pool, int32_t num_pages, int32_t* d_tables, int32_t table_pages, int32_t* d_len,
+                            const int32_t* d_keep, const int32_t* d_add, int32_t nseq, int32_t* d_row_start,
+                            int32_t* d_slots, int32_t row_cap, void* cuda_stream);
+
+/* Write new keys and values at their slots.
+ *   d_k, d_v   bf16 rows of [n_kv_heads][head_dim], consecutive rows k_stride
+ *              (v_stride) elements apart, so that both may be parts of a fused
+ *              QKV output; 16-byte aligned, strides multiples of 8 and at least
+ *              n_kv_heads * head_dim;
+ *   d_slots    int32 [rows]: a negative slot skips its row (padding).  The
+ *              slots of one call are distinct (of two rows with one slot either
+ *              may stay, piecewise);
+ *   d_row_count_opt  NULL, or a device int32: only rows below it are written
+ *              (e.g. d_row_start + nseq);
+ *   d_kpool, d_vpool  16-byte aligned pools of num_pages pages.
+ * head_dim is 64 or 128. */
+spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_slots,
+                              const int32_t* d_row_count_opt, int32_t rows, int32_t n_kv_heads, int32_t head_dim,
+                              void* d_kpool, void* d_vpool, int32_t num_pages, int32_t* d_error_opt, void* cuda_stream);
+
+/* Attention of each sequence's newest positions over its pages.  Sequence q's
+ * m = row_start[q+1] - row_start[q] rows are its last m positions; row j, at
+ * position t = len[q] - m + j, attends to positions 0..t:
+ *   out[row][h] = sum_i softmax_i(scale * q[row][h] . k_i) v_i
+ * with kv head h / (n_heads / n_kv_heads).  Scores, softmax and sums are fp32;
+ * q, k, v and out are bf16.  A row with no position (t < 0) gets zeros.
+ *   d_q        rows of [n_heads][head_dim], q_stride elements apart;
+ *   d_out      the same with out_stride; rows outside every sequence are left
+ *              as they were; must not overlap d_q;
+ *   d_row_start int32 [nseq + 1], rising, within [0, rows];
+ *   d_len      int32 [nseq], lengths with the new positions, at most
+ *              table_pages * SPEC_PAGE;
+ *   max_new    the most rows of any sequence, 1 or more: it picks the tile
+ *              height and is no bound (larger blocks are right, only slower);
+ *   d_work     work_bytes of scratch, 256-byte aligned, at least what
+ *              spec_paged_attention_workspace says for the same heads and
+ *              max_new.  Its contents need not be set and mean nothing between
+ *              calls; calls that may run at the same time need one each.
+ * Values behind a sequence's length are never used, whatever they are (NaN
+ * too), nor is a position that a row may not see.  A visible value that is
+ * infinite or NaN makes that dimension of the rows that see it non-finite.
+ * A sequence with a bad length or row range is skipped (its rows stay as they
+ * were); a bad page reads as zeros.  Both set the error word.
+ * The same call gives the same bits; how keys are grouped depends on the
+ * lengths in the call, so a sequence's last bits may differ from batch to
+ * batch.
+ * Pointers 16-byte aligned, strides multiples of 8 and at least n_heads *
+ * head_dim; head_dim 64 or 128; n_heads a multiple of n_kv_heads, at most 128
+ * query heads per kv head; scale positive and finite; 0 <= nseq <=
+ * SPEC_MAX_SEQS (nseq or rows 0: nothing is done). */
+spec_status spec_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
+                                           size_t* out_bytes);
+spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_t* d_row_start, const int32_t* d_len,
+                                 const int32_t* d_tables, int32_t table_pages, int32_t nseq, int32_t rows,
+                                 int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale,
+                                 const void* d_kpool, const void* d_vpool, int32_t num_pages, void* d_out,
+                                 int64_t out_stride, int32_t* d_error_opt, void* d_work, size_t work_bytes,
+                                 void* cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,10 @@ SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_CAPACITY, SPEC_ERR_STATE, SPEC_ERR_CUDA,
 SPEC_MOE_PER_SLOT, SPEC_MOE_DEDUP = 0, 1
 SPEC_CACHE_TARGET, SPEC_CACHE_DRAFT = 0, 1
 SPEC_MAX_BLOCK = 16
+SPEC_PAGE, SPEC_MAX_SEQS, SPEC_MAX_PAGES, SPEC_MAX_TABLE = 64, 1024, 33554431, 1048576
+SPEC_POOL_HEADER, SPEC_POOL_FREE, SPEC_POOL_ERROR = 8, 0, 1
+(SPEC_PAGED_BAD_LENGTH, SPEC_PAGED_BAD_ROWS, SPEC_PAGED_NO_PAGES, SPEC_PAGED_BAD_PAGE,
+ SPEC_PAGED_TIMEOUT) = range(1, 6)
 
 EXPORTED = ["spec_model_create", "spec_model_destroy", "spec_set_draft_plan", "spec_set_stream", "spec_prefill",
             "spec_draft_step", "spec_verify_step", "spec_kv_rollback", "spec_moe_mode", "spec_last_error",
@@ -29,7 +33,9 @@ EXPORTED = ["spec_model_create", "spec_model_destroy", "spec_set_draft_plan", "s
             "spec_accept_from_logits_noalloc", "spec_trace_enable", "spec_trace_read", "spec_trace_kinds",
             "spec_set_taps", "spec_set_context_fc", "spec_context_append", "spec_batch_reserve",
             "spec_batch_kv_load", "spec_batch_kv_export", "spec_batch_set_len", "spec_batch_len",
-            "spec_verify_batch", "spec_share_prefix", "spec_draft_step_logits", "spec_accept_sampled"]
+            "spec_verify_batch", "spec_share_prefix", "spec_draft_step_logits", "spec_accept_sampled",
+            "spec_pages_init", "spec_pages_step", "spec_paged_append", "spec_paged_attention_workspace",
+            "spec_paged_attention"]
 
 
 class SpecError(RuntimeError):
@@ -72,7 +78,7 @@ def library():
         raise RuntimeError("libspecverify.so is not built; run __graft_entry__.build() "
                            "(the CUDA path has no fallback)")
     lib = ctypes.CDLL(LIB_PATH)
-    i32, vp = ctypes.c_int32, ctypes.c_void_p
+    i32, i64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
     sig = {
         "spec_model_create": [ctypes.POINTER(ModelConfigC), ctypes.POINTER(WeightsC), vp, i32, vp, ctypes.POINTER(vp)],
         "spec_model_destroy": [vp],
@@ -109,6 +115,12 @@ def library():
         "spec_trace_enable": [vp, i32],
         "spec_trace_read": [vp, vp, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "spec_trace_kinds": [vp, vp, i32, ctypes.POINTER(i32)],
+        "spec_pages_init": [vp, i32, vp],
+        "spec_pages_step": [vp, i32, vp, i32, vp, vp, vp, i32, vp, vp, i32, vp],
+        "spec_paged_append": [vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp],
+        "spec_paged_attention_workspace": [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "spec_paged_attention": [vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32,
+                                 vp, i64, vp, vp, ctypes.c_size_t, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -309,6 +321,143 @@ def spec_accept_from_logits_noalloc(d_logits, d_block, d_argmax, d_accept_len, s
     st = _stream() if stream is None else ctypes.c_void_p(stream)
     _check(library().spec_accept_from_logits_noalloc(_ptr(d_logits), n, vocab, _ptr(d_block), _ptr(d_argmax),
                                                      _ptr(d_accept_len), st))
+
+
+# ----------------------------------------------------------------------------
+# A paged cache shared by many sequences (no handle; the current torch stream)
+# ----------------------------------------------------------------------------
+def _refuse(msg):
+    raise SpecError(SPEC_ERR_INVALID_ARG, msg)
+
+
+def _cuda_i32(name, t, need=0):
+    """Data pointer of a contiguous int32 CUDA tensor of at least need entries."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()
+            and t.numel() >= need):
+        _refuse("%s must be a contiguous int32 CUDA tensor of at least %d entries" % (name, need))
+    return t.data_ptr()
+
+
+def _rows_bf16(name, t, heads=None, head_dim=None):
+    """(pointer, row stride) of a bf16 CUDA tensor [rows][heads][head_dim] whose
+    rows are contiguous; the rows may lie any distance apart."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and t.dim() == 3):
+        _refuse("%s must be a 3-D bfloat16 CUDA tensor" % name)
+    rows, h, d = t.shape
+    if (heads is not None and h != heads) or (head_dim is not None and d != head_dim):
+        _refuse("%s must be [rows][%s][%s]" % (name, heads, head_dim))
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        _refuse("the rows of %s must be contiguous [heads][head_dim] blocks" % name)
+    return t.data_ptr(), s0 if rows > 1 else h * d
+
+
+def _pools(d_kpool, d_vpool):
+    """(pages, kv heads, head_dim) of a key and a value pool."""
+    import torch
+    for name, t in (("d_kpool", d_kpool), ("d_vpool", d_vpool)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and t.dim() == 4
+                and t.shape[2] == SPEC_PAGE and t.is_contiguous()):
+            _refuse("%s must be a contiguous bfloat16 CUDA tensor [pages][kv heads][%d][head_dim]" % (name, SPEC_PAGE))
+    if d_kpool.shape != d_vpool.shape:
+        _refuse("d_kpool and d_vpool must have the same shape")
+    pages, heads, _, hd = d_kpool.shape
+    return pages, heads, hd
+
+
+def _same_device(first, *others):
+    """Every buffer on the current device (the calls run there); returns its
+    raw current stream."""
+    import torch
+    dev = first.device.index
+    if dev != torch.cuda.current_device():
+        _refuse("the buffers must be on the current CUDA device")
+    for t in others:
+        if t is not None and t.device.index != dev:
+            _refuse("the buffers must all be on the current CUDA device")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def spec_pages_init(d_pool):
+    """All pages of d_pool (int32 [SPEC_POOL_HEADER + pages]) become free."""
+    ptr = _cuda_i32("d_pool", d_pool, SPEC_POOL_HEADER + 1)
+    _check(library().spec_pages_init(ptr, d_pool.numel() - SPEC_POOL_HEADER, _same_device(d_pool)))
+
+
+def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots):
+    """Crop every sequence to d_keep positions and add d_add new ones: tables
+    int32 [nseq][table_pages], lengths, keep and add int32 [nseq]; writes
+    row_start [nseq + 1] and the new rows' slots.  Errors that only the device
+    can see land in d_pool[SPEC_POOL_ERROR]."""
+    pool = _cuda_i32("d_pool", d_pool, SPEC_POOL_HEADER + 1)
+    tables = _cuda_i32("d_tables", d_tables)
+    if d_tables.dim() != 2:
+        _refuse("d_tables must be [nseq][table_pages]")
+    nseq, width = d_tables.shape
+    args = (_cuda_i32("d_len", d_len, nseq), _cuda_i32("d_keep", d_keep, nseq), _cuda_i32("d_add", d_add, nseq), nseq,
+            _cuda_i32("d_row_start", d_row_start, nseq + 1), _cuda_i32("d_slots", d_slots), d_slots.numel())
+    st = _same_device(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots)
+    _check(library().spec_pages_step(pool, d_pool.numel() - SPEC_POOL_HEADER, tables, width, *args, st))
+
+
+def spec_paged_append(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_error=None):
+    """Write the rows of d_k and d_v (bf16 [rows][kv heads][head_dim], rows any
+    distance apart) at their slots; only rows below the device int32
+    d_row_count (None: all)."""
+    pages, heads, hd = _pools(d_kpool, d_vpool)
+    k, ks = _rows_bf16("d_k", d_k, heads, hd)
+    v, vs = _rows_bf16("d_v", d_v, heads, hd)
+    rows = d_k.shape[0]
+    if d_v.shape[0] != rows:
+        _refuse("d_k and d_v must have the same number of rows")
+    slots = _cuda_i32("d_slots", d_slots, rows)
+    count = None if d_row_count is None else _cuda_i32("d_row_count", d_row_count, 1)
+    err = None if d_error is None else _cuda_i32("d_error", d_error, 1)
+    st = _same_device(d_kpool, d_vpool, d_k, d_v, d_slots, d_row_count, d_error)
+    _check(library().spec_paged_append(k, ks, v, vs, slots, count, rows, heads, hd, d_kpool.data_ptr(),
+                                       d_vpool.data_ptr(), pages, err, st))
+
+
+def spec_paged_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
+    """Bytes of scratch a spec_paged_attention call with these heads needs."""
+    out = ctypes.c_size_t(0)
+    _check(library().spec_paged_attention_workspace(int(n_heads), int(n_kv_heads), int(head_dim), int(max_new),
+                                                    ctypes.byref(out)))
+    return int(out.value)
+
+
+def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, max_new, scale=None, d_out=None,
+                         d_error=None, d_work=None):
+    """Attention of each sequence's newest rows over its pages; returns d_out
+    (bf16 [rows][heads][head_dim]; a new tensor when None, whose rows outside
+    every sequence are then unset).  scale defaults to head_dim ** -0.5; d_work
+    (a uint8 tensor) to scratch from torch's allocator."""
+    import torch
+    pages, hkv, hd = _pools(d_kpool, d_vpool)
+    q, qs = _rows_bf16("d_q", d_q, None, hd)
+    rows, hq, _ = d_q.shape
+    tables = _cuda_i32("d_tables", d_tables)
+    if d_tables.dim() != 2:
+        _refuse("d_tables must be [nseq][table_pages]")
+    nseq, width = d_tables.shape
+    if d_out is None:
+        d_out = torch.empty((rows, hq, hd), dtype=torch.bfloat16, device=d_q.device)
+    out, os_ = _rows_bf16("d_out", d_out, hq, hd)
+    if d_out.shape[0] != rows:
+        _refuse("d_out must have as many rows as d_q")
+    args = (_cuda_i32("d_row_start", d_row_start, nseq + 1), _cuda_i32("d_len", d_len, nseq), tables, width, nseq, rows,
+            int(max_new), hq, hkv, hd, hd ** -0.5 if scale is None else float(scale))
+    err = None if d_error is None else _cuda_i32("d_error", d_error, 1)
+    st = _same_device(d_q, d_out, d_kpool, d_vpool, d_row_start, d_len, d_tables, d_error, d_work)
+    if d_work is None:
+        d_work = torch.empty(spec_paged_attention_workspace(hq, hkv, hd, max_new), dtype=torch.uint8, device=d_q.device)
+    elif not (d_work.dtype is torch.uint8 and d_work.is_cuda and d_work.is_contiguous()):
+        _refuse("d_work must be a contiguous uint8 CUDA tensor")
+    _check(library().spec_paged_attention(q, qs, *args, d_kpool.data_ptr(), d_vpool.data_ptr(), pages, out, os_, err,
+                                          d_work.data_ptr(), d_work.numel(), st))
+    return d_out
 
 
 # ----------------------------------------------------------------------------
