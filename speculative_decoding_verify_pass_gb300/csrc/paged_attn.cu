@@ -6,24 +6,30 @@
 // and the rows are the narrow side.  Per 128-position chunk (two pages):
 //     S^T = K Q^T      M = 128 keys,       N = R rounded up to 16, K = head dim
 //     P^T = exp2(scale log2e S^T - m)
-//     O^T += V^T P^T   M = head dimensions, N as above,            K = 128 keys
+//     O^T += V^T P^T   M = head dimensions, N = as above,          K = 128 keys
 // TMA tiles of 64 positions x 64 dimensions land with the 128-byte swizzle and
 // are MMA operands as they lie: K rows are K-major, V rows are MN-major (V^T
 // without a transpose).  P^T is kept as a bf16 high and a bf16 low part (about
-// 16 significant bits), so that only the result's own rounding shows.
+// 16 significant bits), so that only the result's own rounding shows; up to 32
+// rows the two parts lie side by side in one product's N (an MMA that narrow
+// costs the same for 16 columns as for 64), with a column each in tensor memory.
 //
-// The softmax needs no maximum of its own per chunk: m is a reference that
-// every row takes from its segment's first chunk.  A later score may exceed it
-// by up to 2^40 (fp32 and bf16 hold that), and only if one exceeds it by more do
-// the row's reference, sum and O^T get rescaled.  So per chunk and element there
-// is one multiply-add, one exp2, one add to the thread's own partial sum and the
-// two roundings; nothing crosses lanes until the segment ends.
+// The softmax needs no maximum: m is a reference that a row takes from the score
+// of one key, the first of its first chunk.  Any score may exceed it by up to
+// 2^40 (fp32 and bf16 hold that), and only when one exceeds it by more do the
+// row's reference, sum and O^T move to the chunk's maximum.  So per chunk and
+// element there is one multiply-add, one exp2, one add to the thread's own
+// partial sum and the two roundings; nothing crosses lanes until the segment
+// ends.
 //
-// Roles: warps 0-7 softmax (thread = key, then head dimension; each warpgroup
-// half of the rows), warp 8 issues the MMAs, warp 9 the TMA copies.  S^T of the
-// next chunk is computed while a chunk's softmax runs.  One CTA per SM, each
-// with the same number of chunks (paged_split.h); a second kernel joins the
-// pairs that were split between CTAs.
+// Roles: warps 0-7 softmax (thread = key, then head dimension), warp 8 issues
+// the MMAs, warp 9 the TMA copies.  Up to 64 rows the two warpgroups take
+// alternate chunks, each with its own reference, sum and O^T (joined when the
+// segment ends): a warp's chain of dependent instructions is what a chunk of few
+// rows costs, and two chains run side by side.  128 rows are halved between the
+// warpgroups instead (shared memory has no room for two P^T).  One CTA per SM,
+// each with the same number of chunks (paged_split.h); a second kernel joins
+// the pairs that were split between CTAs.
 #include <cuda.h>
 #include <math.h>
 
@@ -41,16 +47,18 @@ constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
 constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -1e30f;         // reference of a row that has seen no key
+constexpr int kSoftBar = 1, kBothBar = 3;   // named barriers: one per warpgroup, one for both
 
-// What the join kernel needs to know of the pair that begins in a CTA and goes on in the next ones.
+// A split pair, as the join kernel sees it from one of its CTAs.
 struct Meta {
     int count;                  // partials (0: no such pair)
+    int owner;                  // the CTA where it begins
     int slot;                   // the owner's slot
     int rows;                   // R
     int head;                   // first query head
     int row0;                   // first row of the call
     int last0;                  // last visible position of the first token
-    int pad[2];
+    int pad;
 };
 
 struct PagedParams {
@@ -65,24 +73,28 @@ struct PagedParams {
     int* err;
     float* part_o;              // [2 * ctas][RP][HD]
     float2* part_ml;            // [2 * ctas][RP] (reference, sum)
-    Meta* meta;                 // [ctas]
+    Meta* meta;                 // [ctas][2]: the pair that goes on into the CTA, the pair that begins in it and goes on
 };
 
 // Shared-memory plan: NQ query tiles, NP pairs of P^T parts, NS slots that
 // alternately take a chunk's K and V.
 template <int HD, int RP>
 struct Plan {
+    static constexpr bool kStream = RP <= 64;               // warpgroups take alternate chunks
+    static constexpr bool kStack = RP <= 32;                // P^T's parts in one product
     static constexpr int kSlot = kChunk * HD * 2;
     static constexpr int kQ = RP * HD * 2;
     static constexpr int kP = kChunk * RP * 2;              // one part
     static constexpr int NQ = RP <= 32 ? 2 : 1;
-    static constexpr int NP = RP <= 64 ? 2 : 1;
+    static constexpr int NP = kStream ? 2 : 1;
     static constexpr int kFixed = NQ * kQ + NP * 2 * kP + 2048;   // alignment, pad after the last slot
-    static constexpr int kMost = 227 * 1024 - (6144 + 40 * RP) - kFixed; // less the static arrays
+    static constexpr int kMost = 227 * 1024 - (6144 + 64 * RP) - kFixed; // less the static arrays
     static constexpr int NS = kMost / kSlot < 8 ? kMost / kSlot : 8;
     static constexpr int kBytes = kFixed + NS * kSlot;
-    static constexpr int kCols = 4 * RP;                    // tensor-memory columns: S^T x 2, O^T x 2
-    static_assert(NS >= 3, "a chunk's K and the previous chunk's V are live together");
+    static constexpr int kO = kStack ? 2 * RP : RP;         // tensor-memory columns of one O^T
+    static constexpr int kUsed = 2 * RP + (kStream ? 4 : 2) * kO;   // S^T x 2, O^T x 2 (per warpgroup)
+    static constexpr int kCols = kUsed <= 256 ? 256 : 512;
+    static_assert(NS >= 3 && kUsed <= 512, "a chunk's K and the previous chunk's V are live together");
 };
 
 __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -101,11 +113,8 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
            (2ull << 61);
 }
 
-// N consecutive fp32 columns of this warp's 32 lanes (N = 8, 16, 32).
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t t, float* v);
-template <>
-__device__ __forceinline__ void tmem_ld<8>(uint32_t t, float* v) {
+// 8 consecutive fp32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8_async(uint32_t t, float* v) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -128,6 +137,24 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ uint32_t cvt_bf16x2(float a, float b) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Two fp32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
 
@@ -159,6 +186,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) __nanosleep(64);
 }
+
+// Position in a ring of N buffers: index and the parity of its current round.
+template <int N>
+struct Ring {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) at = 0, round ^= 1;
+    }
+};
 
 // A CTA's segments in order; every role walks its own copy.
 struct Walk {
@@ -195,24 +232,43 @@ struct Walk {
     __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
     // last position that the block's first token sees
     __device__ __forceinline__ int last0() const { return len - rows + block * p.tokens; }
+    // the segment's pair, for the join; T units on `work` CTAs
+    __device__ Meta meta(int T, int work) const {
+        const int pair_begin = u - c1, owner = split::cta_of(pair_begin, T, work);
+        Meta m;
+        m.count = split::contributors(owner, pair_begin + chunks, T, work);
+        m.owner = owner;
+        m.slot = 2 * owner + (pair_begin == split::begin_of(owner, T, work) ? 0 : 1);
+        m.rows = R;
+        m.head = head * p.group;
+        m.row0 = row_base + block * p.tokens;
+        m.last0 = last0();
+        m.pad = 0;
+        return m;
+    }
 };
 
 template <int HD, int RP>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p) {
     using L = Plan<HD, RP>;
+    constexpr bool kStream = L::kStream, kStack = L::kStack;
     constexpr int NS = L::NS, NP = L::NP, NQ = L::NQ;
-    constexpr int CW = RP / 2;          // rows of a warpgroup
+    constexpr int NC = kStream ? RP : RP / 2;   // rows of a softmax thread
+    constexpr int kGroups = kStream ? 2 : 1;    // O^T's (and references) of a segment
+    constexpr int kArrive = kStream ? 4 : 8;    // warps that read an S^T and write a P^T
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[NQ], q_empty[NQ], s_full[2], s_empty[2], p_full[NP], p_empty[NP],
         o_full[2], o_empty[2], fin;
     __shared__ uint32_t tmem_base;
-    __shared__ int dead, poison[2], total;
+    __shared__ int dead, total;
+    __shared__ int poison[2];                           // 1 + the last segment (by parity) that silenced a value
     __shared__ int first[split::kMaxSeqs + 1];
     __shared__ long long warp_sum[kThreads / 32];
-    __shared__ __align__(16) float mref[RP];            // reference of each row
-    __shared__ __align__(16) float xred[4][RP];         // per lane quadrant: maxima, then sums
-    __shared__ __align__(16) int tok[RP];               // token of each row
-    __shared__ long long col_off[RP];                   // its offset in the output
+    __shared__ __align__(16) float nref[2][kGroups][RP];    // by segment parity: minus each row's reference
+    __shared__ __align__(16) float xl[2][kGroups][4][RP];   // per lane quadrant: sums (and, while a reference moves, maxima)
+    __shared__ float2 weight[2][RP];                        // what the two O^T's of a row are multiplied with
+    __shared__ __align__(16) int tok[RP];                   // token of each row
+    __shared__ long long col_off[RP];                       // its offset in the output
 
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* slots = base;
@@ -231,13 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], kSoftWarps);
+            mbar_init(&s_empty[i], kArrive);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], kSoftWarps);
             poison[i] = 0;
         }
         for (int i = 0; i < NP; ++i) {
-            mbar_init(&p_full[i], kSoftWarps);
+            mbar_init(&p_full[i], kArrive);
             mbar_init(&p_empty[i], 1);
         }
         mbar_init(&fin, 1);
@@ -304,19 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (warp == kLoadWarp) {
         // ---------------- TMA copies (lane 0 issues; the lanes look up pages) ----------------
         Walk w(p, first, begin, end);
-        int fill = 0;
+        Ring<NS> kv;
+        Ring<NQ> qr;
         bool ok = true;
         while (ok && w.next()) {
             if (lane == 0) {
-                uint64_t* qf = &q_full[w.seg % NQ];
-                ok = wait(&q_empty[w.seg % NQ], ((w.seg / NQ) & 1) ^ 1, deadp);
+                uint64_t* qf = &q_full[qr.at];
+                ok = wait(&q_empty[qr.at], qr.round ^ 1, deadp);
                 if (ok) {
                     mbar_arrive_expect_tx(qf, (uint32_t)(p.tokens * p.group * HD * 2));
 #pragma unroll
                     for (int hf = 0; hf < HD / 64; ++hf)
-                        tma3(qs + (w.seg % NQ) * L::kQ + hf * RP * 128, &p.mq, hf * 64, w.head * p.group,
+                        tma3(qs + qr.at * L::kQ + hf * RP * 128, &p.mq, hf * 64, w.head * p.group,
                              w.row_base + w.block * p.tokens, qf);
                 }
+                qr.step();
             }
             const int held = (w.len + SPEC_PAGE - 1) / SPEC_PAGE;
             const int* tab = p.tables + (size_t)w.q * p.table_pages;
@@ -341,60 +399,75 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 if (lane == 0 && ok) {
                     const int n = min(2, held - 2 * c);   // pages that exist (a bad one reads as zeros: z = -1)
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int s = fill % NS;
-                        ok = ok && wait(&kv_empty[s], ((fill / NS) & 1) ^ 1, deadp);
+                    for (int v = 0; v < 2; ++v) {
+                        ok = ok && wait(&kv_empty[kv.at], kv.round ^ 1, deadp);
                         if (!ok) break;
-                        uint8_t* dst = slots + s * L::kSlot;
-                        const CUtensorMap* map = kv ? &p.mv : &p.mk;
-                        mbar_arrive_expect_tx(&kv_full[s], n > 0 ? (uint32_t)(n * SPEC_PAGE * HD * 2) : 0u);
+                        uint8_t* dst = slots + kv.at * L::kSlot;
+                        uint64_t* full = &kv_full[kv.at];
+                        const CUtensorMap* map = v ? &p.mv : &p.mk;
+                        mbar_arrive_expect_tx(full, n > 0 ? (uint32_t)(n * SPEC_PAGE * HD * 2) : 0u);
 #pragma unroll
                         for (int hf = 0; hf < HD / 64; ++hf) {
-                            if (n > 0) tma3(dst + hf * kChunk * 128, map, hf * 64, 0, a0, &kv_full[s]);
-                            if (n > 1) tma3(dst + hf * kChunk * 128 + SPEC_PAGE * 128, map, hf * 64, 0, a1, &kv_full[s]);
+                            if (n > 0) tma3(dst + hf * kChunk * 128, map, hf * 64, 0, a0, full);
+                            if (n > 1) tma3(dst + hf * kChunk * 128 + SPEC_PAGE * 128, map, hf * 64, 0, a1, full);
                         }
-                        ++fill;
+                        kv.step();
                     }
                 }
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
-        if (lane == 0 && *deadp) {
-            for (int f = fill > NS ? fill - NS : 0; f < fill; ++f) drain(&kv_full[f % NS], (f / NS) & 1);
-            for (int s = w.seg - NQ + 1 < 0 ? 0 : w.seg - NQ + 1; s <= w.seg; ++s) drain(&q_full[s % NQ], (s / NQ) & 1);
+        if (lane == 0 && *deadp) {              // every buffer's last copy, as far as one was issued
+            for (int i = 0; i < NS; ++i) drain(&kv_full[i], i < kv.at ? kv.round : kv.round ^ 1);
+            for (int i = 0; i < NQ; ++i) drain(&q_full[i], i < qr.at ? qr.round : qr.round ^ 1);
+        }
+        if (lane == 0) {                        // what the join kernel has to do here
+            Meta into = {}, from = {};
+            Walk f(p, first, begin, end);
+            if (f.next() && f.c0 > 0) into = f.meta(T, work);
+            if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(T, work);
+            p.meta[2 * blockIdx.x] = into;
+            p.meta[2 * blockIdx.x + 1] = from;
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---------------- MMAs (one thread): S^T one unit ahead of O^T ----------------
         if (lane == 0) {
             Walk ws(p, first, begin, end), wo(p, first, begin, end);
+            Ring<NS> ks, vs;                    // the slots of unit i's K and unit i - 1's V
+            Ring<NQ> qr;
+            Ring<NP> pr;
+            vs.step();
             const uint32_t sa = smem_u32(slots), qa = smem_u32(qs), pa = smem_u32(ps);
             bool ok = true;
             int cs = 0, co = 0;                 // next chunk of ws' and wo's segments
             const int n = end - begin;
             for (int i = 0; i <= n && ok; ++i) {
                 if (i < n) {                    // S^T of unit i
-                    const bool head = i == 0 || cs == ws.c1;
-                    if (head) {
+                    if (i == 0 || cs == ws.c1) {
                         ws.next();
                         cs = ws.c0;
-                        ok = ok && wait(&q_full[ws.seg % NQ], (ws.seg / NQ) & 1, deadp);
+                        ok = ok && wait(&q_full[qr.at], qr.round, deadp);
                     }
-                    const int f = 2 * i, s = f % NS;
-                    ok = ok && wait(&kv_full[s], (f / NS) & 1, deadp);
+                    ok = ok && wait(&kv_full[ks.at], ks.round, deadp);
                     ok = ok && wait(&s_empty[i & 1], ((i >> 1) & 1) ^ 1, deadp);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t id = umma_idesc_bf16(128, (ws.R + 15) & ~15);
-                    const uint64_t dk = desc_sw128(sa + s * L::kSlot, 16, 1024);
-                    const uint64_t dq = desc_sw128(qa + (ws.seg % NQ) * L::kQ, 16, 1024);
+                    const uint64_t dk = desc_sw128(sa + ks.at * L::kSlot, 16, 1024);
+                    const uint64_t dq = desc_sw128(qa + qr.at * L::kQ, 16, 1024);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
                         umma_bf16_id(tmem + (i & 1) * RP, dk + (k >> 2) * (kChunk * 128 >> 4) + (k & 3) * 2,
                                      dq + (k >> 2) * (RP * 128 >> 4) + (k & 3) * 2, id, k > 0);
                     umma_commit(&s_full[i & 1]);
-                    umma_commit(&kv_empty[s]);
-                    if (++cs == ws.c1) umma_commit(&q_empty[ws.seg % NQ]);
+                    umma_commit(&kv_empty[ks.at]);
+                    ks.step();
+                    ks.step();
+                    if (++cs == ws.c1) {
+                        umma_commit(&q_empty[qr.at]);
+                        qr.step();
+                    }
                 }
                 if (i > 0) {                    // O^T of unit i - 1
                     const int j = i - 1;
@@ -403,25 +476,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                         co = wo.c0;
                         ok = ok && wait(&o_empty[wo.seg & 1], ((wo.seg >> 1) & 1) ^ 1, deadp);
                     }
-                    const int f = 2 * j + 1, s = f % NS;
-                    ok = ok && wait(&kv_full[s], (f / NS) & 1, deadp);
-                    ok = ok && wait(&p_full[j % NP], (j / NP) & 1, deadp);
+                    ok = ok && wait(&kv_full[vs.at], vs.round, deadp);
+                    ok = ok && wait(&p_full[pr.at], pr.round, deadp);
                     if (!ok) break;
                     tc_fence_after();
                     // A = V^T and B = P^T, both MN-major
-                    const uint32_t id = umma_idesc_bf16(128, (wo.R + 15) & ~15) | (1u << 15) | (1u << 16);
-                    const uint64_t dv = desc_sw128(sa + s * L::kSlot, HD == 128 ? kChunk * 128 : 1024, 1024);
-                    const uint64_t dp = umma_desc_kmajor(pa + (j % NP) * 2 * L::kP, 128, kChunk * 16);
-                    const uint32_t o = tmem + 2 * RP + (wo.seg & 1) * RP;
+                    const uint32_t id = umma_idesc_bf16(128, kStack ? 2 * RP : (wo.R + 15) & ~15) | (1u << 15) | (1u << 16);
+                    const uint64_t dv = desc_sw128(sa + vs.at * L::kSlot, HD == 128 ? kChunk * 128 : 1024, 1024);
+                    const uint64_t dp = umma_desc_kmajor(pa + pr.at * 2 * L::kP, 128, kChunk * 16);
+                    const int og = kStream ? (wo.seg & 1) * 2 + (j & 1) : wo.seg & 1;
+                    const uint32_t o = tmem + 2 * RP + og * L::kO;
+                    const bool more = co >= wo.c0 + kGroups;   // this O^T holds earlier chunks
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < (kStack ? 1 : 2); ++part)
 #pragma unroll
                         for (int k = 0; k < kChunk / 16; ++k)
                             umma_bf16_id(o, dv + k * (2048 >> 4), dp + part * (L::kP >> 4) + k * (256 >> 4), id,
-                                         co != wo.c0 || (part | k) != 0);
-                    umma_commit(&kv_empty[s]);
-                    umma_commit(&p_empty[j % NP]);
+                                         more || (part | k) != 0);
+                    umma_commit(&kv_empty[vs.at]);
+                    umma_commit(&p_empty[pr.at]);
                     if (++co == wo.c1) umma_commit(&o_full[wo.seg & 1]);
+                    vs.step();
+                    vs.step();
+                    pr.step();
                 }
             }
             if (!ok) {
@@ -433,108 +510,143 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     } else {
         // ---------------- softmax and results: thread = key, then head dimension ----------------
         const int wg = warp >> 2, qd = warp & 3;
-        const uint32_t lanes = (uint32_t)(qd * 32) << 16;
+        const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         const int key = qd * 32 + lane;
-        const int col0 = wg * CW;               // the warpgroup's first row
-        const int bar = 1 + wg;
+        const int col0 = kStream ? 0 : wg * NC; // the thread's first row
+        const int gi = kStream ? wg : 0;        // its reference and O^T
+        const int bar = kSoftBar + wg;
+        const F2 k2(p.scale_log2, p.scale_log2);
         Walk w(p, first, begin, end);
-        int i = 0;                              // unit
+        int base_i = 0;                         // the segment's first unit
+        Ring<NS> vs;                            // slot of the next unit's V
+        vs.step();
         bool ok = true;
         while (w.next()) {
-            const int last0 = w.last0(), last_max = last0 + tok[w.R - 1];
-            const bool idle = w.R <= col0;
-            float l[CW];
+            const int par = w.seg & 1, units = w.c1 - w.c0;
+            const int last0 = w.last0(), rows = w.R - col0;   // live rows of this thread
+            float* const mine = nref[par][gi];
+            F2 l[NC / 2];
 #pragma unroll
-            for (int j = 0; j < CW; ++j) l[j] = 0.f;
-            if (tid == 0) poison[w.seg & 1] = 0;
-            for (int c = w.c0; c < w.c1; ++c, ++i) {
+            for (int j = 0; j < NC / 2; ++j) l[j] = F2(0.f, 0.f);
+            bool fresh = true;
+            for (int c = w.c0; c < w.c1; ++c) {
+                const int i = base_i + c - w.c0;
+                const Ring<NS> v = vs;
+                vs.step();
+                vs.step();
+                if (kStream && (i & 1) != wg) continue;
+                const uint32_t st = lanes + (i & 1) * RP + col0;
                 const int kp = c * kChunk + key;
+                const bool masked = (c + 1) * kChunk - 1 > last0;   // some row does not see all of the chunk
                 ok = ok && wait(&s_full[i & 1], (i >> 1) & 1, deadp);
                 tc_fence_after();
-                float s[CW];
-                if (!idle) {
+                float s[NC];
+                auto scores = [&]() {           // the chunk's scores, -inf where a row does not see the key
 #pragma unroll
-                    for (int j = 0; j < CW; j += 8) tmem_ld<8>(tmem + lanes + (i & 1) * RP + col0 + j, s + j);
+                    for (int j = 0; j < NC; j += 8)
+                        if (j < rows) tmem_ld8_async(st + j, s + j);
                     tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < NC; ++j)
+                            if (j < rows && kp > last0 + tok[col0 + j]) s[j] = -INFINITY;
+                    }
+                };
+                scores();
+                if (fresh && rows > 0) {        // references: the scores of the chunk's first key
+                    if (key == 0) {
+#pragma unroll
+                        for (int j = 0; j < NC; ++j) {
+                            const float m = s[j] * p.scale_log2;
+                            mine[col0 + j] = j >= rows ? -INFINITY : m > kNone ? -m : -kNone;   // rows past R weigh nothing
+                        }
+                    }
+                    named_bar_sync(bar, 128);
+                }
+                float top = kNone;
+                auto exponents = [&]() {
+#pragma unroll
+                    for (int j = 0; j < NC; j += 4)
+                        if ((j & ~7) < rows) {
+                            const float4 m = *reinterpret_cast<const float4*>(&mine[col0 + j]);
+                            fma2(F2(s[j], s[j + 1]), k2, F2(m.x, m.y)).get(s[j], s[j + 1]);
+                            fma2(F2(s[j + 2], s[j + 3]), k2, F2(m.z, m.w)).get(s[j + 2], s[j + 3]);
+                            top = fmaxf(top, fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
+                        }
+                };
+                exponents();
+                // this thread's P^T buffer is free (and its rows' O^T complete) once their last product is
+                auto product_done = [&]() {
+                    ok = ok && wait(&p_empty[kStream ? i & 1 : 0], ((kStream ? i >> 1 : i) & 1) ^ 1, deadp);
+                };
+                if (rows > 0 && bar_any(bar, 128, top > kLimit)) {
+                    // the references move up to the chunk's maxima
+                    product_done();
+                    tc_fence_after();
+                    scores();
+                    float (*const mx)[RP] = xl[par][gi];
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+                        if (j < rows) {
+                            const float m = warp_max_exact(s[j]);
+                            if (lane == 0) mx[qd][col0 + j] = m;
+                        }
+                    named_bar_sync(bar, 128);
+                    auto moved = [&](int r) {   // a row's new reference
+                        const float m = fmaxf(fmaxf(mx[0][r], mx[1][r]), fmaxf(mx[2][r], mx[3][r])) * p.scale_log2;
+                        return fmaxf(-mine[r], m);
+                    };
+                    const int og = kStream ? par * 2 + wg : par;
+#pragma unroll
+                    for (int j = 0; j < NC; j += 8)
+                        if (j < rows) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int r = col0 + j + e;
+                                f[e] = j + e < rows ? ex2_approx(-mine[r] - moved(r)) : 0.f;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                float a, b;
+                                l[(j + e) / 2].get(a, b);
+                                l[(j + e) / 2] = F2(a * f[e], b * f[e + 1]);
+                            }
+                            if (!fresh) {
+#pragma unroll
+                                for (int part = 0; part < (kStack ? 2 : 1); ++part) {
+                                    const uint32_t at = lanes + 2 * RP + og * L::kO + part * RP + col0 + j;
+                                    float o[8];
+                                    tmem_ld8_async(at, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) o[e] *= f[e];
+                                    tmem_st8(at, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                    named_bar_sync(bar, 128);   // everyone has read the old references
+                    if (key < rows && key < NC) mine[col0 + key] = -moved(col0 + key);
+                    named_bar_sync(bar, 128);
+                    exponents();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[i & 1]);
-                const bool masked = (c + 1) * kChunk - 1 > last0;   // some row does not see all of the chunk
-                if (!idle) {
-                    if (masked) {
+                fresh = false;
 #pragma unroll
-                        for (int j = 0; j < CW; ++j)
-                            if (kp > last0 + tok[col0 + j]) s[j] = -INFINITY;
+                for (int j = 0; j < NC; j += 2)
+                    if ((j & ~7) < rows) {
+                        s[j] = ex2_approx(s[j]);
+                        s[j + 1] = ex2_approx(s[j + 1]);
+                        l[j / 2] = add2(l[j / 2], F2(s[j], s[j + 1]));
                     }
-                    float top = kNone;
-                    if (c != w.c0) {
+                product_done();
+                uint8_t* ph = ps + (kStream ? i & 1 : 0) * 2 * L::kP + (col0 >> 3) * (kChunk * 16) + key * 16;
 #pragma unroll
-                        for (int j = 0; j < CW; j += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(&mref[col0 + j]);
-                            top = fmaxf(top, fmaxf(fmaxf(fmaf(s[j], p.scale_log2, -m.x), fmaf(s[j + 1], p.scale_log2, -m.y)),
-                                                   fmaxf(fmaf(s[j + 2], p.scale_log2, -m.z), fmaf(s[j + 3], p.scale_log2, -m.w))));
-                        }
-                    }
-                    if (bar_any(bar, 128, c == w.c0 || top > kLimit)) {
-                        // new references: the chunk's row maxima over the four quadrants
-#pragma unroll
-                        for (int j = 0; j < CW; ++j) {
-                            const float m = warp_max_exact(s[j]);
-                            if (lane == 0) xred[qd][col0 + j] = m;
-                        }
-                        named_bar_sync(bar, 128);
-                        if (c != w.c0) {        // O^T holds the chunks before: rescale it with the sums
-                            ok = ok && wait(&p_empty[(i - 1) % NP], ((i - 1) / NP) & 1, deadp);
-                            tc_fence_after();
-                        }
-#pragma unroll
-                        for (int j = 0; j < CW; j += 8) {
-                            float o[8] = {};
-                            const uint32_t at = tmem + lanes + 2 * RP + (w.seg & 1) * RP + col0 + j;
-                            if (c != w.c0) {
-                                tmem_ld<8>(at, o);
-                                tmem_wait_ld();
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int r = col0 + j + e;
-                                const float m = fmaxf(fmaxf(xred[0][r], xred[1][r]), fmaxf(xred[2][r], xred[3][r])) * p.scale_log2;
-                                const float old = c != w.c0 ? mref[r] : kNone;
-                                const float f = ex2_approx(old - fmaxf(old, m));
-                                l[j + e] *= f;
-                                o[e] *= f;
-                            }
-                            if (c != w.c0) tmem_st8(at, o);
-                        }
-                        if (c != w.c0) {
-                            tmem_wait_st();
-                            tc_fence_before();
-                        }
-                        named_bar_sync(bar, 128);   // everyone has read the old references
-                        for (int r = col0 + key; r < col0 + CW; r += 128) {
-                            const float m = fmaxf(fmaxf(xred[0][r], xred[1][r]), fmaxf(xred[2][r], xred[3][r])) * p.scale_log2;
-                            const float old = c != w.c0 ? mref[r] : kNone;
-                            mref[r] = r >= w.R ? INFINITY : fmaxf(old, m);   // rows past R weigh nothing
-                        }
-                        named_bar_sync(bar, 128);
-                    }
-#pragma unroll
-                    for (int j = 0; j < CW; j += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&mref[col0 + j]);
-                        s[j] = ex2_approx(fmaf(s[j], p.scale_log2, -m.x));
-                        s[j + 1] = ex2_approx(fmaf(s[j + 1], p.scale_log2, -m.y));
-                        s[j + 2] = ex2_approx(fmaf(s[j + 2], p.scale_log2, -m.z));
-                        s[j + 3] = ex2_approx(fmaf(s[j + 3], p.scale_log2, -m.w));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) l[j + e] += s[j + e];
-                    }
-                }
-                if (i >= NP) ok = ok && wait(&p_empty[i % NP], ((i / NP) & 1) ^ 1, deadp);
-                if (!idle) {
-                    uint8_t* ph = ps + (i % NP) * 2 * L::kP + key * 16;
-#pragma unroll
-                    for (int j = 0; j < CW; j += 8) {
+                for (int j = 0; j < NC; j += 8)
+                    if (j < rows) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -542,23 +654,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             hi[e] = cvt_bf16x2(a, b);
                             lo[e] = cvt_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xFFFF0000u));
                         }
-                        uint8_t* dst = ph + ((col0 + j) >> 3) * (kChunk * 16);
+                        uint8_t* dst = ph + (j >> 3) * (kChunk * 16);
                         *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(dst + L::kP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                }
-                if (masked && wg == 0) {
+                if (masked && (kStream || wg == 0)) {
                     // Values of positions that some row does not see: behind the
                     // length they become zero (a weight of zero does not silence a
                     // NaN), between the rows' last positions non-finite ones do,
                     // and are added at the end to the rows that see them.
-                    const int f = 2 * i + 1, sl = f % NS;
-                    ok = ok && wait(&kv_full[sl], (f / NS) & 1, deadp);
-                    uint8_t* v = slots + sl * L::kSlot;
+                    ok = ok && wait(&kv_full[v.at], v.round, deadp);
+                    uint8_t* vt = slots + v.at * L::kSlot;
                     const int from = max(0, last0 + 1 - c * kChunk), live = w.len - c * kChunk;
                     for (int t = from * (HD / 8) + key; t < kChunk * (HD / 8); t += 128) {
                         const int r = t / (HD / 8), d8 = t % (HD / 8);
-                        uint4* at = reinterpret_cast<uint4*>(v + (d8 >> 3) * kChunk * 128 + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
+                        uint4* at = reinterpret_cast<uint4*>(vt + (d8 >> 3) * kChunk * 128 + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
                         if (r >= live) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
                         } else {
@@ -572,65 +682,125 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             }
                             if (hit) {
                                 *at = x;
-                                poison[w.seg & 1] = 1;
+                                poison[par] = w.seg + 1;
                             }
                         }
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[i % NP]);
+                if (lane == 0) mbar_arrive(&p_full[kStream ? i & 1 : 0]);
             }
             // ---- the segment's rows ----
-            const bool whole = w.whole();
-            const int slot = 2 * blockIdx.x + (w.u - (w.c1 - w.c0) == begin ? 0 : 1);
-            if (!idle) {
+            const int ga = kStream ? base_i & 1 : 0;    // the warpgroup of the first unit; the other has none in a segment of one
+            const bool two = kStream && units > 1;
+            base_i += units;
+            // sums over the warp's keys, 8 rows at a time: halves are exchanged until
+            // lane r of each 8 holds row r, then those lanes are added
 #pragma unroll
-                for (int j = 0; j < CW; ++j) {
-                    float x = l[j];
+            for (int j = 0; j < NC; j += 8)
+                if (j < rows) {
+                    float x[8];
 #pragma unroll
-                    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                    if (lane == 0) xred[qd][col0 + j] = x;
+                    for (int e = 0; e < 4; ++e) l[j / 2 + e].get(x[2 * e], x[2 * e + 1]);
+#pragma unroll
+                    for (int h = 4; h >= 1; h >>= 1) {
+                        const bool up = lane & h;
+#pragma unroll
+                        for (int e = 0; e < h; ++e) {
+                            const float give = up ? x[e] : x[e + h], keep = up ? x[e + h] : x[e];
+                            x[e] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+                        }
+                    }
+                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 8);
+                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
+                    if (lane < 8) xl[par][gi][qd][col0 + j + lane] = x[0];
                 }
-                named_bar_sync(bar, 128);
+            if (kStream) named_bar_sync(kBothBar, 256);
+            else named_bar_sync(bar, 128);
+            const bool whole = w.whole();
+            const int slot = 2 * blockIdx.x + (w.u - units == begin ? 0 : 1);
+            // the rows this warpgroup writes: every other 8 (of the halves: its own)
+            auto writes = [&](int r) { return r < w.R && (kStream ? ((r >> 3) & 1) == wg : (r >= col0 && r < col0 + NC)); };
+            if (key < RP && writes(key)) {
+                const int r = key;
+                float ma = -nref[par][ga][r], la = xl[par][ga][0][r] + xl[par][ga][1][r] + xl[par][ga][2][r] + xl[par][ga][3][r];
+                float fa = 1.f, fb = 0.f;
+                if (two) {
+                    const int gb = ga ^ (kGroups - 1);
+                    const float mb = -nref[par][gb][r];
+                    const float lb = xl[par][gb][0][r] + xl[par][gb][1][r] + xl[par][gb][2][r] + xl[par][gb][3][r];
+                    const float m = fmaxf(ma, mb);
+                    fa = ex2_approx(ma - m);
+                    fb = ex2_approx(mb - m);
+                    la = la * fa + lb * fb;
+                    ma = m;
+                }
+                if (whole) {
+                    const float inv = 1.f / la;
+                    fa *= inv;
+                    fb *= inv;
+                } else {
+                    p.part_ml[(size_t)slot * RP + r] = make_float2(ma, la);
+                }
+                weight[par][r] = make_float2(fa, fb);
             }
-            ok = ok && wait(&o_full[w.seg & 1], (w.seg >> 1) & 1, deadp);
-            tc_fence_after();
-            if (!idle) {
+            named_bar_sync(bar, 128);
+            if (kStream ? w.R > 8 * wg : rows > 0) {
+                ok = ok && wait(&o_full[par], (w.seg >> 1) & 1, deadp);
+                tc_fence_after();
                 const int d = key;
-                const bool bad = poison[w.seg & 1] != 0;
-                uint16_t* out = p.out + (long long)(w.row_base + w.block * p.tokens) * p.out_stride +
-                                (long long)w.head * p.group * HD + d;
-                if (!whole)
-                    for (int r = col0 + key; r < min(w.R, col0 + CW); r += 128)
-                        p.part_ml[(size_t)slot * RP + r] =
-                            make_float2(mref[r], xred[0][r] + xred[1][r] + xred[2][r] + xred[3][r]);
+                const bool bad = poison[par] == w.seg + 1;
+                const long long out0 = (long long)(w.row_base + w.block * p.tokens) * p.out_stride +
+                                       (long long)w.head * p.group * HD + d;
 #pragma unroll 1
-                for (int j = 0; j < CW && col0 + j < w.R; j += 8) {
-                    float o[8];
-                    tmem_ld<8>(tmem + lanes + 2 * RP + (w.seg & 1) * RP + col0 + j, o);
-                    tmem_wait_ld();
+                for (int j = kStream ? 8 * wg : col0; j < (kStream ? RP : col0 + NC) && j < w.R; j += kStream ? 16 : 8) {
+                    float o[8], x[8];
+                    const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j;
+                    tmem_ld8_async(at, o);
+                    if (kStack) {
+                        tmem_ld8_async(at + RP, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] += x[e];
+                    } else {
+                        tmem_wait_ld();
+                    }
+                    float2 f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = weight[par][j + e];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] *= f[e].x;
+                    if (two) {
+                        const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j;
+                        tmem_ld8_async(bt, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
+                        if (kStack) {
+                            tmem_ld8_async(bt + RP, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
+                        }
+                    }
                     if (d < HD) {
                         if (bad)
-                            for (int t = max(last0 + 1, w.c0 * kChunk); t <= min(last_max, w.c1 * kChunk - 1); ++t) {
+                            for (int t = max(last0 + 1, w.c0 * kChunk); t < min(w.len, w.c1 * kChunk); ++t) {
                                 const int page = p.tables[(size_t)w.q * p.table_pages + t / SPEC_PAGE];
                                 if (page < 0 || page >= p.num_pages) continue;
                                 const float v = bf2f(p.vpool[(((size_t)page * p.hkv + w.head) * SPEC_PAGE + t % SPEC_PAGE) * HD + d]);
                                 if (!isfinite(v))
 #pragma unroll
                                     for (int e = 0; e < 8; ++e)
-                                        if (t <= last0 + tok[col0 + j + e]) o[e] += v;
+                                        if (t <= last0 + tok[j + e]) o[e] += v;
                             }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int r = col0 + j + e;
+                            const int r = j + e;
                             if (r < w.R) {
-                                if (whole) {
-                                    const float sum = xred[0][r] + xred[1][r] + xred[2][r] + xred[3][r];
-                                    out[col_off[r]] = f2bf(last0 + tok[r] >= 0 ? o[e] / sum : 0.f);
-                                } else {
-                                    p.part_o[((size_t)slot * RP + r) * HD + d] = o[e];
-                                }
+                                if (whole) p.out[out0 + col_off[r]] = f2bf(last0 + tok[r] >= 0 ? o[e] : 0.f);
+                                else p.part_o[((size_t)slot * RP + r) * HD + d] = o[e];
                             }
                         }
                     }
@@ -638,23 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[w.seg & 1]);
-        }
-        // what the join kernel has to do for the pair that begins here and goes on
-        if (tid == 0) {
-            Meta m = {};
-            if (w.seg >= 0 && w.c1 < w.chunks) {
-                const int pair_begin = w.u - w.c1;           // unit of the pair's chunk 0
-                if (pair_begin >= begin) {
-                    m.count = split::contributors(blockIdx.x, pair_begin + w.chunks, T, work);
-                    m.slot = 2 * blockIdx.x + (pair_begin == begin ? 0 : 1);
-                    m.rows = w.R;
-                    m.head = w.head * p.group;
-                    m.row0 = w.row_base + w.block * p.tokens;
-                    m.last0 = w.last0();
-                }
-            }
-            p.meta[blockIdx.x] = m;
+            if (lane == 0) mbar_arrive(&o_empty[par]);
         }
     }
     tc_fence_before();
@@ -666,36 +820,117 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
 }
 
-// Joins the partials of each pair that CTAs shared: CTA (c, y) takes rows 8y,
-// 8y + 8 gridDim.y, .. of the pair that begins in CTA c, one warp a row.
+// Joins the partials of each pair that CTAs shared.  The pair's CTAs deal its
+// rows among themselves (CTA t of n takes rows t, t + n, ..): the more partials
+// a row has, the more CTAs read them.  Up to 8 partials a warp joins a row, its
+// loads all in flight at once; above, the CTA's 8 warps share the row's partials.
+constexpr int kJoinFew = 8, kJoinWarps = 8;
+
 template <int HD>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int rp) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedParams p, int rp) {
+    constexpr int V = HD / 32;
+    __shared__ float so[kJoinWarps][HD];
+    __shared__ float ssum[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    const Meta m = p.meta[blockIdx.x];
-    const int lane = threadIdx.x & 31;
-    constexpr int V = HD / 32;
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < m.rows && m.count > 0; r += gridDim.y * 8) {
+    const Meta metas[2] = {p.meta[2 * blockIdx.x], p.meta[2 * blockIdx.x + 1]};
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const Meta m = metas[k];
+        if (m.count == 0) continue;
+        const int mine = blockIdx.x - m.owner;
         // partial t of the pair: the owner's slot, then the first slots of the CTAs after it
-        auto at = [&](int t) { return (size_t)(t ? 2 * (blockIdx.x + t) : m.slot) * rp + r; };
-        float M = kNone;
-        for (int t = lane; t < m.count; t += 32) M = fmaxf(M, p.part_ml[at(t)].x);
+        auto at = [&](int r, int t) { return (size_t)(t ? 2 * (m.owner + t) : m.slot) * rp + r; };
+        auto store = [&](int r, const float* o, float sum) {
+            const int t = r / p.group;
+            const bool any = m.last0 + t >= 0;
+            uint16_t* out = p.out + (long long)(m.row0 + t) * p.out_stride + (long long)(m.head + r - t * p.group) * HD + lane * V;
+            const float inv = any ? 1.f / sum : 0.f;
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2*>(out) = any ? make_uint2(cvt_bf16x2(o[0] * inv, o[1] * inv), cvt_bf16x2(o[2] * inv, o[3] * inv))
+                                                     : make_uint2(0u, 0u);
+            else
+                *reinterpret_cast<uint32_t*>(out) = any ? cvt_bf16x2(o[0] * inv, o[1] * inv) : 0u;
+        };
+        auto load = [&](size_t i, float* v) {
+            if constexpr (V == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(p.part_o + i * HD + lane * 4);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(p.part_o + i * HD + lane * 2);
+                v[0] = x.x, v[1] = x.y;
+            }
+        };
+        if (m.count <= kJoinFew) {
+            for (int r = mine + m.count * (warp + kJoinWarps * blockIdx.y); r < m.rows; r += m.count * kJoinWarps * gridDim.y) {
+                float v[kJoinFew][V];
+                float2 ml[kJoinFew];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        float sum = 0.f, o[V] = {};
-#pragma unroll 8
-        for (int t = 0; t < m.count; ++t) {
-            const float2 ml = p.part_ml[at(t)];
-            const float* src = p.part_o + at(t) * HD + lane * V;
-            const float f = ex2_approx(ml.x - M);
-            sum += f * ml.y;
+                for (int t = 0; t < kJoinFew; ++t)
+                    if (t < m.count) {
+                        ml[t] = p.part_ml[at(r, t)];
+                        load(at(r, t), v[t]);
+                    }
+                float M = kNone, sum = 0.f, o[V] = {};
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] += f * src[e];
+                for (int t = 0; t < kJoinFew; ++t)
+                    if (t < m.count) M = fmaxf(M, ml[t].x);
+#pragma unroll
+                for (int t = 0; t < kJoinFew; ++t)
+                    if (t < m.count) {
+                        const float f = ex2_approx(ml[t].x - M);
+                        sum += f * ml[t].y;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) o[e] += f * v[t][e];
+                    }
+                store(r, o, sum);
+            }
+        } else {
+            for (int r = mine + m.count * blockIdx.y; r < m.rows; r += m.count * gridDim.y) {
+                float M = kNone, sum = 0.f, o[V] = {};
+                for (int t = lane; t < m.count; t += 32) M = fmaxf(M, p.part_ml[at(r, t)].x);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                for (int t0 = warp; t0 < m.count; t0 += 4 * kJoinWarps) {
+                    float v[4][V];
+                    float2 ml[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = t0 + i * kJoinWarps;
+                        if (t < m.count) {
+                            ml[i] = p.part_ml[at(r, t)];
+                            load(at(r, t), v[i]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t0 + i * kJoinWarps < m.count) {
+                            const float f = ex2_approx(ml[i].x - M);
+                            sum += f * ml[i].y;
+#pragma unroll
+                            for (int e = 0; e < V; ++e) o[e] += f * v[i][e];
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
+                if (lane == 0) ssum[warp] = sum;
+                __syncthreads();
+                if (warp == 0) {
+                    sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kJoinWarps; ++w) {
+                        sum += ssum[w];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) o[e] += so[w][lane * V + e];
+                    }
+                    store(r, o, sum);
+                }
+                __syncthreads();
+            }
         }
-        const int t = r / p.group;
-        uint16_t* out = p.out + (long long)(m.row0 + t) * p.out_stride + (long long)(m.head + r - t * p.group) * HD + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) out[e] = f2bf(m.last0 + t >= 0 ? o[e] / sum : 0.f);
     }
 }
 
@@ -721,14 +956,14 @@ const char* head_error(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, in
     return nullptr;
 }
 
-// Workspace: partial outputs, (reference, sum) pairs, one Meta per CTA.
+// Workspace: partial outputs, (reference, sum) pairs, two Metas per CTA.
 struct Work {
     size_t o, ml, meta, bytes;
     Work(int ctas, int rp, int hd) {
         o = 0;
         ml = (size_t)2 * ctas * rp * hd * 4;
         meta = ml + (size_t)2 * ctas * rp * 8;
-        bytes = (meta + (size_t)ctas * sizeof(Meta) + 255) & ~(size_t)255;
+        bytes = (meta + (size_t)2 * ctas * sizeof(Meta) + 255) & ~(size_t)255;
     }
 };
 
@@ -788,7 +1023,7 @@ cudaError_t run(PagedParams& p, int ctas, cudaStream_t s) {
     if ((e = launch(fn, dim3((unsigned)ctas), kThreads, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess) return e;
     int rp = RP;
     void* jargs[] = {&p, &rp};
-    return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, RP / 16), 256, 0, s, jargs);
+    return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, RP <= 32 ? 1 : RP / 32), 32 * kJoinWarps, 0, s, jargs);
 }
 
 }  // namespace

@@ -44,6 +44,9 @@ SPLIT_HD int64_t units_of(int rows, int len, int tokens, int hkv) {
 SPLIT_HD int working(int ctas, int total) { return total < ctas ? total : ctas; }
 SPLIT_HD int begin_of(int c, int total, int work) { return c < work ? (int)((int64_t)total * c / work) : total; }
 
+// The CTA that works on unit u: the last c with begin_of(c) <= u.
+SPLIT_HD int cta_of(int u, int total, int work) { return (int)((((int64_t)u + 1) * work - 1) / total); }
+
 // The sequence that holds unit u < first[nseq]: the last q with first[q] <= u.
 SPLIT_HD int sequence_of(const int* first, int nseq, int u) {
     int lo = 0, hi = nseq;
@@ -56,11 +59,7 @@ SPLIT_HD int sequence_of(const int* first, int nseq, int u) {
 }
 
 // Number of partials of a pair whose units end at pair_end (exclusive), owner c included.
-SPLIT_HD int contributors(int c, int pair_end, int total, int work) {
-    int k = 1;
-    while (c + k < work && begin_of(c + k, total, work) < pair_end) ++k;
-    return k;
-}
+SPLIT_HD int contributors(int c, int pair_end, int total, int work) { return cta_of(pair_end - 1, total, work) - c + 1; }
 
 // Tile height (rows per kv head) for blocks of max_new tokens of G query
 // heads: the smallest of 16, 32, 64, 128 that holds a whole block, else 128.

@@ -19,6 +19,7 @@ int blocks(int rows, int tokens) { return blocks_of(rows, tokens); }
 long long units(int rows, int len, int tokens, int hkv) { return units_of(rows, len, tokens, hkv); }
 int work(int ctas, int total) { return working(ctas, total); }
 int begin(int c, int total, int w) { return begin_of(c, total, w); }
+int cta(int u, int total, int w) { return cta_of(u, total, w); }
 int sequence(const int* first, int nseq, int u) { return sequence_of(first, nseq, u); }
 int parts(int c, int pair_end, int total, int w) { return contributors(c, pair_end, total, w); }
 int tile(int group, int max_new) { return tile_rows(group, max_new); }
@@ -81,6 +82,7 @@ def test_segments_partition_the_units_and_partials_meet_their_owner(split, case)
             q = split.sequence(arr, len(lens), u)
             assert first[q] <= u < first[q + 1]
             i = pair_of[u]
+            assert split.cta(u, T, w) == c and split.cta(pairs[i][0], T, w) <= c
             e = min(b, pairs[i][1])
             if (u, e) == pairs[i]:
                 whole.add(i)
