@@ -22,14 +22,16 @@
 // partial sum and the two roundings; nothing crosses lanes until the segment
 // ends.
 //
-// Roles: warps 0-7 softmax (thread = key, then head dimension), warp 8 issues
-// the MMAs, warp 9 the TMA copies.  Up to 64 rows the two warpgroups take
-// alternate chunks, each with its own reference, sum and O^T (joined when the
-// segment ends): a warp's chain of dependent instructions is what a chunk of few
-// rows costs, and two chains run side by side.  128 rows are halved between the
-// warpgroups instead (shared memory has no room for two P^T).  One CTA per SM,
-// each with the same number of chunks (paged_split.h); a second kernel joins
-// the pairs that were split between CTAs.
+// Roles, by warpgroup: 0 and 1 softmax (thread = key); 2 one warp each for the
+// MMAs of S^T, the MMAs of O^T, the TMA copies and the list of segments; 3 results
+// (thread = head dimension).  Up to 64 rows the two softmax warpgroups take
+// alternate chunks, each with its own reference, sum and O^T (joined with the
+// results): a warp's chain of dependent instructions is what a chunk of few rows
+// costs, and two chains run side by side.  128 rows are halved between the
+// warpgroups instead (shared memory has no room for two P^T).  O^T and the sums
+// are double buffered by segment, so that a segment's results are written while
+// the next one runs.  One CTA per SM, each with the same number of chunks
+// (paged_split.h); a second kernel joins the pairs that were split between CTAs.
 #include <cuda.h>
 #include <math.h>
 
@@ -42,12 +44,27 @@ namespace {
 
 using split::kChunk;
 
-constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadWarp = 10, kListWarp = 11, kResultWarp = 12, kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+// registers of a thread, by role: 128 each at launch, moved to where S^T and P^T live
+constexpr int kSoftRegs = 184, kIssueRegs = 64, kResultRegs = 80;
+static_assert(2 * kSoftRegs + kIssueRegs + kResultRegs <= 4 * 128, "more registers than the block was launched with");
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -1e30f;         // reference of a row that has seen no key
-constexpr int kSoftBar = 1, kBothBar = 3;   // named barriers: one per warpgroup, one for both
+constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
+constexpr int kSegs = 4;                    // segments listed ahead
+
+// A segment, as the roles need it.
+struct Seg {
+    int c0, units;              // first chunk, number of chunks
+    int R;                      // rows
+    int last0;                  // last position that the first token sees
+    int len;                    // of the sequence
+    int q, head;                // sequence, kv head
+    int row0;                   // first row of the call
+    int slot;                   // where its partial goes; -1: it covers its pair
+    int pad[3];
+};
 
 // A split pair, as the join kernel sees it from one of its CTAs.
 struct Meta {
@@ -76,8 +93,9 @@ struct PagedParams {
     Meta* meta;                 // [ctas][2]: the pair that goes on into the CTA, the pair that begins in it and goes on
 };
 
-// Shared-memory plan: NQ query tiles, NP pairs of P^T parts, NS slots that
-// alternately take a chunk's K and V.
+// Shared-memory plan: NQ query tiles, NP pairs of P^T parts, NK slots for a
+// chunk's K and NV for its V.  K and V do not share slots: different threads wait
+// for them, and a barrier's parity is only sound for one that sees every phase.
 template <int HD, int RP>
 struct Plan {
     static constexpr bool kStream = RP <= 64;               // warpgroups take alternate chunks
@@ -88,13 +106,14 @@ struct Plan {
     static constexpr int NQ = RP <= 32 ? 2 : 1;
     static constexpr int NP = kStream ? 2 : 1;
     static constexpr int kFixed = NQ * kQ + NP * 2 * kP + 2048;   // alignment, pad after the last slot
-    static constexpr int kMost = 227 * 1024 - (6144 + 64 * RP) - kFixed; // less the static arrays
+    static constexpr int kMost = 227 * 1024 - (6656 + 64 * RP) - kFixed; // less the static arrays
     static constexpr int NS = kMost / kSlot < 8 ? kMost / kSlot : 8;
+    static constexpr int NK = NS / 2, NV = NS - NK;
     static constexpr int kBytes = kFixed + NS * kSlot;
     static constexpr int kO = kStack ? 2 * RP : RP;         // tensor-memory columns of one O^T
     static constexpr int kUsed = 2 * RP + (kStream ? 4 : 2) * kO;   // S^T x 2, O^T x 2 (per warpgroup)
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
-    static_assert(NS >= 3 && kUsed <= 512, "a chunk's K and the previous chunk's V are live together");
+    static_assert(NK >= 1 && NV >= 2 && kUsed <= 512, "one K, and V of this chunk and the one before");
 };
 
 __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -113,7 +132,7 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
            (2ull << 61);
 }
 
-// 8 consecutive fp32 columns of this warp's 32 lanes.
+// 8, 16 or 32 consecutive fp32 columns of this warp's 32 lanes, not waited for.
 __device__ __forceinline__ void tmem_ld8_async(uint32_t t, float* v) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -122,6 +141,31 @@ __device__ __forceinline__ void tmem_ld8_async(uint32_t t, float* v) {
                  : "memory");
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld16_async(uint32_t t, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld32_async(uint32_t t, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st8(uint32_t t, const float* v) {
@@ -169,18 +213,26 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool any) {
     return r != 0;
 }
 
-// Bounded wait; a wait that gives up raises `dead`, which ends every later one.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
+// True in one lane of a converged warp, always the same one.  Issuing MMAs and
+// copies under this predicate (and not under lane == 0) tells the compiler that
+// one thread issues them; otherwise every issue pays for finding that out.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Wait bounded in time (2^31 cycles, about a second); one that gives up raises
+// `dead`, which ends every later one.  Inline: a call would fix the registers
+// that setmaxnreg moves.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    do {
         if (mbar_try_wait(bar, parity)) return true;
-        if (i > 256) __nanosleep(i < 4096 ? 32 : 256);
-        if ((i & 255) == 255 && *dead) return false;
-    }
+    } while (!*dead && clock64() - t0 < (1ll << 31));
     *dead = 1;
     return false;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, dead);
 }
 // After a failed wait: let what is in flight finish before the CTA ends.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
@@ -197,7 +249,7 @@ struct Ring {
     }
 };
 
-// A CTA's segments in order; every role walks its own copy.
+// A CTA's segments in order.
 struct Walk {
     const PagedParams& p;
     const int* first;           // [nseq + 1] in shared memory
@@ -232,13 +284,13 @@ struct Walk {
     __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
     // last position that the block's first token sees
     __device__ __forceinline__ int last0() const { return len - rows + block * p.tokens; }
-    // the segment's pair, for the join; T units on `work` CTAs
-    __device__ Meta meta(int T, int work) const {
-        const int pair_begin = u - c1, owner = split::cta_of(pair_begin, T, work);
+    // the segment's pair, for the join
+    __device__ Meta meta(const split::Deal& deal) const {
+        const int pair_begin = u - c1, owner = deal.cta(pair_begin);
         Meta m;
-        m.count = split::contributors(owner, pair_begin + chunks, T, work);
+        m.count = deal.parts(owner, pair_begin + chunks);
         m.owner = owner;
-        m.slot = 2 * owner + (pair_begin == split::begin_of(owner, T, work) ? 0 : 1);
+        m.slot = 2 * owner + (pair_begin == deal.begin(owner) ? 0 : 1);
         m.rows = R;
         m.head = head * p.group;
         m.row0 = row_base + block * p.tokens;
@@ -248,22 +300,32 @@ struct Walk {
     }
 };
 
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 template <int HD, int RP>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p) {
     using L = Plan<HD, RP>;
     constexpr bool kStream = L::kStream, kStack = L::kStack;
-    constexpr int NS = L::NS, NP = L::NP, NQ = L::NQ;
+    constexpr int NK = L::NK, NV = L::NV, NP = L::NP, NQ = L::NQ;
     constexpr int NC = kStream ? RP : RP / 2;   // rows of a softmax thread
+    // rows that a softmax thread handles or skips together: more make longer runs of
+    // independent instructions, fewer waste less on tiles that are not full
+    constexpr int kSpan = NC <= 16 ? 8 : NC <= 32 ? 16 : 32;
     constexpr int kGroups = kStream ? 2 : 1;    // O^T's (and references) of a segment
     constexpr int kArrive = kStream ? 4 : 8;    // warps that read an S^T and write a P^T
+    constexpr int kReaders = kSoftWarps + 3 + 4;    // warps that read the list of segments
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[NQ], q_empty[NQ], s_full[2], s_empty[2], p_full[NP], p_empty[NP],
-        o_full[2], o_empty[2], fin;
+    __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[NQ], q_empty[NQ], s_full[2], s_empty[2], p_full[NP], p_empty[NP],
+        o_full[2], o_empty[2], l_full[2], l_empty[2], seg_full[kSegs], seg_empty[kSegs], fin[2];
     __shared__ uint32_t tmem_base;
     __shared__ int dead, total;
     __shared__ int poison[2];                           // 1 + the last segment (by parity) that silenced a value
     __shared__ int first[split::kMaxSeqs + 1];
-    __shared__ long long warp_sum[kThreads / 32];
+    __shared__ long long warp_sum[kWarps];
+    __shared__ __align__(16) Seg segs[kSegs];
     __shared__ __align__(16) float nref[2][kGroups][RP];    // by segment parity: minus each row's reference
     __shared__ __align__(16) float xl[2][kGroups][4][RP];   // per lane quadrant: sums (and, while a reference moves, maxima)
     __shared__ float2 weight[2][RP];                        // what the two O^T's of a row are multiplied with
@@ -271,15 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     __shared__ long long col_off[RP];                       // its offset in the output
 
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t* slots = base;
-    uint8_t* qs = slots + NS * L::kSlot + 1024;         // 1 KB: an M = 128 MMA over 64 dimensions reads past its slot
+    uint8_t* kslots = base;
+    uint8_t* vslots = kslots + NK * L::kSlot;
+    uint8_t* qs = vslots + NV * L::kSlot + 1024;        // 1 KB: an M = 128 MMA over 64 dimensions reads past its slot
     uint8_t* ps = qs + NQ * L::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&q_full[i], 1);
@@ -289,14 +356,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], kArrive);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_empty[i], kSoftWarps);
+            mbar_init(&o_empty[i], 4);
+            mbar_init(&l_full[i], kSoftWarps);
+            mbar_init(&l_empty[i], 4);
+            mbar_init(&fin[i], 1);
             poison[i] = 0;
         }
         for (int i = 0; i < NP; ++i) {
             mbar_init(&p_full[i], kArrive);
             mbar_init(&p_empty[i], 1);
         }
-        mbar_init(&fin, 1);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], kReaders);
+        }
         fence_barrier_init();
         dead = 0;
         first[0] = 0;
@@ -306,16 +379,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         tok[i] = t;
         col_off[i] = t * p.out_stride + (long long)(i - t * p.group) * HD;
     }
-    if (warp == kMmaWarp) tmem_alloc(&tmem_base, L::kCols);
+    if (warp == kScoreWarp) tmem_alloc(&tmem_base, L::kCols);
     pdl_wait();
     pdl_launch_dependents();
 
-    // first[q]: exclusive sums of the sequences' units, 4 sequences a thread
+    // first[q]: exclusive sums of the sequences' units, 2 sequences a thread
     {
-        long long v[4], sum = 0;   // 64 bits: row ranges that overlap can pass any bound
+        static_assert(2 * kThreads >= split::kMaxSeqs, "2 sequences a thread");
+        long long v[2], sum = 0;   // 64 bits: row ranges that overlap can pass any bound
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int q = tid * 4 + k;
+        for (int k = 0; k < 2; ++k) {
+            const int q = tid * 2 + k;
             v[k] = 0;
             if (q < p.nseq) {
                 const int r0 = p.row_start[q], r1 = p.row_start[q + 1], n = p.len[q];
@@ -335,16 +409,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const long long o = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += o;
         }
-        if (lane == 31) warp_sum[warp] = inc;
-        __syncthreads();
         long long run = inc - sum;
-        for (int w = 0; w < warp; ++w) run += warp_sum[w];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            run += v[k];
-            if (tid * 4 + k < p.nseq) first[tid * 4 + k + 1] = (int)run;
+        if (p.nseq > 64) {                      // more than one warp holds sequences
+            if (lane == 31) warp_sum[warp] = inc;
+            __syncthreads();
+            for (int w = 0; w < warp && w * 64 < p.nseq; ++w) run += warp_sum[w];
         }
-        if (tid == kThreads - 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            run += v[k];
+            if (tid * 2 + k < p.nseq) first[tid * 2 + k + 1] = (int)run;
+        }
+        if (tid == (p.nseq - 1) / 2) {
             total = run > 0x7fffffff ? 0 : (int)run;
             if (run > 0x7fffffff && blockIdx.x == 0 && p.err) atomicCAS(p.err, 0, SPEC_PAGED_BAD_ROWS);
         }
@@ -353,162 +429,197 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const int T = total, work = split::working(gridDim.x, T);
-    const int begin = split::begin_of(blockIdx.x, T, work), end = split::begin_of(blockIdx.x + 1, T, work);
+    const split::Deal deal(total, gridDim.x);
+    const int begin = deal.begin(blockIdx.x), end = deal.begin(blockIdx.x + 1);
+    const int n = end - begin;                  // units
     volatile int* deadp = &dead;
+    Ring<kSegs> sr;                             // every role's place in the list of segments
+    auto take = [&](bool one) {                 // the next segment; `one`: this thread alone stands for its warp
+        wait(&seg_full[sr.at], sr.round, deadp);
+        const Seg s = segs[sr.at];
+        if (!one) __syncwarp();
+        if (one || lane == 0) mbar_arrive(&seg_empty[sr.at]);
+        sr.step();
+        return s;
+    };
 
-    if (warp == kLoadWarp) {
-        // ---------------- TMA copies (lane 0 issues; the lanes look up pages) ----------------
-        Walk w(p, first, begin, end);
-        Ring<NS> kv;
-        Ring<NQ> qr;
-        bool ok = true;
-        while (ok && w.next()) {
+    if (warp >= kScoreWarp && warp < kResultWarp) {
+        regs_down<kIssueRegs>();
+        if (warp == kListWarp) {
+            // ---------------- the list of segments, and what the join kernel has to do here ----------------
             if (lane == 0) {
+                Walk w(p, first, begin, end);
+                Meta into = {}, from = {};
+                while (w.next()) {
+                    Seg s;
+                    s.c0 = w.c0;
+                    s.units = w.c1 - w.c0;
+                    s.R = w.R;
+                    s.last0 = w.last0();
+                    s.len = w.len;
+                    s.q = w.q;
+                    s.head = w.head;
+                    s.row0 = w.row_base + w.block * p.tokens;
+                    s.slot = w.whole() ? -1 : 2 * (int)blockIdx.x + (w.u - s.units == begin ? 0 : 1);
+                    if (!wait(&seg_empty[sr.at], sr.round ^ 1, deadp)) break;
+                    segs[sr.at] = s;
+                    mbar_arrive(&seg_full[sr.at]);
+                    sr.step();
+                    if (w.seg == 0 && w.c0 > 0) into = w.meta(deal);
+                }
+                if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(deal);
+                p.meta[2 * blockIdx.x] = into;
+                p.meta[2 * blockIdx.x + 1] = from;
+            }
+        } else if (warp == kLoadWarp) {
+            // ---------------- TMA copies (one elected lane issues; the lanes look up pages) ----------------
+            Ring<NK> kr;
+            Ring<NV> vr;
+            Ring<NQ> qr;
+            bool ok = true;
+            for (int done = 0; done < n && ok;) {
+                const Seg s = take(false);
+                done += s.units;
                 uint64_t* qf = &q_full[qr.at];
-                ok = wait(&q_empty[qr.at], qr.round ^ 1, deadp);
-                if (ok) {
+                ok = __all_sync(0xffffffffu, wait(&q_empty[qr.at], qr.round ^ 1, deadp) && !*deadp);
+                if (!ok) break;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(qf, (uint32_t)(p.tokens * p.group * HD * 2));
 #pragma unroll
                     for (int hf = 0; hf < HD / 64; ++hf)
-                        tma3(qs + qr.at * L::kQ + hf * RP * 128, &p.mq, hf * 64, w.head * p.group,
-                             w.row_base + w.block * p.tokens, qf);
+                        tma3(qs + qr.at * L::kQ + hf * RP * 128, &p.mq, hf * 64, s.head * p.group, s.row0, qf);
                 }
+                __syncwarp();
                 qr.step();
-            }
-            const int held = (w.len + SPEC_PAGE - 1) / SPEC_PAGE;
-            const int* tab = p.tables + (size_t)w.q * p.table_pages;
-            int z0 = -1, z1 = -1;               // the lane's chunk: tensor-map rows of its two pages
-            for (int c = w.c0; c < w.c1; ++c) {
-                const int k = (c - w.c0) & 31;
-                if (k == 0) {                   // the next 32 chunks' pages, one chunk a lane
-                    const int e = 2 * (c + lane);
+                const int held = (s.len + SPEC_PAGE - 1) / SPEC_PAGE;
+                const int* tab = p.tables + (size_t)s.q * p.table_pages;
+                int z0 = -1, z1 = -1;           // the lane's chunk: tensor-map rows of its two pages
+                for (int k = 0; k < s.units; ++k) {
+                    const int c = s.c0 + k;
+                    if ((k & 31) == 0) {        // the next 32 chunks' pages, one chunk a lane
+                        const int e = 2 * (c + lane);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        int z = -1;
-                        if (c + lane < w.c1 && e + i < held) {
-                            const int page = tab[e + i];
-                            if (page >= 0 && page < p.num_pages) z = page * p.hkv + w.head;
-                            else if (p.err) atomicCAS(p.err, 0, SPEC_PAGED_BAD_PAGE);
+                        for (int i = 0; i < 2; ++i) {
+                            int z = -1;
+                            if (k + lane < s.units && e + i < held) {
+                                const int page = tab[e + i];
+                                if (page >= 0 && page < p.num_pages) z = page * p.hkv + s.head;
+                                else if (p.err) atomicCAS(p.err, 0, SPEC_PAGED_BAD_PAGE);
+                            }
+                            if (i) z1 = z;
+                            else z0 = z;
                         }
-                        if (i) z1 = z;
-                        else z0 = z;
                     }
-                }
-                const int a0 = __shfl_sync(0xffffffffu, z0, k), a1 = __shfl_sync(0xffffffffu, z1, k);
-                if (lane == 0 && ok) {
-                    const int n = min(2, held - 2 * c);   // pages that exist (a bad one reads as zeros: z = -1)
+                    const int a0 = __shfl_sync(0xffffffffu, z0, k & 31), a1 = __shfl_sync(0xffffffffu, z1, k & 31);
+                    const int pages = min(2, held - 2 * c);   // that exist (a bad one reads as zeros: z = -1)
+                    auto copy = [&](uint64_t* empty, uint32_t parity, uint64_t* full, uint8_t* dst, const CUtensorMap* map) {
+                        ok = ok && wait(empty, parity, deadp);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(full, pages > 0 ? (uint32_t)(pages * SPEC_PAGE * HD * 2) : 0u);
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        ok = ok && wait(&kv_empty[kv.at], kv.round ^ 1, deadp);
-                        if (!ok) break;
-                        uint8_t* dst = slots + kv.at * L::kSlot;
-                        uint64_t* full = &kv_full[kv.at];
-                        const CUtensorMap* map = v ? &p.mv : &p.mk;
-                        mbar_arrive_expect_tx(full, n > 0 ? (uint32_t)(n * SPEC_PAGE * HD * 2) : 0u);
-#pragma unroll
-                        for (int hf = 0; hf < HD / 64; ++hf) {
-                            if (n > 0) tma3(dst + hf * kChunk * 128, map, hf * 64, 0, a0, full);
-                            if (n > 1) tma3(dst + hf * kChunk * 128 + SPEC_PAGE * 128, map, hf * 64, 0, a1, full);
+                            for (int hf = 0; hf < HD / 64; ++hf) {
+                                if (pages > 0) tma3(dst + hf * kChunk * 128, map, hf * 64, 0, a0, full);
+                                if (pages > 1) tma3(dst + hf * kChunk * 128 + SPEC_PAGE * 128, map, hf * 64, 0, a1, full);
+                            }
                         }
-                        kv.step();
-                    }
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        }
-        if (lane == 0 && *deadp) {              // every buffer's last copy, as far as one was issued
-            for (int i = 0; i < NS; ++i) drain(&kv_full[i], i < kv.at ? kv.round : kv.round ^ 1);
-            for (int i = 0; i < NQ; ++i) drain(&q_full[i], i < qr.at ? qr.round : qr.round ^ 1);
-        }
-        if (lane == 0) {                        // what the join kernel has to do here
-            Meta into = {}, from = {};
-            Walk f(p, first, begin, end);
-            if (f.next() && f.c0 > 0) into = f.meta(T, work);
-            if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(T, work);
-            p.meta[2 * blockIdx.x] = into;
-            p.meta[2 * blockIdx.x + 1] = from;
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ---------------- MMAs (one thread): S^T one unit ahead of O^T ----------------
-        if (lane == 0) {
-            Walk ws(p, first, begin, end), wo(p, first, begin, end);
-            Ring<NS> ks, vs;                    // the slots of unit i's K and unit i - 1's V
-            Ring<NQ> qr;
-            Ring<NP> pr;
-            vs.step();
-            const uint32_t sa = smem_u32(slots), qa = smem_u32(qs), pa = smem_u32(ps);
-            bool ok = true;
-            int cs = 0, co = 0;                 // next chunk of ws' and wo's segments
-            const int n = end - begin;
-            for (int i = 0; i <= n && ok; ++i) {
-                if (i < n) {                    // S^T of unit i
-                    if (i == 0 || cs == ws.c1) {
-                        ws.next();
-                        cs = ws.c0;
-                        ok = ok && wait(&q_full[qr.at], qr.round, deadp);
-                    }
-                    ok = ok && wait(&kv_full[ks.at], ks.round, deadp);
-                    ok = ok && wait(&s_empty[i & 1], ((i >> 1) & 1) ^ 1, deadp);
+                        __syncwarp();
+                    };
+                    copy(&k_empty[kr.at], kr.round ^ 1, &k_full[kr.at], kslots + kr.at * L::kSlot, &p.mk);
+                    if (ok) kr.step();
+                    copy(&v_empty[vr.at], vr.round ^ 1, &v_full[vr.at], vslots + vr.at * L::kSlot, &p.mv);
+                    if (ok) vr.step();
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t id = umma_idesc_bf16(128, (ws.R + 15) & ~15);
-                    const uint64_t dk = desc_sw128(sa + ks.at * L::kSlot, 16, 1024);
+                }
+            }
+            if (lane == 0 && *deadp) {          // every buffer's last copy, as far as one was issued
+                for (int i = 0; i < NK; ++i) drain(&k_full[i], i < kr.at ? kr.round : kr.round ^ 1);
+                for (int i = 0; i < NV; ++i) drain(&v_full[i], i < vr.at ? vr.round : vr.round ^ 1);
+                for (int i = 0; i < NQ; ++i) drain(&q_full[i], i < qr.at ? qr.round : qr.round ^ 1);
+            }
+        } else if (warp == kScoreWarp) {
+            // ---------------- MMAs of S^T (one elected thread) ----------------
+            if (elect_one()) {
+                Ring<NK> ks;
+                Ring<NQ> qr;
+                Ring<2> sb;
+                const uint32_t sa = smem_u32(kslots), qa = smem_u32(qs);
+                bool ok = true;
+                for (int done = 0; done < n && ok;) {
+                    const Seg s = take(true);
+                    done += s.units;
+                    ok = wait(&q_full[qr.at], qr.round, deadp) && !*deadp;
+                    const uint32_t id = umma_idesc_bf16(128, (s.R + 15) & ~15);
                     const uint64_t dq = desc_sw128(qa + qr.at * L::kQ, 16, 1024);
+                    for (int k = 0; k < s.units && ok; ++k) {
+                        ok = wait(&k_full[ks.at], ks.round, deadp) && wait(&s_empty[sb.at], sb.round ^ 1, deadp);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dk = desc_sw128(sa + ks.at * L::kSlot, 16, 1024);
 #pragma unroll
-                    for (int k = 0; k < HD / 16; ++k)
-                        umma_bf16_id(tmem + (i & 1) * RP, dk + (k >> 2) * (kChunk * 128 >> 4) + (k & 3) * 2,
-                                     dq + (k >> 2) * (RP * 128 >> 4) + (k & 3) * 2, id, k > 0);
-                    umma_commit(&s_full[i & 1]);
-                    umma_commit(&kv_empty[ks.at]);
-                    ks.step();
-                    ks.step();
-                    if (++cs == ws.c1) {
-                        umma_commit(&q_empty[qr.at]);
-                        qr.step();
+                        for (int e = 0; e < HD / 16; ++e)
+                            umma_bf16_id(tmem + sb.at * RP, dk + (e >> 2) * (kChunk * 128 >> 4) + (e & 3) * 2,
+                                         dq + (e >> 2) * (RP * 128 >> 4) + (e & 3) * 2, id, e > 0);
+                        umma_commit(&s_full[sb.at]);
+                        umma_commit(&k_empty[ks.at]);
+                        ks.step();
+                        sb.step();
                     }
+                    if (ok) umma_commit(&q_empty[qr.at]);
+                    qr.step();
                 }
-                if (i > 0) {                    // O^T of unit i - 1
-                    const int j = i - 1;
-                    if (j == 0 || co == wo.c1) {
-                        wo.next();
-                        co = wo.c0;
-                        ok = ok && wait(&o_empty[wo.seg & 1], ((wo.seg >> 1) & 1) ^ 1, deadp);
-                    }
-                    ok = ok && wait(&kv_full[vs.at], vs.round, deadp);
-                    ok = ok && wait(&p_full[pr.at], pr.round, deadp);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // A = V^T and B = P^T, both MN-major
-                    const uint32_t id = umma_idesc_bf16(128, kStack ? 2 * RP : (wo.R + 15) & ~15) | (1u << 15) | (1u << 16);
-                    const uint64_t dv = desc_sw128(sa + vs.at * L::kSlot, HD == 128 ? kChunk * 128 : 1024, 1024);
-                    const uint64_t dp = umma_desc_kmajor(pa + pr.at * 2 * L::kP, 128, kChunk * 16);
-                    const int og = kStream ? (wo.seg & 1) * 2 + (j & 1) : wo.seg & 1;
-                    const uint32_t o = tmem + 2 * RP + og * L::kO;
-                    const bool more = co >= wo.c0 + kGroups;   // this O^T holds earlier chunks
-#pragma unroll
-                    for (int part = 0; part < (kStack ? 1 : 2); ++part)
-#pragma unroll
-                        for (int k = 0; k < kChunk / 16; ++k)
-                            umma_bf16_id(o, dv + k * (2048 >> 4), dp + part * (L::kP >> 4) + k * (256 >> 4), id,
-                                         more || (part | k) != 0);
-                    umma_commit(&kv_empty[vs.at]);
-                    umma_commit(&p_empty[pr.at]);
-                    if (++co == wo.c1) umma_commit(&o_full[wo.seg & 1]);
-                    vs.step();
-                    vs.step();
-                    pr.step();
+                if (!ok) {
+                    umma_commit(&fin[0]);
+                    drain(&fin[0], 0);
                 }
             }
-            if (!ok) {
-                umma_commit(&fin);
-                drain(&fin, 0);
+        } else {   // warp 9
+            // ---------------- MMAs of O^T (one elected thread) ----------------
+            if (elect_one()) {
+                Ring<NV> vs;
+                Ring<NP> pr;
+                const uint32_t sa = smem_u32(vslots), pa = smem_u32(ps);
+                bool ok = true;
+                int j = 0;                      // unit
+                for (int done = 0, seg = 0; done < n && ok; ++seg) {
+                    const Seg s = take(true);
+                    done += s.units;
+                    ok = wait(&o_empty[seg & 1], ((seg >> 1) & 1) ^ 1, deadp) && !*deadp;
+                    // A = V^T and B = P^T, both MN-major
+                    const uint32_t id = umma_idesc_bf16(128, kStack ? 2 * RP : (s.R + 15) & ~15) | (1u << 15) | (1u << 16);
+                    for (int k = 0; k < s.units && ok; ++k, ++j) {
+                        ok = wait(&v_full[vs.at], vs.round, deadp) && wait(&p_full[pr.at], pr.round, deadp);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dv = desc_sw128(sa + vs.at * L::kSlot, HD == 128 ? kChunk * 128 : 1024, 1024);
+                        const uint64_t dp = umma_desc_kmajor(pa + pr.at * 2 * L::kP, 128, kChunk * 16);
+                        const int og = kStream ? (seg & 1) * 2 + (j & 1) : seg & 1;
+                        const uint32_t o = tmem + 2 * RP + og * L::kO;
+                        const bool more = k >= kGroups;     // this O^T holds earlier chunks
+#pragma unroll
+                        for (int part = 0; part < (kStack ? 1 : 2); ++part)
+#pragma unroll
+                            for (int e = 0; e < kChunk / 16; ++e)
+                                umma_bf16_id(o, dv + e * (2048 >> 4), dp + part * (L::kP >> 4) + e * (256 >> 4), id,
+                                             more || (part | e) != 0);
+                        umma_commit(&v_empty[vs.at]);
+                        umma_commit(&p_empty[pr.at]);
+                        vs.step();
+                        pr.step();
+                    }
+                    if (ok) umma_commit(&o_full[seg & 1]);
+                }
+                if (!ok) {
+                    umma_commit(&fin[1]);
+                    drain(&fin[1], 0);
+                }
             }
         }
         __syncwarp();
-    } else {
-        // ---------------- softmax and results: thread = key, then head dimension ----------------
+    } else if (warp < kSoftWarps) {
+        // ---------------- softmax: thread = key ----------------
+        regs_up<kSoftRegs>();
         const int wg = warp >> 2, qd = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         const int key = qd * 32 + lane;
@@ -516,23 +627,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const int gi = kStream ? wg : 0;        // its reference and O^T
         const int bar = kSoftBar + wg;
         const F2 k2(p.scale_log2, p.scale_log2);
-        Walk w(p, first, begin, end);
-        int base_i = 0;                         // the segment's first unit
-        Ring<NS> vs;                            // slot of the next unit's V
-        vs.step();
+        int i = 0;                              // unit
+        Ring<NV> vs;                            // slot of the next unit's V
         bool ok = true;
-        while (w.next()) {
-            const int par = w.seg & 1, units = w.c1 - w.c0;
-            const int last0 = w.last0(), rows = w.R - col0;   // live rows of this thread
+        for (int done = 0, seg = 0; done < n; ++seg) {
+            const Seg w = take(false);
+            if (bar_any(bar, 128, *deadp != 0)) break;   // a wait gave up: nothing was listed (all of the warpgroup leaves)
+            done += w.units;
+            const int par = seg & 1, last0 = w.last0, rows = w.R - col0;   // live rows of this thread
             float* const mine = nref[par][gi];
+            ok = ok && wait(&l_empty[par], ((seg >> 1) & 1) ^ 1, deadp);   // the results of two segments ago have been read
             F2 l[NC / 2];
 #pragma unroll
             for (int j = 0; j < NC / 2; ++j) l[j] = F2(0.f, 0.f);
             bool fresh = true;
-            for (int c = w.c0; c < w.c1; ++c) {
-                const int i = base_i + c - w.c0;
-                const Ring<NS> v = vs;
-                vs.step();
+            for (int c = w.c0; c < w.c0 + w.units; ++c, ++i) {
+                const Ring<NV> v = vs;
                 vs.step();
                 if (kStream && (i & 1) != wg) continue;
                 const uint32_t st = lanes + (i & 1) * RP + col0;
@@ -543,13 +653,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 float s[NC];
                 auto scores = [&]() {           // the chunk's scores, -inf where a row does not see the key
 #pragma unroll
-                    for (int j = 0; j < NC; j += 8)
-                        if (j < rows) tmem_ld8_async(st + j, s + j);
+                    for (int j = 0; j < NC; j += kSpan)
+                        if (j < rows) {
+                            if constexpr (kSpan == 8) tmem_ld8_async(st + j, s + j);
+                            else if constexpr (kSpan == 16) tmem_ld16_async(st + j, s + j);
+                            else tmem_ld32_async(st + j, s + j);
+                        }
                     tmem_wait_ld();
                     if (masked) {
 #pragma unroll
-                        for (int j = 0; j < NC; ++j)
-                            if (j < rows && kp > last0 + tok[col0 + j]) s[j] = -INFINITY;
+                        for (int j = 0; j < NC; j += kSpan)
+                            if (j < rows) {
+#pragma unroll
+                                for (int e = 0; e < kSpan; ++e)
+                                    if (kp > last0 + tok[col0 + j + e]) s[j + e] = -INFINITY;
+                            }
                     }
                 };
                 scores();
@@ -563,15 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     }
                     named_bar_sync(bar, 128);
                 }
-                float top = kNone;
+                float top[2] = {kNone, kNone};
                 auto exponents = [&]() {
 #pragma unroll
-                    for (int j = 0; j < NC; j += 4)
-                        if ((j & ~7) < rows) {
-                            const float4 m = *reinterpret_cast<const float4*>(&mine[col0 + j]);
-                            fma2(F2(s[j], s[j + 1]), k2, F2(m.x, m.y)).get(s[j], s[j + 1]);
-                            fma2(F2(s[j + 2], s[j + 3]), k2, F2(m.z, m.w)).get(s[j + 2], s[j + 3]);
-                            top = fmaxf(top, fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
+                    for (int j0 = 0; j0 < NC; j0 += kSpan)
+                        if (j0 < rows) {
+#pragma unroll
+                            for (int j = j0; j < j0 + kSpan; j += 4) {
+                                const float4 m = *reinterpret_cast<const float4*>(&mine[col0 + j]);
+                                fma2(F2(s[j], s[j + 1]), k2, F2(m.x, m.y)).get(s[j], s[j + 1]);
+                                fma2(F2(s[j + 2], s[j + 3]), k2, F2(m.z, m.w)).get(s[j + 2], s[j + 3]);
+                                top[j / 4 & 1] = fmaxf(top[j / 4 & 1], fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
+                            }
                         }
                 };
                 exponents();
@@ -579,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 auto product_done = [&]() {
                     ok = ok && wait(&p_empty[kStream ? i & 1 : 0], ((kStream ? i >> 1 : i) & 1) ^ 1, deadp);
                 };
-                if (rows > 0 && bar_any(bar, 128, top > kLimit)) {
+                if (rows > 0 && bar_any(bar, 128, fmaxf(top[0], top[1]) > kLimit)) {
                     // the references move up to the chunk's maxima
                     product_done();
                     tc_fence_after();
@@ -635,36 +756,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[i & 1]);
                 fresh = false;
-#pragma unroll
-                for (int j = 0; j < NC; j += 2)
-                    if ((j & ~7) < rows) {
-                        s[j] = ex2_approx(s[j]);
-                        s[j + 1] = ex2_approx(s[j + 1]);
-                        l[j / 2] = add2(l[j / 2], F2(s[j], s[j + 1]));
-                    }
                 product_done();
                 uint8_t* ph = ps + (kStream ? i & 1 : 0) * 2 * L::kP + (col0 >> 3) * (kChunk * 16) + key * 16;
 #pragma unroll
-                for (int j = 0; j < NC; j += 8)
-                    if (j < rows) {
-                        uint32_t hi[4], lo[4];
+                for (int j0 = 0; j0 < NC; j0 += kSpan)
+                    if (j0 < rows) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = s[j + 2 * e], b = s[j + 2 * e + 1];
-                            hi[e] = cvt_bf16x2(a, b);
-                            lo[e] = cvt_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xFFFF0000u));
+                        for (int j = j0; j < j0 + kSpan; j += 8) {
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const F2 x(ex2_approx(s[j + 2 * e]), ex2_approx(s[j + 2 * e + 1]));
+                                l[j / 2 + e] = add2(l[j / 2 + e], x);
+                                float a, b;
+                                x.get(a, b);
+                                hi[e] = cvt_bf16x2(a, b);
+                                const F2 h(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u));
+                                fma2(h, F2(-1.f, -1.f), x).get(a, b);
+                                lo[e] = cvt_bf16x2(a, b);
+                            }
+                            uint8_t* dst = ph + (j >> 3) * (kChunk * 16);
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(dst + L::kP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
-                        uint8_t* dst = ph + (j >> 3) * (kChunk * 16);
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(dst + L::kP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 if (masked && (kStream || wg == 0)) {
                     // Values of positions that some row does not see: behind the
                     // length they become zero (a weight of zero does not silence a
                     // NaN), between the rows' last positions non-finite ones do,
                     // and are added at the end to the rows that see them.
-                    ok = ok && wait(&kv_full[v.at], v.round, deadp);
-                    uint8_t* vt = slots + v.at * L::kSlot;
+                    // (the slot's last V has been consumed: product_done)
+                    ok = ok && wait(&v_full[v.at], v.round, deadp);
+                    uint8_t* vt = vslots + v.at * L::kSlot;
                     const int from = max(0, last0 + 1 - c * kChunk), live = w.len - c * kChunk;
                     for (int t = from * (HD / 8) + key; t < kChunk * (HD / 8); t += 128) {
                         const int r = t / (HD / 8), d8 = t % (HD / 8);
@@ -682,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             }
                             if (hit) {
                                 *at = x;
-                                poison[par] = w.seg + 1;
+                                poison[par] = seg + 1;
                             }
                         }
                     }
@@ -691,10 +814,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[kStream ? i & 1 : 0]);
             }
-            // ---- the segment's rows ----
-            const int ga = kStream ? base_i & 1 : 0;    // the warpgroup of the first unit; the other has none in a segment of one
-            const bool two = kStream && units > 1;
-            base_i += units;
             // sums over the warp's keys, 8 rows at a time: halves are exchanged until
             // lane r of each 8 holds row r, then those lanes are added
 #pragma unroll
@@ -716,14 +835,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
                     if (lane < 8) xl[par][gi][qd][col0 + j + lane] = x[0];
                 }
-            if (kStream) named_bar_sync(kBothBar, 256);
-            else named_bar_sync(bar, 128);
-            const bool whole = w.whole();
-            const int slot = 2 * blockIdx.x + (w.u - units == begin ? 0 : 1);
-            // the rows this warpgroup writes: every other 8 (of the halves: its own)
-            auto writes = [&](int r) { return r < w.R && (kStream ? ((r >> 3) & 1) == wg : (r >= col0 && r < col0 + NC)); };
-            if (key < RP && writes(key)) {
-                const int r = key;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_full[par]);
+        }
+    } else {
+        // ---------------- results: thread = head dimension ----------------
+        regs_down<kResultRegs>();
+        const int qd = warp & 3, d = qd * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
+        int i = 0;                              // the segment's first unit
+        for (int done = 0, seg = 0; done < n; ++seg) {
+            const Seg w = take(false);
+            if (bar_any(kResultBar, 128, *deadp != 0)) break;
+            done += w.units;
+            const int par = seg & 1, last0 = w.last0;
+            const int ga = kStream ? i & 1 : 0; // the warpgroup of the first unit; the other has none in a segment of one
+            const bool two = kStream && w.units > 1, whole = w.slot < 0;
+            i += w.units;
+            bool ok = wait(&l_full[par], (seg >> 1) & 1, deadp);
+            if (d < w.R) {
+                const int r = d;
                 float ma = -nref[par][ga][r], la = xl[par][ga][0][r] + xl[par][ga][1][r] + xl[par][ga][2][r] + xl[par][ga][3][r];
                 float fa = 1.f, fb = 0.f;
                 if (two) {
@@ -741,80 +872,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     fa *= inv;
                     fb *= inv;
                 } else {
-                    p.part_ml[(size_t)slot * RP + r] = make_float2(ma, la);
+                    p.part_ml[(size_t)w.slot * RP + r] = make_float2(ma, la);
                 }
                 weight[par][r] = make_float2(fa, fb);
             }
-            named_bar_sync(bar, 128);
-            if (kStream ? w.R > 8 * wg : rows > 0) {
-                ok = ok && wait(&o_full[par], (w.seg >> 1) & 1, deadp);
-                tc_fence_after();
-                const int d = key;
-                const bool bad = poison[par] == w.seg + 1;
-                const long long out0 = (long long)(w.row_base + w.block * p.tokens) * p.out_stride +
-                                       (long long)w.head * p.group * HD + d;
+            named_bar_sync(kResultBar, 128);
+            const bool bad = poison[par] == seg + 1;
+            ok = ok && wait(&o_full[par], (seg >> 1) & 1, deadp);
+            tc_fence_after();
+            const long long out0 = (long long)w.row0 * p.out_stride + (long long)w.head * p.group * HD + d;
 #pragma unroll 1
-                for (int j = kStream ? 8 * wg : col0; j < (kStream ? RP : col0 + NC) && j < w.R; j += kStream ? 16 : 8) {
-                    float o[8], x[8];
-                    const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j;
-                    tmem_ld8_async(at, o);
+            for (int j = 0; j < w.R; j += 8) {
+                float o[8], x[8];
+                const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j;
+                tmem_ld8_async(at, o);
+                if (kStack) {
+                    tmem_ld8_async(at + RP, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] += x[e];
+                } else {
+                    tmem_wait_ld();
+                }
+                float2 f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = weight[par][j + e];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= f[e].x;
+                if (two) {
+                    const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j;
+                    tmem_ld8_async(bt, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
                     if (kStack) {
-                        tmem_ld8_async(at + RP, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] += x[e];
-                    } else {
-                        tmem_wait_ld();
-                    }
-                    float2 f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = weight[par][j + e];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] *= f[e].x;
-                    if (two) {
-                        const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j;
-                        tmem_ld8_async(bt, x);
+                        tmem_ld8_async(bt + RP, x);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
-                        if (kStack) {
-                            tmem_ld8_async(bt + RP, x);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
-                        }
                     }
-                    if (d < HD) {
-                        if (bad)
-                            for (int t = max(last0 + 1, w.c0 * kChunk); t < min(w.len, w.c1 * kChunk); ++t) {
-                                const int page = p.tables[(size_t)w.q * p.table_pages + t / SPEC_PAGE];
-                                if (page < 0 || page >= p.num_pages) continue;
-                                const float v = bf2f(p.vpool[(((size_t)page * p.hkv + w.head) * SPEC_PAGE + t % SPEC_PAGE) * HD + d]);
-                                if (!isfinite(v))
+                }
+                if (d < HD) {
+                    if (bad)
+                        for (int t = max(last0 + 1, w.c0 * kChunk); t < min(w.len, (w.c0 + w.units) * kChunk); ++t) {
+                            const int page = p.tables[(size_t)w.q * p.table_pages + t / SPEC_PAGE];
+                            if (page < 0 || page >= p.num_pages) continue;
+                            const float v = bf2f(p.vpool[(((size_t)page * p.hkv + w.head) * SPEC_PAGE + t % SPEC_PAGE) * HD + d]);
+                            if (!isfinite(v))
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        if (t <= last0 + tok[j + e]) o[e] += v;
-                            }
+                                for (int e = 0; e < 8; ++e)
+                                    if (t <= last0 + tok[j + e]) o[e] += v;
+                        }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int r = j + e;
-                            if (r < w.R) {
-                                if (whole) p.out[out0 + col_off[r]] = f2bf(last0 + tok[r] >= 0 ? o[e] : 0.f);
-                                else p.part_o[((size_t)slot * RP + r) * HD + d] = o[e];
-                            }
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = j + e;
+                        if (r < w.R) {
+                            if (whole) p.out[out0 + col_off[r]] = f2bf(last0 + tok[r] >= 0 ? o[e] : 0.f);
+                            else p.part_o[((size_t)w.slot * RP + r) * HD + d] = o[e];
                         }
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[par]);
+            if (lane == 0) {
+                mbar_arrive(&o_empty[par]);
+                mbar_arrive(&l_empty[par]);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && dead && p.err) atomicCAS(p.err, 0, SPEC_PAGED_TIMEOUT);
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kCols);
     }

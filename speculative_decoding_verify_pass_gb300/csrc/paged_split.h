@@ -7,9 +7,9 @@
 // blocks * n_kv_heads pairs of `chunks` units each, pairs in (row block, kv
 // head) order; a sequence with rows but no positions has one (empty) chunk, so
 // that its rows are written.  first[q] is the exclusive sum of the units, T their
-// number.  Of C = min(CTAs, T) working CTAs, CTA c takes the contiguous units
-// [T c / C, T (c+1) / C): at least one, and every CTA the same number give or
-// take one, whatever the lengths are.
+// number.  C = min(CTAs, T) CTAs work, each on the same number of contiguous
+// units give or take one, whatever the lengths are: the first T mod C CTAs take
+// T / C + 1, the others T / C.
 //
 // A maximal run of one pair's units inside a CTA is a segment.  A segment that
 // covers its pair writes the rows' results; any other leaves a partial
@@ -40,12 +40,17 @@ SPLIT_HD int64_t units_of(int rows, int len, int tokens, int hkv) {
     return (int64_t)blocks_of(rows, tokens) * hkv * chunks_of(len);
 }
 
-// CTAs that work on `total` units, and the first unit of the c-th.
-SPLIT_HD int working(int ctas, int total) { return total < ctas ? total : ctas; }
-SPLIT_HD int begin_of(int c, int total, int work) { return c < work ? (int)((int64_t)total * c / work) : total; }
-
-// The CTA that works on unit u: the last c with begin_of(c) <= u.
-SPLIT_HD int cta_of(int u, int total, int work) { return (int)((((int64_t)u + 1) * work - 1) / total); }
+// The deal of `total` units to at most `ctas` CTAs.
+struct Deal {
+    int total, work, each, more;    // work CTAs; `more` of them take each + 1 units, the rest `each`
+    SPLIT_HD Deal(int t, int ctas) : total(t), work(t < ctas ? t : ctas), each(work ? t / work : 0), more(t - each * work) {}
+    // first unit of CTA c (the total from `work` on)
+    SPLIT_HD int begin(int c) const { return c < work ? c * each + (c < more ? c : more) : total; }
+    // the CTA that works on unit u < total
+    SPLIT_HD int cta(int u) const { return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each; }
+    // partials of a pair that begins in CTA c and whose units end at pair_end (exclusive), c's included
+    SPLIT_HD int parts(int c, int pair_end) const { return cta(pair_end - 1) - c + 1; }
+};
 
 // The sequence that holds unit u < first[nseq]: the last q with first[q] <= u.
 SPLIT_HD int sequence_of(const int* first, int nseq, int u) {
@@ -57,9 +62,6 @@ SPLIT_HD int sequence_of(const int* first, int nseq, int u) {
     }
     return lo;
 }
-
-// Number of partials of a pair whose units end at pair_end (exclusive), owner c included.
-SPLIT_HD int contributors(int c, int pair_end, int total, int work) { return cta_of(pair_end - 1, total, work) - c + 1; }
 
 // Tile height (rows per kv head) for blocks of max_new tokens of G query
 // heads: the smallest of 16, 32, 64, 128 that holds a whole block, else 128.

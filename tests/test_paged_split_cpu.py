@@ -17,11 +17,11 @@ extern "C" {
 int chunks(int len) { return chunks_of(len); }
 int blocks(int rows, int tokens) { return blocks_of(rows, tokens); }
 long long units(int rows, int len, int tokens, int hkv) { return units_of(rows, len, tokens, hkv); }
-int work(int ctas, int total) { return working(ctas, total); }
-int begin(int c, int total, int w) { return begin_of(c, total, w); }
-int cta(int u, int total, int w) { return cta_of(u, total, w); }
+int work(int ctas, int total) { return Deal(total, ctas).work; }
+int begin(int c, int total, int ctas) { return Deal(total, ctas).begin(c); }
+int cta(int u, int total, int ctas) { return Deal(total, ctas).cta(u); }
 int sequence(const int* first, int nseq, int u) { return sequence_of(first, nseq, u); }
-int parts(int c, int pair_end, int total, int w) { return contributors(c, pair_end, total, w); }
+int parts(int c, int pair_end, int total, int ctas) { return Deal(total, ctas).parts(c, pair_end); }
 int tile(int group, int max_new) { return tile_rows(group, max_new); }
 }
 """
@@ -73,8 +73,8 @@ def test_segments_partition_the_units_and_partials_meet_their_owner(split, case)
             pair_of[u] = i
     metas = []
     for c in range(ctas):
-        a, b = split.begin(c, T, w), split.begin(c + 1, T, w)
-        assert a == at and (b > a if c < w else b == a)
+        a, b = split.begin(c, T, ctas), split.begin(c + 1, T, ctas)
+        assert a == at and (b - a in (T // w, T // w + 1) if c < w else b == a)
         at = b
         u = a
         last = None
@@ -82,7 +82,7 @@ def test_segments_partition_the_units_and_partials_meet_their_owner(split, case)
             q = split.sequence(arr, len(lens), u)
             assert first[q] <= u < first[q + 1]
             i = pair_of[u]
-            assert split.cta(u, T, w) == c and split.cta(pairs[i][0], T, w) <= c
+            assert split.cta(u, T, ctas) == c and split.cta(pairs[i][0], T, ctas) <= c
             e = min(b, pairs[i][1])
             if (u, e) == pairs[i]:
                 whole.add(i)
@@ -94,7 +94,7 @@ def test_segments_partition_the_units_and_partials_meet_their_owner(split, case)
             u = e
         if last and last[2] < pairs[last[0]][1] and pairs[last[0]][0] >= a:
             i = last[0]
-            metas.append((i, c, 2 * c + (0 if pairs[i][0] == a else 1), split.parts(c, pairs[i][1], T, w)))
+            metas.append((i, c, 2 * c + (0 if pairs[i][0] == a else 1), split.parts(c, pairs[i][1], T, ctas)))
     assert at == T
     joined = set()
     for i, c, slot, count in metas:
