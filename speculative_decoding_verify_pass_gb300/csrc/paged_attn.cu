@@ -222,20 +222,19 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Wait bounded in time (2^31 cycles, about a second); one that gives up raises
-// `dead`, which ends every later one.  Inline: a call would fix the registers
-// that setmaxnreg moves.
+// Bounded wait; one that gives up raises `dead`.  Inline (a call would fix the
+// registers that setmaxnreg moves) and short: the roles' loops share one
+// instruction cache.  Callers stop waiting after a failure of theirs.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    do {
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 23); ++i)
         if (mbar_try_wait(bar, parity)) return true;
-    } while (!*dead && clock64() - t0 < (1ll << 31));
     *dead = 1;
     return false;
 }
 // After a failed wait: let what is in flight finish before the CTA ends.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
     for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) __nanosleep(64);
 }
 
@@ -374,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         dead = 0;
         first[0] = 0;
     }
+#pragma unroll 1
     for (int i = tid; i < RP; i += kThreads) {
         const int t = i / p.group;
         tok[i] = t;
@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         if (p.nseq > 64) {                      // more than one warp holds sequences
             if (lane == 31) warp_sum[warp] = inc;
             __syncthreads();
+#pragma unroll 1
             for (int w = 0; w < warp && w * 64 < p.nseq; ++w) run += warp_sum[w];
         }
 #pragma unroll
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (lane == 0) {
                 Walk w(p, first, begin, end);
                 Meta into = {}, from = {};
+#pragma unroll 1
                 while (w.next()) {
                     Seg s;
                     s.c0 = w.c0;
@@ -477,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             Ring<NV> vr;
             Ring<NQ> qr;
             bool ok = true;
+#pragma unroll 1
             for (int done = 0; done < n && ok;) {
                 const Seg s = take(false);
                 done += s.units;
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 const int held = (s.len + SPEC_PAGE - 1) / SPEC_PAGE;
                 const int* tab = p.tables + (size_t)s.q * p.table_pages;
                 int z0 = -1, z1 = -1;           // the lane's chunk: tensor-map rows of its two pages
+#pragma unroll 1
                 for (int k = 0; k < s.units; ++k) {
                     const int c = s.c0 + k;
                     if ((k & 31) == 0) {        // the next 32 chunks' pages, one chunk a lane
@@ -512,10 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     }
                     const int a0 = __shfl_sync(0xffffffffu, z0, k & 31), a1 = __shfl_sync(0xffffffffu, z1, k & 31);
                     const int pages = min(2, held - 2 * c);   // that exist (a bad one reads as zeros: z = -1)
-                    auto copy = [&](uint64_t* empty, uint32_t parity, uint64_t* full, uint8_t* dst, const CUtensorMap* map) {
-                        ok = ok && wait(empty, parity, deadp);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) return;
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        const int at = v ? vr.at : kr.at;
+                        uint64_t* full = v ? &v_full[at] : &k_full[at];
+                        ok = __all_sync(0xffffffffu, wait(v ? &v_empty[at] : &k_empty[at], (v ? vr.round : kr.round) ^ 1, deadp));
+                        if (!ok) break;
+                        uint8_t* dst = (v ? vslots : kslots) + at * L::kSlot;
+                        const CUtensorMap* map = v ? &p.mv : &p.mk;
                         if (elect_one()) {
                             mbar_arrive_expect_tx(full, pages > 0 ? (uint32_t)(pages * SPEC_PAGE * HD * 2) : 0u);
 #pragma unroll
@@ -525,17 +533,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             }
                         }
                         __syncwarp();
-                    };
-                    copy(&k_empty[kr.at], kr.round ^ 1, &k_full[kr.at], kslots + kr.at * L::kSlot, &p.mk);
-                    if (ok) kr.step();
-                    copy(&v_empty[vr.at], vr.round ^ 1, &v_full[vr.at], vslots + vr.at * L::kSlot, &p.mv);
-                    if (ok) vr.step();
+                        if (v) vr.step();
+                        else kr.step();
+                    }
                     if (!ok) break;
                 }
             }
             if (lane == 0 && *deadp) {          // every buffer's last copy, as far as one was issued
+#pragma unroll 1
                 for (int i = 0; i < NK; ++i) drain(&k_full[i], i < kr.at ? kr.round : kr.round ^ 1);
+#pragma unroll 1
                 for (int i = 0; i < NV; ++i) drain(&v_full[i], i < vr.at ? vr.round : vr.round ^ 1);
+#pragma unroll 1
                 for (int i = 0; i < NQ; ++i) drain(&q_full[i], i < qr.at ? qr.round : qr.round ^ 1);
             }
         } else if (warp == kScoreWarp) {
@@ -546,12 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 Ring<2> sb;
                 const uint32_t sa = smem_u32(kslots), qa = smem_u32(qs);
                 bool ok = true;
+#pragma unroll 1
                 for (int done = 0; done < n && ok;) {
                     const Seg s = take(true);
                     done += s.units;
                     ok = wait(&q_full[qr.at], qr.round, deadp) && !*deadp;
                     const uint32_t id = umma_idesc_bf16(128, (s.R + 15) & ~15);
                     const uint64_t dq = desc_sw128(qa + qr.at * L::kQ, 16, 1024);
+#pragma unroll 1
                     for (int k = 0; k < s.units && ok; ++k) {
                         ok = wait(&k_full[ks.at], ks.round, deadp) && wait(&s_empty[sb.at], sb.round ^ 1, deadp);
                         if (!ok) break;
@@ -582,12 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 const uint32_t sa = smem_u32(vslots), pa = smem_u32(ps);
                 bool ok = true;
                 int j = 0;                      // unit
+#pragma unroll 1
                 for (int done = 0, seg = 0; done < n && ok; ++seg) {
                     const Seg s = take(true);
                     done += s.units;
                     ok = wait(&o_empty[seg & 1], ((seg >> 1) & 1) ^ 1, deadp) && !*deadp;
                     // A = V^T and B = P^T, both MN-major
                     const uint32_t id = umma_idesc_bf16(128, kStack ? 2 * RP : (s.R + 15) & ~15) | (1u << 15) | (1u << 16);
+#pragma unroll 1
                     for (int k = 0; k < s.units && ok; ++k, ++j) {
                         ok = wait(&v_full[vs.at], vs.round, deadp) && wait(&p_full[pr.at], pr.round, deadp);
                         if (!ok) break;
@@ -630,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         int i = 0;                              // unit
         Ring<NV> vs;                            // slot of the next unit's V
         bool ok = true;
+#pragma unroll 1
         for (int done = 0, seg = 0; done < n; ++seg) {
             const Seg w = take(false);
             if (bar_any(bar, 128, *deadp != 0)) break;   // a wait gave up: nothing was listed (all of the warpgroup leaves)
@@ -641,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < NC / 2; ++j) l[j] = F2(0.f, 0.f);
             bool fresh = true;
+#pragma unroll 1
             for (int c = w.c0; c < w.c0 + w.units; ++c, ++i) {
                 const Ring<NV> v = vs;
                 vs.step();
@@ -651,7 +666,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 ok = ok && wait(&s_full[i & 1], (i >> 1) & 1, deadp);
                 tc_fence_after();
                 float s[NC];
-                auto scores = [&]() {           // the chunk's scores, -inf where a row does not see the key
+                // this thread's P^T buffer is free (and its rows' O^T complete) once their last product is
+                auto product_done = [&]() {
+                    ok = ok && wait(&p_empty[kStream ? i & 1 : 0], ((kStream ? i >> 1 : i) & 1) ^ 1, deadp);
+                };
+#pragma unroll 1
+                for (bool moved = false;; moved = true) {
+                    // the chunk's scores, -inf where a row does not see the key
 #pragma unroll
                     for (int j = 0; j < NC; j += kSpan)
                         if (j < rows) {
@@ -669,20 +690,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                                     if (kp > last0 + tok[col0 + j + e]) s[j + e] = -INFINITY;
                             }
                     }
-                };
-                scores();
-                if (fresh && rows > 0) {        // references: the scores of the chunk's first key
-                    if (key == 0) {
+                    if (rows <= 0) break;
+                    if (fresh) {                // references: the scores of the chunk's first key
+                        if (key == 0) {
 #pragma unroll
-                        for (int j = 0; j < NC; ++j) {
-                            const float m = s[j] * p.scale_log2;
-                            mine[col0 + j] = j >= rows ? -INFINITY : m > kNone ? -m : -kNone;   // rows past R weigh nothing
+                            for (int j = 0; j < NC; j += 4)
+                                *reinterpret_cast<float4*>(&mine[col0 + j]) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
                         }
+                        named_bar_sync(bar, 128);
+                        if (key < NC) {
+                            const float m = mine[col0 + key] * p.scale_log2;
+                            mine[col0 + key] = key >= rows ? -INFINITY : m > kNone ? -m : -kNone;   // rows past R weigh nothing
+                        }
+                        named_bar_sync(bar, 128);
                     }
-                    named_bar_sync(bar, 128);
-                }
-                float top[2] = {kNone, kNone};
-                auto exponents = [&]() {
+                    float top[2] = {kNone, kNone};
 #pragma unroll
                     for (int j0 = 0; j0 < NC; j0 += kSpan)
                         if (j0 < rows) {
@@ -694,63 +716,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                                 top[j / 4 & 1] = fmaxf(top[j / 4 & 1], fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
                             }
                         }
-                };
-                exponents();
-                // this thread's P^T buffer is free (and its rows' O^T complete) once their last product is
-                auto product_done = [&]() {
-                    ok = ok && wait(&p_empty[kStream ? i & 1 : 0], ((kStream ? i >> 1 : i) & 1) ^ 1, deadp);
-                };
-                if (rows > 0 && bar_any(bar, 128, fmaxf(top[0], top[1]) > kLimit)) {
-                    // the references move up to the chunk's maxima
+                    if (moved || !bar_any(bar, 128, fmaxf(top[0], top[1]) > kLimit)) break;
+                    // The references move up to the chunk's maxima, the sums and O^T
+                    // with them, and the scores are taken again.
                     product_done();
                     tc_fence_after();
-                    scores();
                     float (*const mx)[RP] = xl[par][gi];
+#pragma unroll 1
+                    for (int j = 0; j < NC && j < rows; j += 8) {
+                        float x[8];
+                        tmem_ld8_async(st + j, x);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < NC; ++j)
-                        if (j < rows) {
-                            const float m = warp_max_exact(s[j]);
-                            if (lane == 0) mx[qd][col0 + j] = m;
+                        for (int e = 0; e < 8; ++e) {
+                            const float m = warp_max_exact(masked && kp > last0 + tok[col0 + j + e] ? -INFINITY : x[e]);
+                            if (lane == 0) mx[qd][col0 + j + e] = m;
                         }
+                    }
                     named_bar_sync(bar, 128);
-                    auto moved = [&](int r) {   // a row's new reference
+                    if (key < NC) {             // one thread per row: the new reference, and what the old weights shrink by
+                        const int r = col0 + key;
                         const float m = fmaxf(fmaxf(mx[0][r], mx[1][r]), fmaxf(mx[2][r], mx[3][r])) * p.scale_log2;
-                        return fmaxf(-mine[r], m);
-                    };
-                    const int og = kStream ? par * 2 + wg : par;
-#pragma unroll
-                    for (int j = 0; j < NC; j += 8)
-                        if (j < rows) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int r = col0 + j + e;
-                                f[e] = j + e < rows ? ex2_approx(-mine[r] - moved(r)) : 0.f;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                float a, b;
-                                l[(j + e) / 2].get(a, b);
-                                l[(j + e) / 2] = F2(a * f[e], b * f[e + 1]);
-                            }
-                            if (!fresh) {
-#pragma unroll
-                                for (int part = 0; part < (kStack ? 2 : 1); ++part) {
-                                    const uint32_t at = lanes + 2 * RP + og * L::kO + part * RP + col0 + j;
-                                    float o[8];
-                                    tmem_ld8_async(at, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) o[e] *= f[e];
-                                    tmem_st8(at, o);
-                                }
-                                tmem_wait_st();
-                            }
-                        }
-                    named_bar_sync(bar, 128);   // everyone has read the old references
-                    if (key < rows && key < NC) mine[col0 + key] = -moved(col0 + key);
+                        const float old = -mine[r], now = key < rows ? fmaxf(old, m) : INFINITY;
+                        mine[r] = -now;
+                        mx[0][r] = key < rows ? ex2_approx(old - now) : 0.f;
+                    }
                     named_bar_sync(bar, 128);
-                    exponents();
+#pragma unroll
+                    for (int j = 0; j < NC; j += 2) {
+                        float x, y;
+                        l[j / 2].get(x, y);
+                        l[j / 2] = F2(x * mx[0][col0 + j], y * mx[0][col0 + j + 1]);
+                    }
+                    if (!fresh) {
+                        const uint32_t ot = lanes + 2 * RP + (kStream ? par * 2 + wg : par) * L::kO + col0;
+#pragma unroll 1
+                        for (int j = 0; j < (kStack ? 2 * NC : NC); j += 8)   // stacked: the low part's columns follow
+                            if ((kStack ? j & (NC - 1) : j) < rows) {
+                                float o[8];
+                                tmem_ld8_async(ot + j, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) o[e] *= mx[0][col0 + (j & (NC - 1)) + e];
+                                tmem_st8(ot + j, o);
+                            }
+                        tmem_wait_st();
+                    }
+                    fresh = false;
+                    named_bar_sync(bar, 128);   // everyone has read mx
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -789,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     ok = ok && wait(&v_full[v.at], v.round, deadp);
                     uint8_t* vt = vslots + v.at * L::kSlot;
                     const int from = max(0, last0 + 1 - c * kChunk), live = w.len - c * kChunk;
+#pragma unroll 1
                     for (int t = from * (HD / 8) + key; t < kChunk * (HD / 8); t += 128) {
                         const int r = t / (HD / 8), d8 = t % (HD / 8);
                         uint4* at = reinterpret_cast<uint4*>(vt + (d8 >> 3) * kChunk * 128 + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
@@ -844,6 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const int qd = warp & 3, d = qd * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         int i = 0;                              // the segment's first unit
+#pragma unroll 1
         for (int done = 0, seg = 0; done < n; ++seg) {
             const Seg w = take(false);
             if (bar_any(kResultBar, 128, *deadp != 0)) break;
@@ -883,37 +898,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const long long out0 = (long long)w.row0 * p.out_stride + (long long)w.head * p.group * HD + d;
 #pragma unroll 1
             for (int j = 0; j < w.R; j += 8) {
-                float o[8], x[8];
+                // the row's O^T (both parts) of the first warpgroup, and of the other
+                float o[8], x[8], y[8], z[8];
                 const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j;
+                const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j;
                 tmem_ld8_async(at, o);
-                if (kStack) {
-                    tmem_ld8_async(at + RP, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] += x[e];
-                } else {
-                    tmem_wait_ld();
-                }
-                float2 f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = weight[par][j + e];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= f[e].x;
+                if (kStack) tmem_ld8_async(at + RP, x);
                 if (two) {
-                    const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j;
-                    tmem_ld8_async(bt, x);
-                    tmem_wait_ld();
+                    tmem_ld8_async(bt, y);
+                    if (kStack) tmem_ld8_async(bt + RP, z);
+                }
+                tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
-                    if (kStack) {
-                        tmem_ld8_async(bt + RP, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] += f[e].y * x[e];
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = weight[par][j + e];
+                    o[e] = (kStack ? o[e] + x[e] : o[e]) * f.x;
+                    if (two) o[e] += (kStack ? y[e] + z[e] : y[e]) * f.y;
                 }
                 if (d < HD) {
                     if (bad)
+#pragma unroll 1
                         for (int t = max(last0 + 1, w.c0 * kChunk); t < min(w.len, (w.c0 + w.units) * kChunk); ++t) {
                             const int page = p.tables[(size_t)w.q * p.table_pages + t / SPEC_PAGE];
                             if (page < 0 || page >= p.num_pages) continue;

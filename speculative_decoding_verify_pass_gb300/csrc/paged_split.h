@@ -55,6 +55,9 @@ struct Deal {
 // The sequence that holds unit u < first[nseq]: the last q with first[q] <= u.
 SPLIT_HD int sequence_of(const int* first, int nseq, int u) {
     int lo = 0, hi = nseq;
+#ifdef __CUDACC__
+#pragma unroll 1
+#endif
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (first[mid] <= u) lo = mid;
