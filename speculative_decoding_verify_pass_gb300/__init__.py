@@ -10,6 +10,7 @@ raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -326,64 +327,63 @@ def spec_accept_from_logits_noalloc(d_logits, d_block, d_argmax, d_accept_len, s
 # ----------------------------------------------------------------------------
 # A paged cache shared by many sequences (no handle; the current torch stream)
 # ----------------------------------------------------------------------------
+# A call's host side is short (these calls run in serving loops, once per layer):
+# one pass over the arguments, the raw stream, no tensor but the result and its scratch.
 def _refuse(msg):
     raise SpecError(SPEC_ERR_INVALID_ARG, msg)
 
 
-def _cuda_i32(name, t, need=0):
-    """Data pointer of a contiguous int32 CUDA tensor of at least need entries."""
+def _current(t):
+    """Index of the current CUDA device, which must hold t."""
     import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse("the buffers must be tensors on the current CUDA device")
+    return dev
+
+
+def _i32(name, t, need, dev):
+    """Data pointer of a contiguous int32 tensor of at least need entries on device dev."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous()
             and t.numel() >= need):
-        _refuse("%s must be a contiguous int32 CUDA tensor of at least %d entries" % (name, need))
+        _refuse("%s must be a contiguous int32 tensor of at least %d entries on the current CUDA device" % (name, need))
     return t.data_ptr()
 
 
-def _rows_bf16(name, t, heads=None, head_dim=None):
-    """(pointer, row stride) of a bf16 CUDA tensor [rows][heads][head_dim] whose
-    rows are contiguous; the rows may lie any distance apart."""
+def _rows_bf16(name, t, rows, heads, head_dim, dev):
+    """(pointer, row stride) of a bf16 tensor [rows][heads][head_dim] whose rows
+    are contiguous; the rows may lie any distance apart."""
     import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and t.dim() == 3):
-        _refuse("%s must be a 3-D bfloat16 CUDA tensor" % name)
-    rows, h, d = t.shape
-    if (heads is not None and h != heads) or (head_dim is not None and d != head_dim):
-        _refuse("%s must be [rows][%s][%s]" % (name, heads, head_dim))
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev
+            and t.shape == (rows, heads, head_dim)):
+        _refuse("%s must be a bfloat16 tensor [%d][%d][%d] on the current CUDA device" % (name, rows, heads, head_dim))
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+    if (s2 != 1 and head_dim > 1) or (s1 != head_dim and heads > 1):
         _refuse("the rows of %s must be contiguous [heads][head_dim] blocks" % name)
-    return t.data_ptr(), s0 if rows > 1 else h * d
+    return t.data_ptr(), s0 if rows > 1 else heads * head_dim
 
 
-def _pools(d_kpool, d_vpool):
-    """(pages, kv heads, head_dim) of a key and a value pool."""
+def _pools(k, v, dev):
+    """Shape [pages, kv heads, SPEC_PAGE, head_dim] of a key and a value pool."""
     import torch
-    for name, t in (("d_kpool", d_kpool), ("d_vpool", d_vpool)):
-        if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and t.dim() == 4
-                and t.shape[2] == SPEC_PAGE and t.is_contiguous()):
-            _refuse("%s must be a contiguous bfloat16 CUDA tensor [pages][kv heads][%d][head_dim]" % (name, SPEC_PAGE))
-    if d_kpool.shape != d_vpool.shape:
-        _refuse("d_kpool and d_vpool must have the same shape")
-    pages, heads, _, hd = d_kpool.shape
-    return pages, heads, hd
-
-
-def _same_device(first, *others):
-    """Every buffer on the current device (the calls run there); returns its
-    raw current stream."""
-    import torch
-    dev = first.device.index
-    if dev != torch.cuda.current_device():
-        _refuse("the buffers must be on the current CUDA device")
-    for t in others:
-        if t is not None and t.device.index != dev:
-            _refuse("the buffers must all be on the current CUDA device")
-    return torch.cuda.current_stream(dev).cuda_stream
+    for name, t in (("d_kpool", k), ("d_vpool", v)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.dim() == 4
+                and t.is_contiguous()):
+            _refuse("%s must be a contiguous bfloat16 tensor [pages][kv heads][%d][head_dim] on the current CUDA device"
+                    % (name, SPEC_PAGE))
+    shape = k.shape
+    if shape[2] != SPEC_PAGE or v.shape != shape:
+        _refuse("d_kpool and d_vpool must both be [pages][kv heads][%d][head_dim]" % SPEC_PAGE)
+    return shape
 
 
 def spec_pages_init(d_pool):
     """All pages of d_pool (int32 [SPEC_POOL_HEADER + pages]) become free."""
-    ptr = _cuda_i32("d_pool", d_pool, SPEC_POOL_HEADER + 1)
-    _check(library().spec_pages_init(ptr, d_pool.numel() - SPEC_POOL_HEADER, _same_device(d_pool)))
+    import torch
+    dev = _current(d_pool)
+    ptr = _i32("d_pool", d_pool, SPEC_POOL_HEADER + 1, dev)
+    _check(library().spec_pages_init(ptr, d_pool.numel() - SPEC_POOL_HEADER, torch._C._cuda_getCurrentRawStream(dev)))
 
 
 def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots):
@@ -391,41 +391,48 @@ def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots
     int32 [nseq][table_pages], lengths, keep and add int32 [nseq]; writes
     row_start [nseq + 1] and the new rows' slots.  Errors that only the device
     can see land in d_pool[SPEC_POOL_ERROR]."""
-    pool = _cuda_i32("d_pool", d_pool, SPEC_POOL_HEADER + 1)
-    tables = _cuda_i32("d_tables", d_tables)
+    import torch
+    dev = _current(d_pool)
+    tables = _i32("d_tables", d_tables, 0, dev)
     if d_tables.dim() != 2:
         _refuse("d_tables must be [nseq][table_pages]")
     nseq, width = d_tables.shape
-    args = (_cuda_i32("d_len", d_len, nseq), _cuda_i32("d_keep", d_keep, nseq), _cuda_i32("d_add", d_add, nseq), nseq,
-            _cuda_i32("d_row_start", d_row_start, nseq + 1), _cuda_i32("d_slots", d_slots), d_slots.numel())
-    st = _same_device(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots)
-    _check(library().spec_pages_step(pool, d_pool.numel() - SPEC_POOL_HEADER, tables, width, *args, st))
+    _check(library().spec_pages_step(
+        _i32("d_pool", d_pool, SPEC_POOL_HEADER + 1, dev), d_pool.numel() - SPEC_POOL_HEADER, tables, width,
+        _i32("d_len", d_len, nseq, dev), _i32("d_keep", d_keep, nseq, dev), _i32("d_add", d_add, nseq, dev), nseq,
+        _i32("d_row_start", d_row_start, nseq + 1, dev), _i32("d_slots", d_slots, 0, dev), d_slots.numel(),
+        torch._C._cuda_getCurrentRawStream(dev)))
 
 
 def spec_paged_append(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_error=None):
     """Write the rows of d_k and d_v (bf16 [rows][kv heads][head_dim], rows any
     distance apart) at their slots; only rows below the device int32
     d_row_count (None: all)."""
-    pages, heads, hd = _pools(d_kpool, d_vpool)
-    k, ks = _rows_bf16("d_k", d_k, heads, hd)
-    v, vs = _rows_bf16("d_v", d_v, heads, hd)
-    rows = d_k.shape[0]
-    if d_v.shape[0] != rows:
-        _refuse("d_k and d_v must have the same number of rows")
-    slots = _cuda_i32("d_slots", d_slots, rows)
-    count = None if d_row_count is None else _cuda_i32("d_row_count", d_row_count, 1)
-    err = None if d_error is None else _cuda_i32("d_error", d_error, 1)
-    st = _same_device(d_kpool, d_vpool, d_k, d_v, d_slots, d_row_count, d_error)
-    _check(library().spec_paged_append(k, ks, v, vs, slots, count, rows, heads, hd, d_kpool.data_ptr(),
-                                       d_vpool.data_ptr(), pages, err, st))
+    import torch
+    dev = _current(d_k)
+    pages, heads, _, hd = _pools(d_kpool, d_vpool, dev)
+    rows = d_k.shape[0] if d_k.dim() else 0
+    k, ks = _rows_bf16("d_k", d_k, rows, heads, hd, dev)
+    v, vs = _rows_bf16("d_v", d_v, rows, heads, hd, dev)
+    _check(library().spec_paged_append(
+        k, ks, v, vs, _i32("d_slots", d_slots, rows, dev),
+        None if d_row_count is None else _i32("d_row_count", d_row_count, 1, dev), rows, heads, hd, d_kpool.data_ptr(),
+        d_vpool.data_ptr(), pages, None if d_error is None else _i32("d_error", d_error, 1, dev),
+        torch._C._cuda_getCurrentRawStream(dev)))
 
 
 def spec_paged_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
-    """Bytes of scratch a spec_paged_attention call with these heads needs."""
+    """Bytes of scratch a spec_paged_attention call with these heads needs on
+    the current device."""
     out = ctypes.c_size_t(0)
     _check(library().spec_paged_attention_workspace(int(n_heads), int(n_kv_heads), int(head_dim), int(max_new),
                                                     ctypes.byref(out)))
     return int(out.value)
+
+
+@functools.lru_cache(maxsize=256)
+def _work_bytes(dev, n_heads, n_kv_heads, head_dim, max_new):
+    return spec_paged_attention_workspace(n_heads, n_kv_heads, head_dim, max_new)
 
 
 def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, max_new, scale=None, d_out=None,
@@ -435,28 +442,30 @@ def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, ma
     every sequence are then unset).  scale defaults to head_dim ** -0.5; d_work
     (a uint8 tensor) to scratch from torch's allocator."""
     import torch
-    pages, hkv, hd = _pools(d_kpool, d_vpool)
-    q, qs = _rows_bf16("d_q", d_q, None, hd)
+    dev = _current(d_q)
+    pages, hkv, _, hd = _pools(d_kpool, d_vpool, dev)
+    if d_q.dim() != 3:
+        _refuse("d_q must be [rows][heads][head_dim]")
     rows, hq, _ = d_q.shape
-    tables = _cuda_i32("d_tables", d_tables)
+    q, qs = _rows_bf16("d_q", d_q, rows, hq, hd, dev)
+    tables = _i32("d_tables", d_tables, 0, dev)
     if d_tables.dim() != 2:
         _refuse("d_tables must be [nseq][table_pages]")
     nseq, width = d_tables.shape
+    max_new = int(max_new)
     if d_out is None:
         d_out = torch.empty((rows, hq, hd), dtype=torch.bfloat16, device=d_q.device)
-    out, os_ = _rows_bf16("d_out", d_out, hq, hd)
-    if d_out.shape[0] != rows:
-        _refuse("d_out must have as many rows as d_q")
-    args = (_cuda_i32("d_row_start", d_row_start, nseq + 1), _cuda_i32("d_len", d_len, nseq), tables, width, nseq, rows,
-            int(max_new), hq, hkv, hd, hd ** -0.5 if scale is None else float(scale))
-    err = None if d_error is None else _cuda_i32("d_error", d_error, 1)
-    st = _same_device(d_q, d_out, d_kpool, d_vpool, d_row_start, d_len, d_tables, d_error, d_work)
+    out, os_ = _rows_bf16("d_out", d_out, rows, hq, hd, dev)
     if d_work is None:
-        d_work = torch.empty(spec_paged_attention_workspace(hq, hkv, hd, max_new), dtype=torch.uint8, device=d_q.device)
-    elif not (d_work.dtype is torch.uint8 and d_work.is_cuda and d_work.is_contiguous()):
-        _refuse("d_work must be a contiguous uint8 CUDA tensor")
-    _check(library().spec_paged_attention(q, qs, *args, d_kpool.data_ptr(), d_vpool.data_ptr(), pages, out, os_, err,
-                                          d_work.data_ptr(), d_work.numel(), st))
+        d_work = torch.empty(_work_bytes(dev, hq, hkv, hd, max_new), dtype=torch.uint8, device=d_q.device)
+    elif not (isinstance(d_work, torch.Tensor) and d_work.dtype is torch.uint8 and d_work.get_device() == dev
+              and d_work.is_contiguous()):
+        _refuse("d_work must be a contiguous uint8 tensor on the current CUDA device")
+    _check(library().spec_paged_attention(
+        q, qs, _i32("d_row_start", d_row_start, nseq + 1, dev), _i32("d_len", d_len, nseq, dev), tables, width, nseq, rows,
+        max_new, hq, hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
+        out, os_, None if d_error is None else _i32("d_error", d_error, 1, dev), d_work.data_ptr(), d_work.numel(),
+        torch._C._cuda_getCurrentRawStream(dev)))
     return d_out
 
 
