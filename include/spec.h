@@ -502,9 +502,10 @@ spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v
  *   max_new    the most rows of any sequence, 1 or more: it picks the tile
  *              height and is no bound (larger blocks are right, only slower);
  *   d_work     work_bytes of scratch, 256-byte aligned, at least what
- *              spec_paged_attention_workspace says for the same heads and
- *              max_new.  Its contents need not be set and mean nothing between
- *              calls; calls that may run at the same time need one each.
+ *              spec_paged_attention_workspace says for the same heads, max_new
+ *              and table_pages on the same device (0 for short tables: d_work
+ *              may then be NULL).  Its contents need not be set and mean nothing
+ *              between calls; calls that may run at the same time need one each.
  * Values behind a sequence's length are never used, whatever they are (NaN
  * too), nor is a position that a row may not see.  A visible value that is
  * infinite or NaN makes that dimension of the rows that see it non-finite.
@@ -518,7 +519,7 @@ spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v
  * query heads per kv head; scale positive and finite; 0 <= nseq <=
  * SPEC_MAX_SEQS (nseq or rows 0: nothing is done). */
 spec_status spec_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
-                                           size_t* out_bytes);
+                                           int32_t table_pages, size_t* out_bytes);
 spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_t* d_row_start, const int32_t* d_len,
                                  const int32_t* d_tables, int32_t table_pages, int32_t nseq, int32_t rows,
                                  int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale,

@@ -119,7 +119,7 @@ def library():
         "spec_pages_init": [vp, i32, vp],
         "spec_pages_step": [vp, i32, vp, i32, vp, vp, vp, i32, vp, vp, i32, vp],
         "spec_paged_append": [vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp],
-        "spec_paged_attention_workspace": [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "spec_paged_attention_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "spec_paged_attention": [vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32,
                                  vp, i64, vp, vp, ctypes.c_size_t, vp],
     }
@@ -421,18 +421,18 @@ def spec_paged_append(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_error=
         torch._C._cuda_getCurrentRawStream(dev)))
 
 
-def spec_paged_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
-    """Bytes of scratch a spec_paged_attention call with these heads needs on
-    the current device."""
+def spec_paged_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int, table_pages: int) -> int:
+    """Bytes of scratch a spec_paged_attention call with these heads and table
+    width needs on the current device."""
     out = ctypes.c_size_t(0)
     _check(library().spec_paged_attention_workspace(int(n_heads), int(n_kv_heads), int(head_dim), int(max_new),
-                                                    ctypes.byref(out)))
+                                                    int(table_pages), ctypes.byref(out)))
     return int(out.value)
 
 
 @functools.lru_cache(maxsize=256)
-def _work_bytes(dev, n_heads, n_kv_heads, head_dim, max_new):
-    return spec_paged_attention_workspace(n_heads, n_kv_heads, head_dim, max_new)
+def _work_bytes(dev, n_heads, n_kv_heads, head_dim, max_new, table_pages):
+    return spec_paged_attention_workspace(n_heads, n_kv_heads, head_dim, max_new, table_pages)
 
 
 def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, max_new, scale=None, d_out=None,
@@ -456,15 +456,21 @@ def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, ma
     if d_out is None:
         d_out = torch.empty((rows, hq, hd), dtype=torch.bfloat16, device=d_q.device)
     out, os_ = _rows_bf16("d_out", d_out, rows, hq, hd, dev)
+    work, work_bytes = None, 0
     if d_work is None:
-        d_work = torch.empty(_work_bytes(dev, hq, hkv, hd, max_new), dtype=torch.uint8, device=d_q.device)
+        work_bytes = _work_bytes(dev, hq, hkv, hd, max_new, width)
+        if work_bytes:
+            d_work = torch.empty(work_bytes, dtype=torch.uint8, device=d_q.device)
+            work = d_work.data_ptr()
     elif not (isinstance(d_work, torch.Tensor) and d_work.dtype is torch.uint8 and d_work.get_device() == dev
               and d_work.is_contiguous()):
         _refuse("d_work must be a contiguous uint8 tensor on the current CUDA device")
+    else:
+        work, work_bytes = d_work.data_ptr(), d_work.numel()
     _check(library().spec_paged_attention(
         q, qs, _i32("d_row_start", d_row_start, nseq + 1, dev), _i32("d_len", d_len, nseq, dev), tables, width, nseq, rows,
         max_new, hq, hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
-        out, os_, None if d_error is None else _i32("d_error", d_error, 1, dev), d_work.data_ptr(), d_work.numel(),
+        out, os_, None if d_error is None else _i32("d_error", d_error, 1, dev), work, work_bytes,
         torch._C._cuda_getCurrentRawStream(dev)))
     return d_out
 

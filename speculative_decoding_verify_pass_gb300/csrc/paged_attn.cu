@@ -56,7 +56,7 @@ constexpr int kSegs = 4;                    // segments listed ahead
 
 // A segment, as the roles need it.
 struct Seg {
-    int c0, units;              // first chunk, number of chunks
+    int c0, units;              // first chunk, number of chunks (0: the list ends)
     int R;                      // rows
     int last0;                  // last position that the first token sees
     int len;                    // of the sequence
@@ -82,6 +82,7 @@ struct PagedParams {
     CUtensorMap mq, mk, mv;
     const int *row_start, *len, *tables;
     int table_pages, nseq, rows, hq, hkv, group, tokens;
+    int whole;                  // pairs are not split: a CTA takes those that begin in its range
     float scale_log2;
     const uint16_t* vpool;
     int num_pages;
@@ -260,7 +261,20 @@ struct Walk {
 
     __device__ Walk(const PagedParams& pp, const int* f, int begin, int e) : p(pp), first(f), u(begin), end(e) {}
     __device__ __forceinline__ bool next() {
-        if (u >= end) return false;
+        for (;;) {
+            if (u >= end) return false;
+            find();
+            if (!p.whole || c0 == 0) break;
+            u += chunks - c0;   // begins in another CTA's range, which takes it
+        }
+        c1 = p.whole ? chunks : min(chunks, c0 + end - u);
+        R = min(p.tokens, rows - block * p.tokens) * p.group;
+        u += c1 - c0;
+        ++seg;
+        return true;
+    }
+    // where unit u lies
+    __device__ __forceinline__ void find() {
         if (q < 0 || u >= q1) {
             q = split::sequence_of(first, p.nseq, u);
             q0 = first[q];
@@ -274,11 +288,6 @@ struct Walk {
         block = pair / p.hkv;
         head = pair - block * p.hkv;
         c0 = u - q0 - pair * chunks;
-        c1 = min(chunks, c0 + end - u);
-        R = min(p.tokens, rows - block * p.tokens) * p.group;
-        u += c1 - c0;
-        ++seg;
-        return true;
     }
     __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
     // last position that the block's first token sees
@@ -432,7 +441,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     const uint32_t tmem = tmem_base;
     const split::Deal deal(total, gridDim.x);
     const int begin = deal.begin(blockIdx.x), end = deal.begin(blockIdx.x + 1);
-    const int n = end - begin;                  // units
     volatile int* deadp = &dead;
     Ring<kSegs> sr;                             // every role's place in the list of segments
     auto take = [&](bool one) {                 // the next segment; `one`: this thread alone stands for its warp
@@ -452,8 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 Walk w(p, first, begin, end);
                 Meta into = {}, from = {};
 #pragma unroll 1
-                while (w.next()) {
-                    Seg s;
+                for (bool more = true; more;) {
+                    more = w.next();
+                    Seg s = {};
+                    if (!more) {                // the list ends
+                        if (!wait(&seg_empty[sr.at], sr.round ^ 1, deadp)) break;
+                        segs[sr.at] = s;
+                        mbar_arrive(&seg_full[sr.at]);
+                        break;
+                    }
                     s.c0 = w.c0;
                     s.units = w.c1 - w.c0;
                     s.R = w.R;
@@ -469,9 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     sr.step();
                     if (w.seg == 0 && w.c0 > 0) into = w.meta(deal);
                 }
-                if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(deal);
-                p.meta[2 * blockIdx.x] = into;
-                p.meta[2 * blockIdx.x + 1] = from;
+                if (!p.whole) {
+                    if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(deal);
+                    p.meta[2 * blockIdx.x] = into;
+                    p.meta[2 * blockIdx.x + 1] = from;
+                }
             }
         } else if (warp == kLoadWarp) {
             // ---------------- TMA copies (one elected lane issues; the lanes look up pages) ----------------
@@ -480,11 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             Ring<NQ> qr;
             bool ok = true;
 #pragma unroll 1
-            for (int done = 0; done < n && ok;) {
+            for (;;) {
                 const Seg s = take(false);
-                done += s.units;
+                ok = __all_sync(0xffffffffu, !*deadp);
+                if (!ok || s.units == 0) break;
                 uint64_t* qf = &q_full[qr.at];
-                ok = __all_sync(0xffffffffu, wait(&q_empty[qr.at], qr.round ^ 1, deadp) && !*deadp);
+                ok = __all_sync(0xffffffffu, wait(&q_empty[qr.at], qr.round ^ 1, deadp));
                 if (!ok) break;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(qf, (uint32_t)(p.tokens * p.group * HD * 2));
@@ -538,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     }
                     if (!ok) break;
                 }
+                if (!ok) break;
             }
             if (lane == 0 && *deadp) {          // every buffer's last copy, as far as one was issued
 #pragma unroll 1
@@ -556,10 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 const uint32_t sa = smem_u32(kslots), qa = smem_u32(qs);
                 bool ok = true;
 #pragma unroll 1
-                for (int done = 0; done < n && ok;) {
+                while (ok) {
                     const Seg s = take(true);
-                    done += s.units;
-                    ok = wait(&q_full[qr.at], qr.round, deadp) && !*deadp;
+                    ok = !*deadp;
+                    if (!ok || s.units == 0) break;
+                    ok = wait(&q_full[qr.at], qr.round, deadp);
                     const uint32_t id = umma_idesc_bf16(128, (s.R + 15) & ~15);
                     const uint64_t dq = desc_sw128(qa + qr.at * L::kQ, 16, 1024);
 #pragma unroll 1
@@ -594,10 +614,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 bool ok = true;
                 int j = 0;                      // unit
 #pragma unroll 1
-                for (int done = 0, seg = 0; done < n && ok; ++seg) {
+                for (int seg = 0; ok; ++seg) {
                     const Seg s = take(true);
-                    done += s.units;
-                    ok = wait(&o_empty[seg & 1], ((seg >> 1) & 1) ^ 1, deadp) && !*deadp;
+                    ok = !*deadp;
+                    if (!ok || s.units == 0) break;
+                    ok = wait(&o_empty[seg & 1], ((seg >> 1) & 1) ^ 1, deadp);
                     // A = V^T and B = P^T, both MN-major
                     const uint32_t id = umma_idesc_bf16(128, kStack ? 2 * RP : (s.R + 15) & ~15) | (1u << 15) | (1u << 16);
 #pragma unroll 1
@@ -644,10 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         Ring<NV> vs;                            // slot of the next unit's V
         bool ok = true;
 #pragma unroll 1
-        for (int done = 0, seg = 0; done < n; ++seg) {
+        for (int seg = 0;; ++seg) {
             const Seg w = take(false);
-            if (bar_any(bar, 128, *deadp != 0)) break;   // a wait gave up: nothing was listed (all of the warpgroup leaves)
-            done += w.units;
+            if (bar_any(bar, 128, *deadp != 0) || w.units == 0) break;   // after a wait that gave up, all of the warpgroup leaves
             const int par = seg & 1, last0 = w.last0, rows = w.R - col0;   // live rows of this thread
             float* const mine = nref[par][gi];
             ok = ok && wait(&l_empty[par], ((seg >> 1) & 1) ^ 1, deadp);   // the results of two segments ago have been read
@@ -859,10 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         int i = 0;                              // the segment's first unit
 #pragma unroll 1
-        for (int done = 0, seg = 0; done < n; ++seg) {
+        for (int seg = 0;; ++seg) {
             const Seg w = take(false);
-            if (bar_any(kResultBar, 128, *deadp != 0)) break;
-            done += w.units;
+            if (bar_any(kResultBar, 128, *deadp != 0) || w.units == 0) break;
             const int par = seg & 1, last0 = w.last0;
             const int ga = kStream ? i & 1 : 0; // the warpgroup of the first unit; the other has none in a segment of one
             const bool two = kStream && w.units > 1, whole = w.slot < 0;
@@ -1154,7 +1173,7 @@ cudaError_t run(PagedParams& p, int ctas, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<HD, RP>::kBytes);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
-    if ((e = launch(fn, dim3((unsigned)ctas), kThreads, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess) return e;
+    if ((e = launch(fn, dim3((unsigned)ctas), kThreads, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess || p.whole) return e;
     int rp = RP;
     void* jargs[] = {&p, &rp};
     return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, RP <= 32 ? 1 : RP / 32), 32 * kJoinWarps, 0, s, jargs);
@@ -1168,9 +1187,14 @@ extern "C" {
 using namespace sv;
 
 spec_status spec_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
-                                           size_t* out_bytes) {
+                                           int32_t table_pages, size_t* out_bytes) {
     if (!out_bytes) return bad("spec_paged_attention_workspace: null pointer");
     if (const char* e = head_error(n_heads, n_kv_heads, head_dim, max_new)) return bad(e);
+    if (table_pages < 1 || table_pages > SPEC_MAX_TABLE) return bad("spec_paged_attention: table_pages must be in 1..1048576");
+    if (split::whole_pairs(table_pages)) {
+        *out_bytes = 0;
+        return SPEC_OK;
+    }
     const int sms = current_sms();
     if (!sms) {
         set_last_error("spec_paged_attention_workspace: no current CUDA device");
@@ -1198,7 +1222,8 @@ spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_
         out_stride >= (1ll << 38))
         return bad("spec_paged_attention: row strides must be multiples of 8, at least n_heads * head_dim and below 2^38");
     if (nseq == 0 || rows == 0) return SPEC_OK;
-    if (!d_q || !d_row_start || !d_len || !d_tables || !d_kpool || !d_vpool || !d_out || !d_work)
+    const bool whole = split::whole_pairs(table_pages);
+    if (!d_q || !d_row_start || !d_len || !d_tables || !d_kpool || !d_vpool || !d_out || (!whole && !d_work))
         return bad("spec_paged_attention: null pointer");
     if (misaligned(d_q, 16) || misaligned(d_out, 16) || misaligned(d_kpool, 16) || misaligned(d_vpool, 16))
         return bad("spec_paged_attention: queries, output and pools must be 16-byte aligned");
@@ -1210,14 +1235,14 @@ spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_
     const int64_t pairs = ((int64_t)nseq + rows / tokens) * n_kv_heads;
     if (pairs > 0x7fffffffll / ((table_pages + 1) / 2))
         return bad("spec_paged_attention: too much work for one call ((nseq + rows / tile) * n_kv_heads * table_pages / 2)");
-    if (work_bytes < Work(1, rp, head_dim).bytes) return bad("spec_paged_attention: work_bytes is less than these heads need");
+    if (!whole && work_bytes < Work(1, rp, head_dim).bytes) return bad("spec_paged_attention: work_bytes is less than these heads need");
     const int sms = current_sms();
     if (!sms) {
         set_last_error("spec_paged_attention: no current CUDA device");
         return SPEC_ERR_CUDA;
     }
     const Work work(sms, rp, head_dim);
-    if (work_bytes < work.bytes) return bad("spec_paged_attention: work_bytes is less than these heads need");
+    if (!whole && work_bytes < work.bytes) return bad("spec_paged_attention: work_bytes is less than these heads need");
     if (!encode_fn()) {
         set_last_error("spec_paged_attention: the driver has no cuTensorMapEncodeTiled");
         return SPEC_ERR_CUDA;
@@ -1240,6 +1265,7 @@ spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_
     p.hkv = n_kv_heads;
     p.group = group;
     p.tokens = tokens;
+    p.whole = whole;
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.vpool = static_cast<const uint16_t*>(d_vpool);
     p.num_pages = num_pages;

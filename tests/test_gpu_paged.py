@@ -469,8 +469,9 @@ def test_attention_same_call_same_bits():
 def test_attention_workspace_from_the_caller_and_its_refusals():
     torch = torch_cuda()
     sv = sv_()
-    c = Case([700], [4], 16, 2, 128, seed=16)
-    need = sv.spec_paged_attention_workspace(16, 2, 128, 4)
+    c = Case([2700], [4], 16, 2, 128, seed=16)
+    need = sv.spec_paged_attention_workspace(16, 2, 128, 4, c.d["tables"].shape[1])
+    assert need > 0
     work = torch.full((need,), 255, dtype=torch.uint8, device="cuda")    # NaN bits
     c.check(c.run(d_work=work))
     for bad in (work[:need - 1], work.float()):

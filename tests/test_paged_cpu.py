@@ -57,7 +57,7 @@ def test_paged_append_refusals(lib, over, word):
                                        a["hd"], a["kpool"], a["vpool"], a["pages"], a["err"], None), word)
 
 
-ATTN = dict(q=P, qs=1024, start=P, length=P, tables=P, width=4, nseq=2, rows=3, max_new=2, hq=8, hkv=2, hd=128,
+ATTN = dict(q=P, qs=1024, start=P, length=P, tables=P, width=40, nseq=2, rows=3, max_new=2, hq=8, hkv=2, hd=128,
             scale=0.1, kpool=P, vpool=P, pages=8, out=P, os=1024, err=None, work=P, wbytes=1 << 30)
 
 
@@ -82,11 +82,13 @@ def test_paged_attention_refusals(lib, over, word):
 
 def test_paged_attention_workspace_refusals(lib):
     out = ctypes.c_size_t(7)
-    refused(lib, lib.spec_paged_attention_workspace(8, 2, 128, 1, None), "null")
-    refused(lib, lib.spec_paged_attention_workspace(8, 3, 128, 1, ctypes.byref(out)), "multiple")
-    refused(lib, lib.spec_paged_attention_workspace(8, 2, 80, 1, ctypes.byref(out)), "head_dim")
-    refused(lib, lib.spec_paged_attention_workspace(8, 2, 128, 0, ctypes.byref(out)), "max_new")
+    refused(lib, lib.spec_paged_attention_workspace(8, 2, 128, 1, 40, None), "null")
+    refused(lib, lib.spec_paged_attention_workspace(8, 3, 128, 1, 40, ctypes.byref(out)), "multiple")
+    refused(lib, lib.spec_paged_attention_workspace(8, 2, 80, 1, 40, ctypes.byref(out)), "head_dim")
+    refused(lib, lib.spec_paged_attention_workspace(8, 2, 128, 0, 40, ctypes.byref(out)), "max_new")
+    refused(lib, lib.spec_paged_attention_workspace(8, 2, 128, 1, 0, ctypes.byref(out)), "table_pages")
     assert out.value == 7
+    assert lib.spec_paged_attention_workspace(8, 2, 128, 1, 16, ctypes.byref(out)) == 0 and out.value == 0
 
 
 def test_nothing_to_do_is_no_error(lib):

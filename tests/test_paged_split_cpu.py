@@ -109,6 +109,21 @@ def test_segments_partition_the_units_and_partials_meet_their_owner(split, case)
     assert len(whole) + len(metas) == len(pairs)
 
 
+@pytest.mark.parametrize("case", CASES + [random_case(random.Random(i)) for i in range(12)], ids=lambda c: "%dx%d" % (len(c[0]), c[2]))
+def test_whole_pairs_are_each_taken_by_the_cta_they_begin_in(split, case):
+    lens, rows, hkv, tokens, ctas = case
+    starts, at = [], 0
+    for n, m in zip(lens, rows):
+        for _ in range(split.blocks(m, tokens) * hkv):
+            starts.append(at)
+            at += split.chunks(n)
+    taken = []
+    for c in range(ctas):
+        a, b = split.begin(c, at, ctas), split.begin(c + 1, at, ctas)
+        taken += [u for u in starts if a <= u < b]
+    assert taken == starts
+
+
 def test_tile_rows(split):
     for g in range(1, 129):
         for n in (1, 2, 3, 8, 16, 17, 1000, 2 ** 31 - 1):
