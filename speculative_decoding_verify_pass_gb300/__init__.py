@@ -327,63 +327,66 @@ def spec_accept_from_logits_noalloc(d_logits, d_block, d_argmax, d_accept_len, s
 # ----------------------------------------------------------------------------
 # A paged cache shared by many sequences (no handle; the current torch stream)
 # ----------------------------------------------------------------------------
-# A call's host side is short (these calls run in serving loops, once per layer):
-# one pass over the arguments, the raw stream, no tensor but the result and its scratch.
+# These calls run in serving loops, once per layer, so their host side is short:
+# one expression accepts what is right, and only when it does not hold does
+# _explain look for what is wrong.
+_torch = _I32 = _BF16 = None
+
+
+def _load_torch():
+    global _torch, _I32, _BF16
+    import torch
+    _torch, _I32, _BF16 = torch, torch.int32, torch.bfloat16
+    return torch
+
+
 def _refuse(msg):
     raise SpecError(SPEC_ERR_INVALID_ARG, msg)
 
 
-def _current(t):
-    """Index of the current CUDA device, which must hold t."""
-    import torch
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        _refuse("the buffers must be tensors on the current CUDA device")
-    return dev
+def _explain(call, i32=(), pools=(), rows=(), dims=()):
+    """Raises for the first argument that is not what its call needs.  i32:
+    (name, tensor, entries); pools: the key and the value pool; rows: (name,
+    tensor, shape or None); dims: (name, tensor, dimensions, what they are)."""
+    T = _torch or _load_torch()
+    tensors = [(n, t) for n, t, _ in i32] + [(n, t) for n, t, _ in rows] + list(zip(("d_kpool", "d_vpool"), pools))
+    for name, t in tensors:
+        if not isinstance(t, T.Tensor) or t.get_device() < 0 or t.get_device() != T._C._cuda_getDevice():
+            _refuse("%s: %s must be a tensor on the current CUDA device" % (call, name))
+    for name, t, count, what in dims:
+        if t.dim() != count:
+            _refuse("%s: %s must be %s" % (call, name, what))
+    for name, t, need in i32:
+        if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < need:
+            _refuse("%s: %s must be a contiguous int32 tensor of at least %d entries" % (call, name, need))
+    for name, t in zip(("d_kpool", "d_vpool"), pools):
+        if t.dtype is not _BF16 or not t.is_contiguous() or t.shape[2] != SPEC_PAGE or t.shape != pools[0].shape:
+            _refuse("%s: %s must be a contiguous bfloat16 tensor [pages][kv heads][%d][head_dim], both pools alike"
+                    % (call, name, SPEC_PAGE))
+    for name, t, shape in rows:
+        if t.dtype is not _BF16 or tuple(t.shape) != tuple(shape):
+            _refuse("%s: %s must be a bfloat16 tensor %s" % (call, name, list(shape)))
+        if _row_stride(t) is None:
+            _refuse("%s: the rows of %s must be contiguous [heads][head_dim] blocks" % (call, name))
 
 
-def _i32(name, t, need, dev):
-    """Data pointer of a contiguous int32 tensor of at least need entries on device dev."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous()
-            and t.numel() >= need):
-        _refuse("%s must be a contiguous int32 tensor of at least %d entries on the current CUDA device" % (name, need))
-    return t.data_ptr()
-
-
-def _rows_bf16(name, t, rows, heads, head_dim, dev):
-    """(pointer, row stride) of a bf16 tensor [rows][heads][head_dim] whose rows
-    are contiguous; the rows may lie any distance apart."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev
-            and t.shape == (rows, heads, head_dim)):
-        _refuse("%s must be a bfloat16 tensor [%d][%d][%d] on the current CUDA device" % (name, rows, heads, head_dim))
+def _row_stride(t):
+    """Elements from a row of t [rows][heads][head_dim] to the next; None when
+    a row is not contiguous.  Rows may lie any distance apart; a stride over a
+    dimension of size one is not looked at."""
+    rows, heads, hd = t.shape
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and head_dim > 1) or (s1 != head_dim and heads > 1):
-        _refuse("the rows of %s must be contiguous [heads][head_dim] blocks" % name)
-    return t.data_ptr(), s0 if rows > 1 else heads * head_dim
-
-
-def _pools(k, v, dev):
-    """Shape [pages, kv heads, SPEC_PAGE, head_dim] of a key and a value pool."""
-    import torch
-    for name, t in (("d_kpool", k), ("d_vpool", v)):
-        if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.dim() == 4
-                and t.is_contiguous()):
-            _refuse("%s must be a contiguous bfloat16 tensor [pages][kv heads][%d][head_dim] on the current CUDA device"
-                    % (name, SPEC_PAGE))
-    shape = k.shape
-    if shape[2] != SPEC_PAGE or v.shape != shape:
-        _refuse("d_kpool and d_vpool must both be [pages][kv heads][%d][head_dim]" % SPEC_PAGE)
-    return shape
+    if (s2 != 1 and hd > 1) or (s1 != hd and heads > 1):
+        return None
+    return s0 if rows > 1 else heads * hd
 
 
 def spec_pages_init(d_pool):
     """All pages of d_pool (int32 [SPEC_POOL_HEADER + pages]) become free."""
-    import torch
-    dev = _current(d_pool)
-    ptr = _i32("d_pool", d_pool, SPEC_POOL_HEADER + 1, dev)
-    _check(library().spec_pages_init(ptr, d_pool.numel() - SPEC_POOL_HEADER, torch._C._cuda_getCurrentRawStream(dev)))
+    T = _torch or _load_torch()
+    _explain("spec_pages_init", i32=(("d_pool", d_pool, SPEC_POOL_HEADER + 1),))
+    _check(library().spec_pages_init(d_pool.data_ptr(), d_pool.numel() - SPEC_POOL_HEADER,
+                                     T._C._cuda_getCurrentRawStream(d_pool.get_device())))
 
 
 def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots):
@@ -391,34 +394,73 @@ def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots
     int32 [nseq][table_pages], lengths, keep and add int32 [nseq]; writes
     row_start [nseq + 1] and the new rows' slots.  Errors that only the device
     can see land in d_pool[SPEC_POOL_ERROR]."""
-    import torch
-    dev = _current(d_pool)
-    tables = _i32("d_tables", d_tables, 0, dev)
-    if d_tables.dim() != 2:
-        _refuse("d_tables must be [nseq][table_pages]")
-    nseq, width = d_tables.shape
-    _check(library().spec_pages_step(
-        _i32("d_pool", d_pool, SPEC_POOL_HEADER + 1, dev), d_pool.numel() - SPEC_POOL_HEADER, tables, width,
-        _i32("d_len", d_len, nseq, dev), _i32("d_keep", d_keep, nseq, dev), _i32("d_add", d_add, nseq, dev), nseq,
-        _i32("d_row_start", d_row_start, nseq + 1, dev), _i32("d_slots", d_slots, 0, dev), d_slots.numel(),
-        torch._C._cuda_getCurrentRawStream(dev)))
+    T = _torch or _load_torch()
+    try:
+        nseq, width = d_tables.shape
+        dev = d_pool.get_device()
+        cap = d_slots.numel()
+        ok = (dev >= 0 and dev == T._C._cuda_getDevice() and d_pool.dtype is _I32 and d_tables.dtype is _I32
+              and d_len.dtype is _I32 and d_keep.dtype is _I32 and d_add.dtype is _I32 and d_row_start.dtype is _I32
+              and d_slots.dtype is _I32 and d_tables.get_device() == dev and d_len.get_device() == dev
+              and d_keep.get_device() == dev and d_add.get_device() == dev and d_row_start.get_device() == dev
+              and d_slots.get_device() == dev and d_pool.is_contiguous() and d_tables.is_contiguous()
+              and d_len.is_contiguous() and d_keep.is_contiguous() and d_add.is_contiguous()
+              and d_row_start.is_contiguous() and d_slots.is_contiguous() and d_pool.numel() > SPEC_POOL_HEADER
+              and d_len.numel() >= nseq and d_keep.numel() >= nseq and d_add.numel() >= nseq
+              and d_row_start.numel() > nseq)
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        _explain("spec_pages_step", i32=(("d_pool", d_pool, SPEC_POOL_HEADER + 1), ("d_tables", d_tables, 0)),
+                 dims=(("d_tables", d_tables, 2, "[nseq][table_pages]"),))
+        n = d_tables.shape[0]
+        _explain("spec_pages_step", i32=(("d_len", d_len, n), ("d_keep", d_keep, n), ("d_add", d_add, n),
+                                         ("d_row_start", d_row_start, n + 1), ("d_slots", d_slots, 0)))
+        _refuse("spec_pages_step: bad arguments")
+    st = library().spec_pages_step(d_pool.data_ptr(), d_pool.numel() - SPEC_POOL_HEADER, d_tables.data_ptr(), width,
+                                   d_len.data_ptr(), d_keep.data_ptr(), d_add.data_ptr(), nseq, d_row_start.data_ptr(),
+                                   d_slots.data_ptr(), cap, T._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
 
 
 def spec_paged_append(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_error=None):
     """Write the rows of d_k and d_v (bf16 [rows][kv heads][head_dim], rows any
     distance apart) at their slots; only rows below the device int32
     d_row_count (None: all)."""
-    import torch
-    dev = _current(d_k)
-    pages, heads, _, hd = _pools(d_kpool, d_vpool, dev)
-    rows = d_k.shape[0] if d_k.dim() else 0
-    k, ks = _rows_bf16("d_k", d_k, rows, heads, hd, dev)
-    v, vs = _rows_bf16("d_v", d_v, rows, heads, hd, dev)
-    _check(library().spec_paged_append(
-        k, ks, v, vs, _i32("d_slots", d_slots, rows, dev),
-        None if d_row_count is None else _i32("d_row_count", d_row_count, 1, dev), rows, heads, hd, d_kpool.data_ptr(),
-        d_vpool.data_ptr(), pages, None if d_error is None else _i32("d_error", d_error, 1, dev),
-        torch._C._cuda_getCurrentRawStream(dev)))
+    T = _torch or _load_torch()
+    try:
+        pages, heads, page, hd = d_kpool.shape
+        rows = d_k.shape[0]
+        dev = d_k.get_device()
+        ks, vs = _row_stride(d_k), _row_stride(d_v)
+        ok = (dev >= 0 and dev == T._C._cuda_getDevice() and page == SPEC_PAGE and d_k.dtype is _BF16 and d_v.dtype is _BF16
+              and d_kpool.dtype is _BF16 and d_vpool.dtype is _BF16 and d_slots.dtype is _I32 and ks is not None
+              and vs is not None and d_k.shape == (rows, heads, hd) and d_v.shape == d_k.shape
+              and d_vpool.shape == d_kpool.shape and d_v.get_device() == dev and d_kpool.get_device() == dev
+              and d_vpool.get_device() == dev and d_slots.get_device() == dev and d_kpool.is_contiguous()
+              and d_vpool.is_contiguous() and d_slots.is_contiguous() and d_slots.numel() >= rows)
+        for t in (d_row_count, d_error):
+            if t is not None:
+                ok = ok and t.dtype is _I32 and t.get_device() == dev and t.is_contiguous() and t.numel() > 0
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        more = tuple((n, t, 1) for n, t in (("d_row_count", d_row_count), ("d_error", d_error)) if t is not None)
+        _explain("spec_paged_append", pools=(d_kpool, d_vpool), i32=(("d_slots", d_slots, 0),) + more,
+                 dims=(("d_kpool", d_kpool, 4, "4-D"), ("d_vpool", d_vpool, 4, "4-D")))
+        for name, t in (("d_k", d_k), ("d_v", d_v)):
+            if not isinstance(t, T.Tensor) or t.dim() != 3:
+                _refuse("spec_paged_append: %s must be [rows][kv heads][head_dim]" % name)
+        want = (d_k.shape[0], d_kpool.shape[1], d_kpool.shape[3])
+        _explain("spec_paged_append", rows=(("d_k", d_k, want), ("d_v", d_v, want)), i32=(("d_slots", d_slots, want[0]),))
+        _refuse("spec_paged_append: bad arguments")
+    st = library().spec_paged_append(d_k.data_ptr(), ks, d_v.data_ptr(), vs, d_slots.data_ptr(),
+                                     None if d_row_count is None else d_row_count.data_ptr(), rows, heads, hd,
+                                     d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
+                                     None if d_error is None else d_error.data_ptr(), T._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
 
 
 def spec_paged_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int, table_pages: int) -> int:
@@ -441,37 +483,64 @@ def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, ma
     (bf16 [rows][heads][head_dim]; a new tensor when None, whose rows outside
     every sequence are then unset).  scale defaults to head_dim ** -0.5; d_work
     (a uint8 tensor) to scratch from torch's allocator."""
-    import torch
-    dev = _current(d_q)
-    pages, hkv, _, hd = _pools(d_kpool, d_vpool, dev)
-    if d_q.dim() != 3:
-        _refuse("d_q must be [rows][heads][head_dim]")
-    rows, hq, _ = d_q.shape
-    q, qs = _rows_bf16("d_q", d_q, rows, hq, hd, dev)
-    tables = _i32("d_tables", d_tables, 0, dev)
-    if d_tables.dim() != 2:
-        _refuse("d_tables must be [nseq][table_pages]")
-    nseq, width = d_tables.shape
+    T = _torch or _load_torch()
+    try:
+        pages, hkv, page, hd = d_kpool.shape
+        rows, hq, qd = d_q.shape
+        nseq, width = d_tables.shape
+        dev = d_q.get_device()
+        qs = _row_stride(d_q)
+        ok = (dev >= 0 and dev == T._C._cuda_getDevice() and page == SPEC_PAGE and qd == hd and qs is not None
+              and d_q.dtype is _BF16 and d_kpool.dtype is _BF16 and d_vpool.dtype is _BF16 and d_tables.dtype is _I32
+              and d_len.dtype is _I32 and d_row_start.dtype is _I32 and d_vpool.shape == d_kpool.shape
+              and d_kpool.get_device() == dev and d_vpool.get_device() == dev and d_tables.get_device() == dev
+              and d_len.get_device() == dev and d_row_start.get_device() == dev and d_kpool.is_contiguous()
+              and d_vpool.is_contiguous() and d_tables.is_contiguous() and d_len.is_contiguous()
+              and d_row_start.is_contiguous() and d_len.numel() >= nseq and d_row_start.numel() > nseq)
+        if d_error is not None:
+            ok = (ok and d_error.dtype is _I32 and d_error.get_device() == dev and d_error.is_contiguous()
+                  and d_error.numel() > 0)
+        os_ = hq * qd
+        if d_out is not None:
+            os_ = _row_stride(d_out)
+            ok = (ok and os_ is not None and d_out.dtype is _BF16 and d_out.get_device() == dev
+                  and d_out.shape == d_q.shape)
+        if d_work is not None:
+            ok = ok and d_work.dtype is T.uint8 and d_work.get_device() == dev and d_work.is_contiguous()
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        more = () if d_error is None else (("d_error", d_error, 1),)
+        _explain("spec_paged_attention", pools=(d_kpool, d_vpool), i32=(("d_tables", d_tables, 0),) + more,
+                 dims=(("d_kpool", d_kpool, 4, "4-D"), ("d_vpool", d_vpool, 4, "4-D"),
+                       ("d_tables", d_tables, 2, "[nseq][table_pages]")))
+        n = d_tables.shape[0]
+        _explain("spec_paged_attention", i32=(("d_row_start", d_row_start, n + 1), ("d_len", d_len, n)))
+        if not isinstance(d_q, T.Tensor) or d_q.dim() != 3:
+            _refuse("spec_paged_attention: d_q must be [rows][heads][head_dim]")
+        want = (d_q.shape[0], d_q.shape[1], d_kpool.shape[3])
+        for name, t in (("d_q", d_q), ("d_out", d_out)):
+            if t is not None:
+                _explain("spec_paged_attention", rows=((name, t, want),))
+        _refuse("spec_paged_attention: d_work must be a contiguous uint8 tensor on the current CUDA device")
     max_new = int(max_new)
     if d_out is None:
-        d_out = torch.empty((rows, hq, hd), dtype=torch.bfloat16, device=d_q.device)
-    out, os_ = _rows_bf16("d_out", d_out, rows, hq, hd, dev)
+        d_out = T.empty((rows, hq, hd), dtype=_BF16, device=d_q.device)
     work, work_bytes = None, 0
-    if d_work is None:
+    if d_work is not None:
+        work, work_bytes = d_work.data_ptr(), d_work.numel()
+    else:
         work_bytes = _work_bytes(dev, hq, hkv, hd, max_new, width)
         if work_bytes:
-            d_work = torch.empty(work_bytes, dtype=torch.uint8, device=d_q.device)
+            d_work = T.empty(work_bytes, dtype=T.uint8, device=d_q.device)
             work = d_work.data_ptr()
-    elif not (isinstance(d_work, torch.Tensor) and d_work.dtype is torch.uint8 and d_work.get_device() == dev
-              and d_work.is_contiguous()):
-        _refuse("d_work must be a contiguous uint8 tensor on the current CUDA device")
-    else:
-        work, work_bytes = d_work.data_ptr(), d_work.numel()
-    _check(library().spec_paged_attention(
-        q, qs, _i32("d_row_start", d_row_start, nseq + 1, dev), _i32("d_len", d_len, nseq, dev), tables, width, nseq, rows,
-        max_new, hq, hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
-        out, os_, None if d_error is None else _i32("d_error", d_error, 1, dev), work, work_bytes,
-        torch._C._cuda_getCurrentRawStream(dev)))
+    st = library().spec_paged_attention(
+        d_q.data_ptr(), qs, d_row_start.data_ptr(), d_len.data_ptr(), d_tables.data_ptr(), width, nseq, rows, max_new, hq,
+        hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
+        d_out.data_ptr(), os_, None if d_error is None else d_error.data_ptr(), work, work_bytes,
+        T._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
     return d_out
 
 
