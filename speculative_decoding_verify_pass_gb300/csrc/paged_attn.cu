@@ -46,9 +46,6 @@ using split::kChunk;
 
 constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadWarp = 10, kListWarp = 11, kResultWarp = 12, kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-// registers of a thread, by role: 128 each at launch, moved to where S^T and P^T live
-constexpr int kSoftRegs = 184, kIssueRegs = 64, kResultRegs = 80;
-static_assert(2 * kSoftRegs + kIssueRegs + kResultRegs <= 4 * 128, "more registers than the block was launched with");
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -1e30f;         // reference of a row that has seen no key
 constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
@@ -114,6 +111,9 @@ struct Plan {
     static constexpr int kO = kStack ? 2 * RP : RP;         // tensor-memory columns of one O^T
     static constexpr int kUsed = 2 * RP + (kStream ? 4 : 2) * kO;   // S^T x 2, O^T x 2 (per warpgroup)
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
+    // registers of a thread, by role: 128 each at launch, moved to where S^T and P^T live
+    static constexpr int kSoftRegs = RP <= 32 ? 160 : 184, kIssueRegs = 64, kResultRegs = RP <= 32 ? 128 : 80;
+    static_assert(2 * kSoftRegs + kIssueRegs + kResultRegs <= 4 * 128, "more registers than the block was launched with");
     static_assert(NK >= 1 && NV >= 2 && kUsed <= 512, "one K, and V of this chunk and the one before");
 };
 
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     };
 
     if (warp >= kScoreWarp && warp < kResultWarp) {
-        regs_down<kIssueRegs>();
+        regs_down<L::kIssueRegs>();
         if (warp == kListWarp) {
             // ---------------- the list of segments, and what the join kernel has to do here ----------------
             if (lane == 0) {
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         __syncwarp();
     } else if (warp < kSoftWarps) {
         // ---------------- softmax: thread = key ----------------
-        regs_up<kSoftRegs>();
+        regs_up<L::kSoftRegs>();
         const int wg = warp >> 2, qd = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         const int key = qd * 32 + lane;
@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         }
     } else {
         // ---------------- results: thread = head dimension ----------------
-        regs_down<kResultRegs>();
+        if constexpr (L::kResultRegs < 128) regs_down<L::kResultRegs>();
         const int qd = warp & 3, d = qd * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         int i = 0;                              // the segment's first unit
@@ -914,23 +914,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const bool bad = poison[par] == seg + 1;
             ok = ok && wait(&o_full[par], (seg >> 1) & 1, deadp);
             tc_fence_after();
-            const long long out0 = (long long)w.row0 * p.out_stride + (long long)w.head * p.group * HD + d;
+            uint16_t* const out = p.out + (long long)w.row0 * p.out_stride + (long long)w.head * p.group * HD + d;
+            float* const part = p.part_o + (size_t)(whole ? 0 : w.slot) * RP * HD + d;
+            constexpr int kStep = 16;           // rows whose O^T is in flight together
 #pragma unroll 1
-            for (int j = 0; j < w.R; j += 8) {
-                // the row's O^T (both parts) of the first warpgroup, and of the other
-                float o[8], x[8], y[8], z[8];
-                const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j;
-                const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j;
-                tmem_ld8_async(at, o);
-                if (kStack) tmem_ld8_async(at + RP, x);
+            for (int j0 = 0; j0 < w.R; j0 += kStep) {
+                // the rows' O^T (both parts) of the first warpgroup, and of the other
+                float o[kStep], x[kStep], y[kStep], z[kStep];
+                const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j0;
+                const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j0;
+                tmem_ld16_async(at, o);
+                if (kStack) tmem_ld16_async(at + RP, x);
                 if (two) {
-                    tmem_ld8_async(bt, y);
-                    if (kStack) tmem_ld8_async(bt + RP, z);
+                    tmem_ld16_async(bt, y);
+                    if (kStack) tmem_ld16_async(bt + RP, z);
                 }
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 f = weight[par][j + e];
+                for (int e = 0; e < kStep; ++e) {
+                    const float2 f = weight[par][j0 + e];
                     o[e] = (kStack ? o[e] + x[e] : o[e]) * f.x;
                     if (two) o[e] += (kStack ? y[e] + z[e] : y[e]) * f.y;
                 }
@@ -943,16 +945,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             const float v = bf2f(p.vpool[(((size_t)page * p.hkv + w.head) * SPEC_PAGE + t % SPEC_PAGE) * HD + d]);
                             if (!isfinite(v))
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    if (t <= last0 + tok[j + e]) o[e] += v;
+                                for (int e = 0; e < kStep; ++e)
+                                    if (t <= last0 + tok[j0 + e]) o[e] += v;
+                        }
+                    if (whole) {
+                        if (last0 < 0) {        // rows without a position
+#pragma unroll
+                            for (int e = 0; e < kStep; ++e)
+                                if (last0 + tok[j0 + e] < 0) o[e] = 0.f;
                         }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = j + e;
-                        if (r < w.R) {
-                            if (whole) p.out[out0 + col_off[r]] = f2bf(last0 + tok[r] >= 0 ? o[e] : 0.f);
-                            else p.part_o[((size_t)w.slot * RP + r) * HD + d] = o[e];
-                        }
+                        for (int e = 0; e < kStep; ++e)
+                            if (j0 + e < w.R) out[col_off[j0 + e]] = f2bf(o[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kStep; ++e)
+                            if (j0 + e < w.R) part[(j0 + e) * HD] = o[e];
                     }
                 }
             }
@@ -973,9 +981,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
 }
 
-// Joins the partials of each pair that CTAs shared.  The pair's CTAs deal its
-// rows among themselves (CTA t of n takes rows t, t + n, ..): the more partials
-// a row has, the more CTAs read them.  Up to 8 partials a warp joins a row, its
+// Joins the partials of each pair that CTAs shared: CTA (c, y) works for the pair
+// that goes on into attention CTA c (y even) or begins in it and goes on (odd).
+// The CTAs of a pair deal its rows among themselves (t of n takes rows t, t + n,
+// ..): the more partials a row has, the more CTAs read them.  Up to 8 partials a warp joins a row, its
 // loads all in flight at once; above, the CTA's 8 warps share the row's partials.
 constexpr int kJoinFew = 8, kJoinWarps = 8;
 
@@ -987,12 +996,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    const Meta metas[2] = {p.meta[2 * blockIdx.x], p.meta[2 * blockIdx.x + 1]};
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const Meta m = metas[k];
-        if (m.count == 0) continue;
-        const int mine = blockIdx.x - m.owner;
+    {
+        const Meta m = p.meta[2 * blockIdx.x + (blockIdx.y & 1)];
+        if (m.count == 0) return;
+        const int mine = blockIdx.x - m.owner, y0 = blockIdx.y >> 1, ny = gridDim.y >> 1;
         // partial t of the pair: the owner's slot, then the first slots of the CTAs after it
         auto at = [&](int r, int t) { return (size_t)(t ? 2 * (m.owner + t) : m.slot) * rp + r; };
         auto store = [&](int r, const float* o, float sum) {
@@ -1016,7 +1023,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
             }
         };
         if (m.count <= kJoinFew) {
-            for (int r = mine + m.count * (warp + kJoinWarps * blockIdx.y); r < m.rows; r += m.count * kJoinWarps * gridDim.y) {
+            for (int r = mine + m.count * (warp + kJoinWarps * y0); r < m.rows; r += m.count * kJoinWarps * ny) {
                 float v[kJoinFew][V];
                 float2 ml[kJoinFew];
 #pragma unroll
@@ -1040,7 +1047,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
                 store(r, o, sum);
             }
         } else {
-            for (int r = mine + m.count * blockIdx.y; r < m.rows; r += m.count * gridDim.y) {
+            for (int r = mine + m.count * y0; r < m.rows; r += m.count * ny) {
                 float M = kNone, sum = 0.f, o[V] = {};
                 for (int t = lane; t < m.count; t += 32) M = fmaxf(M, p.part_ml[at(r, t)].x);
 #pragma unroll
@@ -1176,7 +1183,7 @@ cudaError_t run(PagedParams& p, int ctas, cudaStream_t s) {
     if ((e = launch(fn, dim3((unsigned)ctas), kThreads, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess || p.whole) return e;
     int rp = RP;
     void* jargs[] = {&p, &rp};
-    return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, RP <= 32 ? 1 : RP / 32), 32 * kJoinWarps, 0, s, jargs);
+    return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, 2 * (RP <= 16 ? 1 : RP / 16)), 32 * kJoinWarps, 0, s, jargs);
 }
 
 }  // namespace
