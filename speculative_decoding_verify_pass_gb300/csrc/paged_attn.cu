@@ -23,7 +23,9 @@
 // ends.
 //
 // Roles, by warpgroup: 0 and 1 softmax (thread = key); 2 one warp each for the
-// MMAs of S^T, the MMAs of O^T, the TMA copies and the list of segments; 3 results
+// MMAs of S^T, the MMAs of O^T, the copies of V, and the list of segments with the
+// copies of Q and K (K runs ahead of V: one copying warp would wait for a V slot
+// with K slots free); 3 results
 // (thread = head dimension).  Up to 64 rows the two softmax warpgroups take
 // alternate chunks, each with its own reference, sum and O^T (joined with the
 // results): a warp's chain of dependent instructions is what a chunk of few rows
@@ -44,7 +46,7 @@ namespace {
 
 using split::kChunk;
 
-constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadWarp = 10, kListWarp = 11, kResultWarp = 12, kWarps = 16;
+constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12, kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -1e30f;         // reference of a row that has seen no key
@@ -106,15 +108,20 @@ struct Plan {
     static constexpr int kFixed = NQ * kQ + NP * 2 * kP + 2048;   // alignment, pad after the last slot
     static constexpr int kMost = 227 * 1024 - (6656 + 64 * RP) - kFixed; // less the static arrays
     static constexpr int NS = kMost / kSlot < 8 ? kMost / kSlot : 8;
-    static constexpr int NK = NS / 2, NV = NS - NK;
-    static constexpr int kBytes = kFixed + NS * kSlot;
+    // V slots hold a chunk, or from 64 rows on, where there is room for few, a page:
+    // the next chunk's first page then loads while this one's is still in use.
+    // Of an odd number of pages K takes the rounded up half.
+    static constexpr int kPieces = RP >= 64 ? 2 : 1, kPiece = kSlot / kPieces;
+    static constexpr int NK = kPieces == 2 ? (kMost / kPiece + 2) / 4 : NS / 2;
+    static constexpr int NV = (kMost - NK * kSlot) / kPiece < 8 ? (kMost - NK * kSlot) / kPiece : 8;
+    static constexpr int kBytes = kFixed + NK * kSlot + NV * kPiece;
     static constexpr int kO = kStack ? 2 * RP : RP;         // tensor-memory columns of one O^T
     static constexpr int kUsed = 2 * RP + (kStream ? 4 : 2) * kO;   // S^T x 2, O^T x 2 (per warpgroup)
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     // registers of a thread, by role: 128 each at launch, moved to where S^T and P^T live
     static constexpr int kSoftRegs = RP <= 32 ? 160 : 184, kIssueRegs = 64, kResultRegs = RP <= 32 ? 128 : 80;
     static_assert(2 * kSoftRegs + kIssueRegs + kResultRegs <= 4 * 128, "more registers than the block was launched with");
-    static_assert(NK >= 1 && NV >= 2 && kUsed <= 512, "one K, and V of this chunk and the one before");
+    static_assert(NK >= 1 && NV >= kPieces + 1 && kUsed <= 512, "a K, and a V beyond the one in use");
 };
 
 __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -254,18 +261,35 @@ struct Walk {
     const PagedParams& p;
     const int* first;           // [nseq + 1] in shared memory
     int u, end;                 // next unit, end of the CTA's range
-    int q = -1, q0 = 0, q1 = 0; // sequence and its units
+    int q = 0, q1 = 0;          // sequence, the end of its units
     int rows = 0, len = 0, row_base = 0, chunks = 1;
     // the segment
     int head = 0, block = 0, c0 = 0, c1 = 0, R = 0, seg = -1;
 
     __device__ Walk(const PagedParams& pp, const int* f, int begin, int e) : p(pp), first(f), u(begin), end(e) {}
+    __device__ __forceinline__ void sequence() {
+        q1 = first[q + 1];
+        row_base = p.row_start[q];
+        rows = p.row_start[q + 1] - row_base;
+        len = p.len[q];
+        chunks = split::chunks_of(len);
+    }
     __device__ __forceinline__ bool next() {
-        for (;;) {
-            if (u >= end) return false;
-            find();
-            if (!p.whole || c0 == 0) break;
-            u += chunks - c0;   // begins in another CTA's range, which takes it
+        if (u >= end) return false;
+        if (seg < 0) {                          // where the range begins
+            q = split::sequence_of(first, p.nseq, u);
+            sequence();
+            const int at = u - first[q], pair = at / chunks;
+            block = pair / p.hkv;
+            head = pair - block * p.hkv;
+            c0 = at - pair * chunks;
+            if (p.whole && c0 > 0) {            // this pair begins in another CTA's range, which takes it
+                u += chunks - c0;
+                if (u >= end) return false;
+                step();
+            }
+        } else {
+            step();
         }
         c1 = p.whole ? chunks : min(chunks, c0 + end - u);
         R = min(p.tokens, rows - block * p.tokens) * p.group;
@@ -273,21 +297,18 @@ struct Walk {
         ++seg;
         return true;
     }
-    // where unit u lies
-    __device__ __forceinline__ void find() {
-        if (q < 0 || u >= q1) {
-            q = split::sequence_of(first, p.nseq, u);
-            q0 = first[q];
-            q1 = first[q + 1];
-            row_base = p.row_start[q];
-            rows = p.row_start[q + 1] - row_base;
-            len = p.len[q];
-            chunks = split::chunks_of(len);
+    // the pair after the current one
+    __device__ __forceinline__ void step() {
+        c0 = 0;
+        if (u >= q1) {
+            do ++q;
+            while (first[q + 1] <= u);          // sequences without units
+            sequence();
+            block = head = 0;
+        } else if (++head == p.hkv) {
+            head = 0;
+            ++block;
         }
-        const int pair = (u - q0) / chunks;
-        block = pair / p.hkv;
-        head = pair - block * p.hkv;
-        c0 = u - q0 - pair * chunks;
     }
     __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
     // last position that the block's first token sees
@@ -308,6 +329,28 @@ struct Walk {
     }
 };
 
+// The pages of a segment's chunks, looked up 32 chunks at a time, one a lane.
+struct PageWalk {
+    int y0 = -1, y1 = -1;       // the lane's chunk: tensor-map rows of its two pages
+    int z0 = -1, z1 = -1;       // the current chunk's (a bad page's -1 lies outside the pool and reads as zeros)
+    int count = 0;              // and how many of them exist
+    __device__ __forceinline__ void at(const PagedParams& p, const Seg& s, int k, int lane) {
+        const int held = (s.len + SPEC_PAGE - 1) / SPEC_PAGE, c = s.c0 + k;
+        if ((k & 31) == 0) {
+            const int* tab = p.tables + (size_t)s.q * p.table_pages + 2 * (c + lane);
+            const int have = k + lane < s.units ? held - 2 * (c + lane) : 0;
+            const int a = have > 0 ? tab[0] : -1, b = have > 1 ? tab[1] : -1;
+            const bool oka = a >= 0 && a < p.num_pages, okb = b >= 0 && b < p.num_pages;
+            if (p.err && ((have > 0 && !oka) || (have > 1 && !okb))) atomicCAS(p.err, 0, SPEC_PAGED_BAD_PAGE);
+            y0 = oka ? a * p.hkv + s.head : -1;
+            y1 = okb ? b * p.hkv + s.head : -1;
+        }
+        z0 = __shfl_sync(0xffffffffu, y0, k & 31);
+        z1 = __shfl_sync(0xffffffffu, y1, k & 31);
+        count = max(0, min(2, held - 2 * c));
+    }
+};
+
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -325,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     constexpr int kGroups = kStream ? 2 : 1;    // O^T's (and references) of a segment
     constexpr int kArrive = kStream ? 4 : 8;    // warps that read an S^T and write a P^T
     constexpr int kReaders = kSoftWarps + 3 + 4;    // warps that read the list of segments
+    constexpr int kPieces = L::kPieces, kPieceRows = kChunk / kPieces;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[NQ], q_empty[NQ], s_full[2], s_empty[2], p_full[NP], p_empty[NP],
         o_full[2], o_empty[2], l_full[2], l_empty[2], seg_full[kSegs], seg_empty[kSegs], fin[2];
@@ -343,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* kslots = base;
     uint8_t* vslots = kslots + NK * L::kSlot;
-    uint8_t* qs = vslots + NV * L::kSlot + 1024;        // 1 KB: an M = 128 MMA over 64 dimensions reads past its slot
+    uint8_t* qs = vslots + NV * L::kPiece + 1024;       // 1 KB: an M = 128 MMA over 64 dimensions reads past its slot
     uint8_t* ps = qs + NQ * L::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -454,21 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
     if (warp >= kScoreWarp && warp < kResultWarp) {
         regs_down<L::kIssueRegs>();
-        if (warp == kListWarp) {
-            // ---------------- the list of segments, and what the join kernel has to do here ----------------
-            if (lane == 0) {
-                Walk w(p, first, begin, end);
-                Meta into = {}, from = {};
+        if (warp == kLoadKWarp) {
+            // ---------------- the list of segments, Q and K copies, and what the join kernel has to do here ----------------
+            Walk w(p, first, begin, end);
+            Meta into = {}, from = {};
+            Ring<NK> kr;
+            Ring<NQ> qr;
+            bool ok = true;
 #pragma unroll 1
-                for (bool more = true; more;) {
-                    more = w.next();
-                    Seg s = {};
-                    if (!more) {                // the list ends
-                        if (!wait(&seg_empty[sr.at], sr.round ^ 1, deadp)) break;
-                        segs[sr.at] = s;
-                        mbar_arrive(&seg_full[sr.at]);
-                        break;
-                    }
+            for (bool more = true; more && ok;) {
+                more = w.next();
+                Seg s = {};                     // no units: the list ends
+                if (more) {
                     s.c0 = w.c0;
                     s.units = w.c1 - w.c0;
                     s.R = w.R;
@@ -478,33 +519,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     s.head = w.head;
                     s.row0 = w.row_base + w.block * p.tokens;
                     s.slot = w.whole() ? -1 : 2 * (int)blockIdx.x + (w.u - s.units == begin ? 0 : 1);
-                    if (!wait(&seg_empty[sr.at], sr.round ^ 1, deadp)) break;
+                }
+                ok = __all_sync(0xffffffffu, wait(&seg_empty[sr.at], sr.round ^ 1, deadp));
+                if (!ok) break;
+                if (lane == 0) {
                     segs[sr.at] = s;
                     mbar_arrive(&seg_full[sr.at]);
-                    sr.step();
-                    if (w.seg == 0 && w.c0 > 0) into = w.meta(deal);
                 }
-                if (!p.whole) {
-                    if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(deal);
-                    p.meta[2 * blockIdx.x] = into;
-                    p.meta[2 * blockIdx.x + 1] = from;
-                }
-            }
-        } else if (warp == kLoadWarp) {
-            // ---------------- TMA copies (one elected lane issues; the lanes look up pages) ----------------
-            Ring<NK> kr;
-            Ring<NV> vr;
-            Ring<NQ> qr;
-            bool ok = true;
-#pragma unroll 1
-            for (;;) {
-                const Seg s = take(false);
-                ok = __all_sync(0xffffffffu, !*deadp);
-                if (!ok || s.units == 0) break;
-                uint64_t* qf = &q_full[qr.at];
+                sr.step();
+                if (!more) break;
                 ok = __all_sync(0xffffffffu, wait(&q_empty[qr.at], qr.round ^ 1, deadp));
                 if (!ok) break;
                 if (elect_one()) {
+                    uint64_t* qf = &q_full[qr.at];
                     mbar_arrive_expect_tx(qf, (uint32_t)(p.tokens * p.group * HD * 2));
 #pragma unroll
                     for (int hf = 0; hf < HD / 64; ++hf)
@@ -512,59 +539,75 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 }
                 __syncwarp();
                 qr.step();
-                const int held = (s.len + SPEC_PAGE - 1) / SPEC_PAGE;
-                const int* tab = p.tables + (size_t)s.q * p.table_pages;
-                int z0 = -1, z1 = -1;           // the lane's chunk: tensor-map rows of its two pages
+                PageWalk pages;
 #pragma unroll 1
                 for (int k = 0; k < s.units; ++k) {
-                    const int c = s.c0 + k;
-                    if ((k & 31) == 0) {        // the next 32 chunks' pages, one chunk a lane
-                        const int e = 2 * (c + lane);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            int z = -1;
-                            if (k + lane < s.units && e + i < held) {
-                                const int page = tab[e + i];
-                                if (page >= 0 && page < p.num_pages) z = page * p.hkv + s.head;
-                                else if (p.err) atomicCAS(p.err, 0, SPEC_PAGED_BAD_PAGE);
-                            }
-                            if (i) z1 = z;
-                            else z0 = z;
-                        }
-                    }
-                    const int a0 = __shfl_sync(0xffffffffu, z0, k & 31), a1 = __shfl_sync(0xffffffffu, z1, k & 31);
-                    const int pages = min(2, held - 2 * c);   // that exist (a bad one reads as zeros: z = -1)
-#pragma unroll 1
-                    for (int v = 0; v < 2; ++v) {
-                        const int at = v ? vr.at : kr.at;
-                        uint64_t* full = v ? &v_full[at] : &k_full[at];
-                        ok = __all_sync(0xffffffffu, wait(v ? &v_empty[at] : &k_empty[at], (v ? vr.round : kr.round) ^ 1, deadp));
-                        if (!ok) break;
-                        uint8_t* dst = (v ? vslots : kslots) + at * L::kSlot;
-                        const CUtensorMap* map = v ? &p.mv : &p.mk;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(full, pages > 0 ? (uint32_t)(pages * SPEC_PAGE * HD * 2) : 0u);
-#pragma unroll
-                            for (int hf = 0; hf < HD / 64; ++hf) {
-                                if (pages > 0) tma3(dst + hf * kChunk * 128, map, hf * 64, 0, a0, full);
-                                if (pages > 1) tma3(dst + hf * kChunk * 128 + SPEC_PAGE * 128, map, hf * 64, 0, a1, full);
-                            }
-                        }
-                        __syncwarp();
-                        if (v) vr.step();
-                        else kr.step();
-                    }
+                    pages.at(p, s, k, lane);
+                    ok = __all_sync(0xffffffffu, wait(&k_empty[kr.at], kr.round ^ 1, deadp));
                     if (!ok) break;
+                    if (elect_one()) {
+                        uint64_t* full = &k_full[kr.at];
+                        uint8_t* dst = kslots + kr.at * L::kSlot;
+                        mbar_arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD * 2));
+#pragma unroll
+                        for (int hf = 0; hf < HD / 64; ++hf) {
+                            if (pages.count > 0) tma3(dst + hf * kChunk * 128, &p.mk, hf * 64, 0, pages.z0, full);
+                            if (pages.count > 1) tma3(dst + hf * kChunk * 128 + SPEC_PAGE * 128, &p.mk, hf * 64, 0, pages.z1, full);
+                        }
+                    }
+                    __syncwarp();
+                    kr.step();
                 }
-                if (!ok) break;
+                if (w.seg == 0 && w.c0 > 0) into = w.meta(deal);
+            }
+            if (lane == 0 && !p.whole) {
+                if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(deal);
+                p.meta[2 * blockIdx.x] = into;
+                p.meta[2 * blockIdx.x + 1] = from;
             }
             if (lane == 0 && *deadp) {          // every buffer's last copy, as far as one was issued
 #pragma unroll 1
                 for (int i = 0; i < NK; ++i) drain(&k_full[i], i < kr.at ? kr.round : kr.round ^ 1);
 #pragma unroll 1
-                for (int i = 0; i < NV; ++i) drain(&v_full[i], i < vr.at ? vr.round : vr.round ^ 1);
-#pragma unroll 1
                 for (int i = 0; i < NQ; ++i) drain(&q_full[i], i < qr.at ? qr.round : qr.round ^ 1);
+            }
+        } else if (warp == kLoadVWarp) {
+            // ---------------- V copies ----------------
+            Ring<NV> vr;
+            bool ok = true;
+#pragma unroll 1
+            for (;;) {
+                const Seg s = take(false);
+                ok = __all_sync(0xffffffffu, !*deadp);
+                if (!ok || s.units == 0) break;
+                PageWalk pages;
+#pragma unroll 1
+                for (int k = 0; k < s.units && ok; ++k) {
+                    pages.at(p, s, k, lane);
+#pragma unroll 1
+                    for (int v = 0; v < L::kPieces; ++v) {
+                        ok = __all_sync(0xffffffffu, wait(&v_empty[vr.at], vr.round ^ 1, deadp));
+                        if (!ok) break;
+                        const int count = kPieces == 1 ? pages.count : pages.count > v ? 1 : 0;
+                        if (elect_one()) {
+                            uint64_t* full = &v_full[vr.at];
+                            uint8_t* dst = vslots + vr.at * L::kPiece;
+                            mbar_arrive_expect_tx(full, (uint32_t)(count * SPEC_PAGE * HD * 2));
+#pragma unroll
+                            for (int hf = 0; hf < HD / 64; ++hf) {
+                                if (count > 0) tma3(dst + hf * kPieceRows * 128, &p.mv, hf * 64, 0, v ? pages.z1 : pages.z0, full);
+                                if (count > 1) tma3(dst + hf * kPieceRows * 128 + SPEC_PAGE * 128, &p.mv, hf * 64, 0, pages.z1, full);
+                            }
+                        }
+                        __syncwarp();
+                        vr.step();
+                    }
+                }
+                if (!ok) break;
+            }
+            if (lane == 0 && *deadp) {
+#pragma unroll 1
+                for (int i = 0; i < NV; ++i) drain(&v_full[i], i < vr.at ? vr.round : vr.round ^ 1);
             }
         } else if (warp == kScoreWarp) {
             // ---------------- MMAs of S^T (one elected thread) ----------------
@@ -623,23 +666,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     const uint32_t id = umma_idesc_bf16(128, kStack ? 2 * RP : (s.R + 15) & ~15) | (1u << 15) | (1u << 16);
 #pragma unroll 1
                     for (int k = 0; k < s.units && ok; ++k, ++j) {
-                        ok = wait(&v_full[vs.at], vs.round, deadp) && wait(&p_full[pr.at], pr.round, deadp);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t dv = desc_sw128(sa + vs.at * L::kSlot, HD == 128 ? kChunk * 128 : 1024, 1024);
+                        ok = wait(&p_full[pr.at], pr.round, deadp);
                         const uint64_t dp = umma_desc_kmajor(pa + pr.at * 2 * L::kP, 128, kChunk * 16);
                         const int og = kStream ? (seg & 1) * 2 + (j & 1) : seg & 1;
                         const uint32_t o = tmem + 2 * RP + og * L::kO;
                         const bool more = k >= kGroups;     // this O^T holds earlier chunks
 #pragma unroll
-                        for (int part = 0; part < (kStack ? 1 : 2); ++part)
+                        for (int v = 0; v < kPieces; ++v) {
+                            ok = ok && wait(&v_full[vs.at], vs.round, deadp);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t dv = desc_sw128(sa + vs.at * L::kPiece, HD == 128 ? kPieceRows * 128 : 1024, 1024);
 #pragma unroll
-                            for (int e = 0; e < kChunk / 16; ++e)
-                                umma_bf16_id(o, dv + e * (2048 >> 4), dp + part * (L::kP >> 4) + e * (256 >> 4), id,
-                                             more || (part | e) != 0);
-                        umma_commit(&v_empty[vs.at]);
+                            for (int part = 0; part < (kStack ? 1 : 2); ++part)
+#pragma unroll
+                                for (int e = 0; e < kPieceRows / 16; ++e)
+                                    umma_bf16_id(o, dv + e * (2048 >> 4),
+                                                 dp + part * (L::kP >> 4) + (v * (kPieceRows / 16) + e) * (256 >> 4), id,
+                                                 more || (v | part | e) != 0);
+                            umma_commit(&v_empty[vs.at]);
+                            vs.step();
+                        }
+                        if (!ok) break;
                         umma_commit(&p_empty[pr.at]);
-                        vs.step();
                         pr.step();
                     }
                     if (ok) umma_commit(&o_full[seg & 1]);
@@ -677,7 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             bool fresh = true;
 #pragma unroll 1
             for (int c = w.c0; c < w.c0 + w.units; ++c, ++i) {
-                const Ring<NV> v = vs;
+                const Ring<NV> v0 = vs;         // the slots of the chunk's V: its first page's,
+                if (kPieces == 2) vs.step();
+                const Ring<NV> v1 = vs;         // and its second's
                 vs.step();
                 if (kStream && (i & 1) != wg) continue;
                 const uint32_t st = lanes + (i & 1) * RP + col0;
@@ -702,13 +753,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                         }
                     tmem_wait_ld();
                     if (masked) {
+                        // rows are in token order: the key is hidden from the tokens before it
+                        const int hidden = min(max(kp - last0, 0), RP) * p.group - col0;
 #pragma unroll
-                        for (int j = 0; j < NC; j += kSpan)
-                            if (j < rows) {
-#pragma unroll
-                                for (int e = 0; e < kSpan; ++e)
-                                    if (kp > last0 + tok[col0 + j + e]) s[j + e] = -INFINITY;
-                            }
+                        for (int j = 0; j < NC; ++j)
+                            if (j < hidden) s[j] = -INFINITY;
                     }
                     if (rows <= 0) break;
                     if (fresh) {                // references: the scores of the chunk's first key
@@ -749,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float m = warp_max_exact(masked && kp > last0 + tok[col0 + j + e] ? -INFINITY : x[e]);
+                            const float m = warp_max_exact(kp > last0 + tok[col0 + j + e] ? -INFINITY : x[e]);
                             if (lane == 0) mx[qd][col0 + j + e] = m;
                         }
                     }
@@ -818,29 +867,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     // length they become zero (a weight of zero does not silence a
                     // NaN), between the rows' last positions non-finite ones do,
                     // and are added at the end to the rows that see them.
-                    // (the slot's last V has been consumed: product_done)
-                    ok = ok && wait(&v_full[v.at], v.round, deadp);
-                    uint8_t* vt = vslots + v.at * L::kSlot;
-                    const int from = max(0, last0 + 1 - c * kChunk), live = w.len - c * kChunk;
-#pragma unroll 1
-                    for (int t = from * (HD / 8) + key; t < kChunk * (HD / 8); t += 128) {
-                        const int r = t / (HD / 8), d8 = t % (HD / 8);
-                        uint4* at = reinterpret_cast<uint4*>(vt + (d8 >> 3) * kChunk * 128 + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
-                        if (r >= live) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-                            uint4 x = *at;
-                            uint32_t* e = &x.x;
-                            bool hit = false;
+                    // (The slots' last V have been consumed: product_done.)
+                    ok = ok && wait(&v_full[v0.at], v0.round, deadp);
+                    if (kPieces == 2) ok = ok && wait(&v_full[v1.at], v1.round, deadp);
+                    auto row = [&](int r) {
+                        return vslots + (kPieces == 2 && r >= SPEC_PAGE ? v1.at : v0.at) * L::kPiece +
+                               (kPieces == 2 ? r & (SPEC_PAGE - 1) : r) * 128;
+                    };
+                    if (kp >= w.len) {          // a thread's own row; lanes start at different banks
+                        uint8_t* const z = row(key);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if ((e[k] & 0x7F80u) == 0x7F80u) hit = true, e[k] &= 0xFFFF0000u;
-                                if ((e[k] & 0x7F800000u) == 0x7F800000u) hit = true, e[k] &= 0xFFFFu;
-                            }
-                            if (hit) {
-                                *at = x;
-                                poison[par] = seg + 1;
-                            }
+                        for (int hf = 0; hf < HD / 64; ++hf)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(z + hf * kPieceRows * 128 + (((e + lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    const int from = max(0, last0 + 1 - c * kChunk), to = min(kChunk, w.len - c * kChunk);
+#pragma unroll 1
+                    for (int t = from * (HD / 8) + key; t < to * (HD / 8); t += 128) {
+                        const int e = t % (HD / 8);
+                        uint4* const at = reinterpret_cast<uint4*>(row(t / (HD / 8)) + (e >> 3) * kPieceRows * 128 + ((e & 7) << 4));
+                        uint4 x = *at;
+                        uint32_t* y = &x.x;
+                        bool hit = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((y[k] & 0x7F80u) == 0x7F80u) hit = true, y[k] &= 0xFFFF0000u;
+                            if ((y[k] & 0x7F800000u) == 0x7F800000u) hit = true, y[k] &= 0xFFFFu;
+                        }
+                        if (hit) {
+                            *at = x;
+                            poison[par] = seg + 1;
                         }
                     }
                 }
@@ -916,18 +973,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             tc_fence_after();
             uint16_t* const out = p.out + (long long)w.row0 * p.out_stride + (long long)w.head * p.group * HD + d;
             float* const part = p.part_o + (size_t)(whole ? 0 : w.slot) * RP * HD + d;
-            constexpr int kStep = 16;           // rows whose O^T is in flight together
+            // rows whose O^T is in flight together (more would be more instructions than the cache likes)
+            constexpr int kStep = kStack ? 8 : 16;
 #pragma unroll 1
             for (int j0 = 0; j0 < w.R; j0 += kStep) {
                 // the rows' O^T (both parts) of the first warpgroup, and of the other
                 float o[kStep], x[kStep], y[kStep], z[kStep];
                 const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j0;
                 const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j0;
-                tmem_ld16_async(at, o);
-                if (kStack) tmem_ld16_async(at + RP, x);
+                auto ld = [](uint32_t a, float* r) { if constexpr (kStep == 8) tmem_ld8_async(a, r); else tmem_ld16_async(a, r); };
+                ld(at, o);
+                if (kStack) ld(at + RP, x);
                 if (two) {
-                    tmem_ld16_async(bt, y);
-                    if (kStack) tmem_ld16_async(bt + RP, z);
+                    ld(bt, y);
+                    if (kStack) ld(bt + RP, z);
                 }
                 tmem_wait_ld();
 #pragma unroll
