@@ -425,7 +425,7 @@ spec_status spec_accept_from_logits_noalloc(const float* d_logits, int32_t n, in
  * and writes nothing through it and puts one of the codes below into the error
  * word, unless that already holds one.  The error word of spec_pages_step is
  * d_pool[SPEC_POOL_ERROR]; the other calls take any int32 (that word too), or
- * NULL. */
+ * NULL (errors then go unreported, a timeout of a wait too). */
 #define SPEC_PAGE 64             /* positions per page                             */
 #define SPEC_MAX_SEQS 1024       /* sequences per call                             */
 #define SPEC_MAX_PAGES 33554431  /* pages of one pool (a slot fits int32)          */

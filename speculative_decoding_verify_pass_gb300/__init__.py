@@ -523,7 +523,7 @@ def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, ma
             if t is not None:
                 _explain("spec_paged_attention", rows=((name, t, want),))
         _refuse("spec_paged_attention: d_work must be a contiguous uint8 tensor on the current CUDA device")
-    max_new = int(max_new)
+    max_new = min(int(max_new), 0x7fffffff)
     if d_out is None:
         d_out = T.empty((rows, hq, hd), dtype=_BF16, device=d_q.device)
     work, work_bytes = None, 0

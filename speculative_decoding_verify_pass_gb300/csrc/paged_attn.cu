@@ -230,15 +230,24 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Bounded wait; one that gives up raises `dead`.  Inline (a call would fix the
-// registers that setmaxnreg moves) and short: the roles' loops share one
-// instruction cache.  Callers stop waiting after a failure of theirs.
+// Wait bounded in time (2^31 cycles, about a second, whatever one poll takes);
+// one that gives up raises `dead`.  Inline (a call would fix the registers that
+// setmaxnreg moves) and short: the roles' loops share one instruction cache.
+// A role whose wait failed waits no more.
+__device__ __forceinline__ uint32_t cycles() {
+    uint32_t c;
+    asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
+    return c;
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    const uint32_t t0 = cycles();
 #pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 23); ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    *dead = 1;
-    return false;
+    while (!mbar_try_wait(bar, parity))
+        if (cycles() - t0 > 0x7fffffffu) {
+            *dead = 1;
+            return false;
+        }
+    return true;
 }
 // After a failed wait: let what is in flight finish before the CTA ends.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     if (ok) umma_commit(&q_empty[qr.at]);
                     qr.step();
                 }
-                if (!ok) {
+                if (!ok || *deadp) {
                     umma_commit(&fin[0]);
                     drain(&fin[0], 0);
                 }
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     }
                     if (ok) umma_commit(&o_full[seg & 1]);
                 }
-                if (!ok) {
+                if (!ok || *deadp) {
                     umma_commit(&fin[1]);
                     drain(&fin[1], 0);
                 }

@@ -511,6 +511,44 @@ def test_attention_two_streams_at_once():
         assert torch.equal(got.view(torch.int16), last.view(torch.int16))
 
 
+def test_pools_of_more_than_2_31_elements():
+    """Pages whose elements lie past 32 bits: append and attention at the pool's end."""
+    torch = torch_cuda()
+    sv = sv_()
+    pages = 540000                                     # x 64 x 64: 2.2e9 elements
+    kp = torch.empty((pages, 1, PAGE, 64), dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    c = Case([3000, 70], [3, 1], 4, 1, 64, seed=23)
+    at = 0
+    for q, n in enumerate(c.lens):
+        for j in range(pages_of(n)):
+            c.d["tables"][q, j] = c.tables_cpu[q, j] = pages - 1 - at
+            at += 1
+    slots = torch.cat([c.tables_cpu[q, torch.arange(n) // PAGE] * PAGE + torch.arange(n) % PAGE for q, n in enumerate(c.lens)])
+    k, v = torch.cat(c.k).cuda(), torch.cat(c.v).cuda()
+    c.d["kp"], c.d["vp"] = kp, vp
+    err = i32([0])
+    sv.spec_paged_append(k, v, slots.to(torch.int32).cuda(), None, kp, vp, err)
+    c.check(c.run(d_error=err))
+    assert err.item() == 0
+    del kp, vp
+    c.d.clear()
+    torch.cuda.empty_cache()
+
+
+def test_tables_at_the_border_of_whole_pairs():
+    """Tables of 16 pages keep a pair on one CTA, of 17 split it: the same answer to the tolerance."""
+    torch = torch_cuda()
+    sv = sv_()
+    c = Case([1024, 1000, 5, 0, 513], [4, 1, 2, 1, 16], 8, 2, 128, seed=24)
+    out, bound = c.reference()
+    for width in (16, 17, 18):
+        c.d["tables"] = c.tables_cpu[:, :width].contiguous().cuda()
+        assert (sv.spec_paged_attention_workspace(8, 2, 128, 16, width) == 0) == (width <= 16)
+        g = c.run().float().cpu().numpy()
+        assert np.all(np.abs(g[:c.start[-1]] - out[:c.start[-1]]) <= bound[:c.start[-1]])
+
+
 # ---------------------------------------------------------- run together ----
 class Cycle:
     """A serving loop's state: step, append to two layers, attend both."""
