@@ -526,19 +526,22 @@ def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, ma
     max_new = min(int(max_new), 0x7fffffff)
     if d_out is None:
         d_out = T.empty((rows, hq, hd), dtype=_BF16, device=d_q.device)
-    work, work_bytes = None, 0
+    stream = T._C._cuda_getCurrentRawStream(dev)
+    work, work_bytes, own = None, 0, None
     if d_work is not None:
         work, work_bytes = d_work.data_ptr(), d_work.numel()
     else:
         work_bytes = _work_bytes(dev, hq, hkv, hd, max_new, width)
-        if work_bytes:
-            d_work = T.empty(work_bytes, dtype=T.uint8, device=d_q.device)
-            work = d_work.data_ptr()
-    st = library().spec_paged_attention(
-        d_q.data_ptr(), qs, d_row_start.data_ptr(), d_len.data_ptr(), d_tables.data_ptr(), width, nseq, rows, max_new, hq,
-        hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
-        d_out.data_ptr(), os_, None if d_error is None else d_error.data_ptr(), work, work_bytes,
-        T._C._cuda_getCurrentRawStream(dev))
+        if work_bytes:   # from torch's allocator, given back in the stream's order as a tensor would be
+            work = own = T._C._cuda_cudaCachingAllocator_raw_alloc(work_bytes, stream)
+    try:
+        st = library().spec_paged_attention(
+            d_q.data_ptr(), qs, d_row_start.data_ptr(), d_len.data_ptr(), d_tables.data_ptr(), width, nseq, rows, max_new,
+            hq, hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
+            d_out.data_ptr(), os_, None if d_error is None else d_error.data_ptr(), work, work_bytes, stream)
+    finally:
+        if own is not None:
+            T._C._cuda_cudaCachingAllocator_raw_delete(own)
     if st:
         _check(st)
     return d_out
