@@ -914,16 +914,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[kStream ? i & 1 : 0]);
             }
-            // sums over the warp's keys, 8 rows at a time: halves are exchanged until
-            // lane r of each 8 holds row r, then those lanes are added
+            // sums over the warp's keys, a span of rows at a time: lanes exchange halves
+            // until lane r holds row r, then lanes of the same row are added
 #pragma unroll
-            for (int j = 0; j < NC; j += 8)
+            for (int j = 0; j < NC; j += kSpan)
                 if (j < rows) {
-                    float x[8];
+                    float x[kSpan];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) l[j / 2 + e].get(x[2 * e], x[2 * e + 1]);
+                    for (int e = 0; e < kSpan; e += 2) l[(j + e) / 2].get(x[e], x[e + 1]);
 #pragma unroll
-                    for (int h = 4; h >= 1; h >>= 1) {
+                    for (int h = kSpan / 2; h >= 1; h >>= 1) {
                         const bool up = lane & h;
 #pragma unroll
                         for (int e = 0; e < h; ++e) {
@@ -931,9 +931,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             x[e] = keep + __shfl_xor_sync(0xffffffffu, give, h);
                         }
                     }
-                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 8);
-                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
-                    if (lane < 8) xl[par][gi][qd][col0 + j + lane] = x[0];
+#pragma unroll
+                    for (int h = kSpan; h < 32; h <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], h);
+                    if (lane < kSpan) xl[par][gi][qd][col0 + j + lane] = x[0];
                 }
             __syncwarp();
             if (lane == 0) mbar_arrive(&l_full[par]);
@@ -1022,9 +1022,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             for (int e = 0; e < kStep; ++e)
                                 if (last0 + tok[j0 + e] < 0) o[e] = 0.f;
                         }
+                        // (the offsets first: a guard around each load would wait for each)
 #pragma unroll
-                        for (int e = 0; e < kStep; ++e)
-                            if (j0 + e < w.R) out[col_off[j0 + e]] = f2bf(o[e]);
+                        for (int e0 = 0; e0 < kStep; e0 += 8) {
+                            long long off[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) off[e] = col_off[j0 + e0 + e];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (j0 + e0 + e < w.R) out[off[e]] = f2bf(o[e0 + e]);
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < kStep; ++e)
