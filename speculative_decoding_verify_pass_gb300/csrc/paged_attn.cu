@@ -140,6 +140,20 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
            (2ull << 61);
 }
 
+// The upper half of such a descriptor (stride, version, swizzle).
+constexpr uint32_t hi_sw128(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+
+// D[tmem] (+)= A B^T with descriptors in halves: the upper one is a constant of the
+// operand's layout, so that stepping along k is one 32-bit addition.
+__device__ __forceinline__ void umma_lo(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // 8, 16 or 32 consecutive fp32 columns of this warp's 32 lanes, not waited for.
 __device__ __forceinline__ void tmem_ld8_async(uint32_t t, float* v) {
     uint32_t r[8];
@@ -633,17 +647,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     if (!ok || s.units == 0) break;
                     ok = wait(&q_full[qr.at], qr.round, deadp);
                     const uint32_t id = umma_idesc_bf16(128, (s.R + 15) & ~15);
-                    const uint64_t dq = desc_sw128(qa + qr.at * L::kQ, 16, 1024);
+                    const uint32_t dq = (uint32_t)desc_sw128(qa + qr.at * L::kQ, 16, 1024);
+                    constexpr uint32_t kHi = hi_sw128(1024);
 #pragma unroll 1
                     for (int k = 0; k < s.units && ok; ++k) {
                         ok = wait(&k_full[ks.at], ks.round, deadp) && wait(&s_empty[sb.at], sb.round ^ 1, deadp);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t dk = desc_sw128(sa + ks.at * L::kSlot, 16, 1024);
+                        const uint32_t dk = (uint32_t)desc_sw128(sa + ks.at * L::kSlot, 16, 1024);
 #pragma unroll
                         for (int e = 0; e < HD / 16; ++e)
-                            umma_bf16_id(tmem + sb.at * RP, dk + (e >> 2) * (kChunk * 128 >> 4) + (e & 3) * 2,
-                                         dq + (e >> 2) * (RP * 128 >> 4) + (e & 3) * 2, id, e > 0);
+                            umma_lo(tmem + sb.at * RP, dk + (e >> 2) * (kChunk * 128 >> 4) + (e & 3) * 2, kHi,
+                                    dq + (e >> 2) * (RP * 128 >> 4) + (e & 3) * 2, kHi, id, e > 0);
                         umma_commit(&s_full[sb.at]);
                         umma_commit(&k_empty[ks.at]);
                         ks.step();
@@ -676,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll 1
                     for (int k = 0; k < s.units && ok; ++k, ++j) {
                         ok = wait(&p_full[pr.at], pr.round, deadp);
-                        const uint64_t dp = umma_desc_kmajor(pa + pr.at * 2 * L::kP, 128, kChunk * 16);
+                        const uint32_t dp = (uint32_t)umma_desc_kmajor(pa + pr.at * 2 * L::kP, 128, kChunk * 16);
+                        constexpr uint32_t kHiV = hi_sw128(1024), kHiP = (kChunk * 16 >> 4) | (1u << 14);
                         const int og = kStream ? (seg & 1) * 2 + (j & 1) : seg & 1;
                         const uint32_t o = tmem + 2 * RP + og * L::kO;
                         const bool more = k >= kGroups;     // this O^T holds earlier chunks
@@ -685,14 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                             ok = ok && wait(&v_full[vs.at], vs.round, deadp);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint64_t dv = desc_sw128(sa + vs.at * L::kPiece, HD == 128 ? kPieceRows * 128 : 1024, 1024);
+                            const uint32_t dv = (uint32_t)desc_sw128(sa + vs.at * L::kPiece, HD == 128 ? kPieceRows * 128 : 1024, 1024);
 #pragma unroll
                             for (int part = 0; part < (kStack ? 1 : 2); ++part)
 #pragma unroll
                                 for (int e = 0; e < kPieceRows / 16; ++e)
-                                    umma_bf16_id(o, dv + e * (2048 >> 4),
-                                                 dp + part * (L::kP >> 4) + (v * (kPieceRows / 16) + e) * (256 >> 4), id,
-                                                 more || (v | part | e) != 0);
+                                    umma_lo(o, dv + e * (2048 >> 4), kHiV,
+                                            dp + part * (L::kP >> 4) + (v * (kPieceRows / 16) + e) * (256 >> 4), kHiP, id,
+                                            more || (v | part | e) != 0);
                             umma_commit(&v_empty[vs.at]);
                             vs.step();
                         }
