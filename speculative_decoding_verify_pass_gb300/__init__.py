@@ -10,7 +10,6 @@ raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import numpy as np
@@ -327,17 +326,21 @@ def spec_accept_from_logits_noalloc(d_logits, d_block, d_argmax, d_accept_len, s
 # ----------------------------------------------------------------------------
 # A paged cache shared by many sequences (no handle; the current torch stream)
 # ----------------------------------------------------------------------------
-# These calls run in serving loops, once per layer, so their host side is short:
-# one expression accepts what is right, and only when it does not hold does
-# _explain look for what is wrong.
-_torch = _I32 = _BF16 = None
+# The calls' host side is native (csrc/binding.cpp, _paged.so): it accepts what the
+# kernels can read, and only when it does not does _explain look for what is wrong.
+_torch = _native = None
 
 
-def _load_torch():
-    global _torch, _I32, _BF16
+def _load_native():
+    """torch and the native half of these calls (raises if it has not been built)."""
+    global _torch, _native
     import torch
-    _torch, _I32, _BF16 = torch, torch.int32, torch.bfloat16
-    return torch
+    library()
+    if not os.path.exists(os.path.join(_HERE, "_paged.so")):
+        raise RuntimeError("_paged.so is not built; run __graft_entry__.build() (the CUDA path has no fallback)")
+    from . import _paged
+    _torch, _native = torch, _paged
+    return _paged
 
 
 def _refuse(msg):
@@ -348,7 +351,7 @@ def _explain(call, i32=(), pools=(), rows=(), dims=()):
     """Raises for the first argument that is not what its call needs.  i32:
     (name, tensor, entries); pools: the key and the value pool; rows: (name,
     tensor, shape or None); dims: (name, tensor, dimensions, what they are)."""
-    T = _torch or _load_torch()
+    T = _torch
     tensors = [(n, t) for n, t, _ in i32] + [(n, t) for n, t, _ in rows] + list(zip(("d_kpool", "d_vpool"), pools))
     for name, t in tensors:
         if not isinstance(t, T.Tensor) or t.get_device() < 0 or t.get_device() != T._C._cuda_getDevice():
@@ -357,36 +360,25 @@ def _explain(call, i32=(), pools=(), rows=(), dims=()):
         if t.dim() != count:
             _refuse("%s: %s must be %s" % (call, name, what))
     for name, t, need in i32:
-        if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < need:
+        if t.dtype is not T.int32 or not t.is_contiguous() or t.numel() < need:
             _refuse("%s: %s must be a contiguous int32 tensor of at least %d entries" % (call, name, need))
     for name, t in zip(("d_kpool", "d_vpool"), pools):
-        if t.dtype is not _BF16 or not t.is_contiguous() or t.shape[2] != SPEC_PAGE or t.shape != pools[0].shape:
+        if t.dtype is not T.bfloat16 or not t.is_contiguous() or t.shape[2] != SPEC_PAGE or t.shape != pools[0].shape:
             _refuse("%s: %s must be a contiguous bfloat16 tensor [pages][kv heads][%d][head_dim], both pools alike"
                     % (call, name, SPEC_PAGE))
     for name, t, shape in rows:
-        if t.dtype is not _BF16 or tuple(t.shape) != tuple(shape):
+        if t.dtype is not T.bfloat16 or tuple(t.shape) != tuple(shape):
             _refuse("%s: %s must be a bfloat16 tensor %s" % (call, name, list(shape)))
-        if _row_stride(t) is None:
+        (_, s1, s2), (_, heads, hd) = t.stride(), t.shape
+        if (s2 != 1 and hd > 1) or (s1 != hd and heads > 1):
             _refuse("%s: the rows of %s must be contiguous [heads][head_dim] blocks" % (call, name))
-
-
-def _row_stride(t):
-    """Elements from a row of t [rows][heads][head_dim] to the next; None when
-    a row is not contiguous.  Rows may lie any distance apart; a stride over a
-    dimension of size one is not looked at."""
-    rows, heads, hd = t.shape
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and hd > 1) or (s1 != hd and heads > 1):
-        return None
-    return s0 if rows > 1 else heads * hd
 
 
 def spec_pages_init(d_pool):
     """All pages of d_pool (int32 [SPEC_POOL_HEADER + pages]) become free."""
-    T = _torch or _load_torch()
+    _native or _load_native()
     _explain("spec_pages_init", i32=(("d_pool", d_pool, SPEC_POOL_HEADER + 1),))
-    _check(library().spec_pages_init(d_pool.data_ptr(), d_pool.numel() - SPEC_POOL_HEADER,
-                                     T._C._cuda_getCurrentRawStream(d_pool.get_device())))
+    _check(library().spec_pages_init(d_pool.data_ptr(), d_pool.numel() - SPEC_POOL_HEADER, _stream()))
 
 
 def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots):
@@ -394,32 +386,14 @@ def spec_pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots
     int32 [nseq][table_pages], lengths, keep and add int32 [nseq]; writes
     row_start [nseq + 1] and the new rows' slots.  Errors that only the device
     can see land in d_pool[SPEC_POOL_ERROR]."""
-    T = _torch or _load_torch()
-    try:
-        nseq, width = d_tables.shape
-        dev = d_pool.get_device()
-        cap = d_slots.numel()
-        ok = (dev >= 0 and dev == T._C._cuda_getDevice() and d_pool.dtype is _I32 and d_tables.dtype is _I32
-              and d_len.dtype is _I32 and d_keep.dtype is _I32 and d_add.dtype is _I32 and d_row_start.dtype is _I32
-              and d_slots.dtype is _I32 and d_tables.get_device() == dev and d_len.get_device() == dev
-              and d_keep.get_device() == dev and d_add.get_device() == dev and d_row_start.get_device() == dev
-              and d_slots.get_device() == dev and d_pool.is_contiguous() and d_tables.is_contiguous()
-              and d_len.is_contiguous() and d_keep.is_contiguous() and d_add.is_contiguous()
-              and d_row_start.is_contiguous() and d_slots.is_contiguous() and d_pool.numel() > SPEC_POOL_HEADER
-              and d_len.numel() >= nseq and d_keep.numel() >= nseq and d_add.numel() >= nseq
-              and d_row_start.numel() > nseq)
-    except (AttributeError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    st = (_native or _load_native()).pages_step(d_pool, d_tables, d_len, d_keep, d_add, d_row_start, d_slots)
+    if st < 0:
         _explain("spec_pages_step", i32=(("d_pool", d_pool, SPEC_POOL_HEADER + 1), ("d_tables", d_tables, 0)),
                  dims=(("d_tables", d_tables, 2, "[nseq][table_pages]"),))
         n = d_tables.shape[0]
         _explain("spec_pages_step", i32=(("d_len", d_len, n), ("d_keep", d_keep, n), ("d_add", d_add, n),
                                          ("d_row_start", d_row_start, n + 1), ("d_slots", d_slots, 0)))
-        _refuse("spec_pages_step: bad arguments")
-    st = library().spec_pages_step(d_pool.data_ptr(), d_pool.numel() - SPEC_POOL_HEADER, d_tables.data_ptr(), width,
-                                   d_len.data_ptr(), d_keep.data_ptr(), d_add.data_ptr(), nseq, d_row_start.data_ptr(),
-                                   d_slots.data_ptr(), cap, T._C._cuda_getCurrentRawStream(dev))
+        _refuse("spec_pages_step: an argument has more than 2147483647 entries")
     if st:
         _check(st)
 
@@ -428,37 +402,17 @@ def spec_paged_append(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_error=
     """Write the rows of d_k and d_v (bf16 [rows][kv heads][head_dim], rows any
     distance apart) at their slots; only rows below the device int32
     d_row_count (None: all)."""
-    T = _torch or _load_torch()
-    try:
-        pages, heads, page, hd = d_kpool.shape
-        rows = d_k.shape[0]
-        dev = d_k.get_device()
-        ks, vs = _row_stride(d_k), _row_stride(d_v)
-        ok = (dev >= 0 and dev == T._C._cuda_getDevice() and page == SPEC_PAGE and d_k.dtype is _BF16 and d_v.dtype is _BF16
-              and d_kpool.dtype is _BF16 and d_vpool.dtype is _BF16 and d_slots.dtype is _I32 and ks is not None
-              and vs is not None and d_k.shape == (rows, heads, hd) and d_v.shape == d_k.shape
-              and d_vpool.shape == d_kpool.shape and d_v.get_device() == dev and d_kpool.get_device() == dev
-              and d_vpool.get_device() == dev and d_slots.get_device() == dev and d_kpool.is_contiguous()
-              and d_vpool.is_contiguous() and d_slots.is_contiguous() and d_slots.numel() >= rows)
-        for t in (d_row_count, d_error):
-            if t is not None:
-                ok = ok and t.dtype is _I32 and t.get_device() == dev and t.is_contiguous() and t.numel() > 0
-    except (AttributeError, TypeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    st = (_native or _load_native()).paged_append(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_error)
+    if st < 0:
         more = tuple((n, t, 1) for n, t in (("d_row_count", d_row_count), ("d_error", d_error)) if t is not None)
         _explain("spec_paged_append", pools=(d_kpool, d_vpool), i32=(("d_slots", d_slots, 0),) + more,
                  dims=(("d_kpool", d_kpool, 4, "4-D"), ("d_vpool", d_vpool, 4, "4-D")))
         for name, t in (("d_k", d_k), ("d_v", d_v)):
-            if not isinstance(t, T.Tensor) or t.dim() != 3:
+            if not isinstance(t, _torch.Tensor) or t.dim() != 3:
                 _refuse("spec_paged_append: %s must be [rows][kv heads][head_dim]" % name)
         want = (d_k.shape[0], d_kpool.shape[1], d_kpool.shape[3])
         _explain("spec_paged_append", rows=(("d_k", d_k, want), ("d_v", d_v, want)), i32=(("d_slots", d_slots, want[0]),))
-        _refuse("spec_paged_append: bad arguments")
-    st = library().spec_paged_append(d_k.data_ptr(), ks, d_v.data_ptr(), vs, d_slots.data_ptr(),
-                                     None if d_row_count is None else d_row_count.data_ptr(), rows, heads, hd,
-                                     d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
-                                     None if d_error is None else d_error.data_ptr(), T._C._cuda_getCurrentRawStream(dev))
+        _refuse("spec_paged_append: an argument has more than 2147483647 entries")
     if st:
         _check(st)
 
@@ -472,79 +426,33 @@ def spec_paged_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int,
     return int(out.value)
 
 
-@functools.lru_cache(maxsize=256)
-def _work_bytes(dev, n_heads, n_kv_heads, head_dim, max_new, table_pages):
-    return spec_paged_attention_workspace(n_heads, n_kv_heads, head_dim, max_new, table_pages)
-
-
 def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, max_new, scale=None, d_out=None,
                          d_error=None, d_work=None):
     """Attention of each sequence's newest rows over its pages; returns d_out
     (bf16 [rows][heads][head_dim]; a new tensor when None, whose rows outside
     every sequence are then unset).  scale defaults to head_dim ** -0.5; d_work
     (a uint8 tensor) to scratch from torch's allocator."""
-    T = _torch or _load_torch()
-    try:
-        pages, hkv, page, hd = d_kpool.shape
-        rows, hq, qd = d_q.shape
-        nseq, width = d_tables.shape
-        dev = d_q.get_device()
-        qs = _row_stride(d_q)
-        ok = (dev >= 0 and dev == T._C._cuda_getDevice() and page == SPEC_PAGE and qd == hd and qs is not None
-              and d_q.dtype is _BF16 and d_kpool.dtype is _BF16 and d_vpool.dtype is _BF16 and d_tables.dtype is _I32
-              and d_len.dtype is _I32 and d_row_start.dtype is _I32 and d_vpool.shape == d_kpool.shape
-              and d_kpool.get_device() == dev and d_vpool.get_device() == dev and d_tables.get_device() == dev
-              and d_len.get_device() == dev and d_row_start.get_device() == dev and d_kpool.is_contiguous()
-              and d_vpool.is_contiguous() and d_tables.is_contiguous() and d_len.is_contiguous()
-              and d_row_start.is_contiguous() and d_len.numel() >= nseq and d_row_start.numel() > nseq)
-        if d_error is not None:
-            ok = (ok and d_error.dtype is _I32 and d_error.get_device() == dev and d_error.is_contiguous()
-                  and d_error.numel() > 0)
-        os_ = hq * qd
-        if d_out is not None:
-            os_ = _row_stride(d_out)
-            ok = (ok and os_ is not None and d_out.dtype is _BF16 and d_out.get_device() == dev
-                  and d_out.shape == d_q.shape)
-        if d_work is not None:
-            ok = ok and d_work.dtype is T.uint8 and d_work.get_device() == dev and d_work.is_contiguous()
-    except (AttributeError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    native = _native or _load_native()
+    out = native.paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, max_new, scale, d_out, d_error, d_work)
+    if out.__class__ is not int:
+        return out
+    if out < 0:
         more = () if d_error is None else (("d_error", d_error, 1),)
         _explain("spec_paged_attention", pools=(d_kpool, d_vpool), i32=(("d_tables", d_tables, 0),) + more,
                  dims=(("d_kpool", d_kpool, 4, "4-D"), ("d_vpool", d_vpool, 4, "4-D"),
                        ("d_tables", d_tables, 2, "[nseq][table_pages]")))
         n = d_tables.shape[0]
         _explain("spec_paged_attention", i32=(("d_row_start", d_row_start, n + 1), ("d_len", d_len, n)))
-        if not isinstance(d_q, T.Tensor) or d_q.dim() != 3:
+        if not isinstance(d_q, _torch.Tensor) or d_q.dim() != 3:
             _refuse("spec_paged_attention: d_q must be [rows][heads][head_dim]")
         want = (d_q.shape[0], d_q.shape[1], d_kpool.shape[3])
         for name, t in (("d_q", d_q), ("d_out", d_out)):
             if t is not None:
                 _explain("spec_paged_attention", rows=((name, t, want),))
-        _refuse("spec_paged_attention: d_work must be a contiguous uint8 tensor on the current CUDA device")
-    max_new = min(int(max_new), 0x7fffffff)
-    if d_out is None:
-        d_out = T.empty((rows, hq, hd), dtype=_BF16, device=d_q.device)
-    stream = T._C._cuda_getCurrentRawStream(dev)
-    work, work_bytes, own = None, 0, None
-    if d_work is not None:
-        work, work_bytes = d_work.data_ptr(), d_work.numel()
-    else:
-        work_bytes = _work_bytes(dev, hq, hkv, hd, max_new, width)
-        if work_bytes:   # from torch's allocator, given back in the stream's order as a tensor would be
-            work = own = T._C._cuda_cudaCachingAllocator_raw_alloc(work_bytes, stream)
-    try:
-        st = library().spec_paged_attention(
-            d_q.data_ptr(), qs, d_row_start.data_ptr(), d_len.data_ptr(), d_tables.data_ptr(), width, nseq, rows, max_new,
-            hq, hkv, hd, hd ** -0.5 if scale is None else float(scale), d_kpool.data_ptr(), d_vpool.data_ptr(), pages,
-            d_out.data_ptr(), os_, None if d_error is None else d_error.data_ptr(), work, work_bytes, stream)
-    finally:
-        if own is not None:
-            T._C._cuda_cudaCachingAllocator_raw_delete(own)
-    if st:
-        _check(st)
-    return d_out
+        if d_work is not None:
+            _refuse("spec_paged_attention: d_work must be a contiguous uint8 tensor on the current CUDA device")
+        _refuse("spec_paged_attention: an argument has more than 2147483647 entries")
+    _check(out)
 
 
 # ----------------------------------------------------------------------------

@@ -1,21 +1,25 @@
-"""Builds libspecverify.so (sm_103a) in-tree with nvcc.
+"""Builds libspecverify.so (sm_103a) in-tree with nvcc, and beside it _paged.so,
+the native half of the Python binding of the paged-cache calls, with g++.
 
-Each CUDA translation unit compiles in parallel; the shared library links
-against the shared CUDA runtime so it uses the same runtime instance as the
-process's PyTorch.
+Each translation unit compiles in parallel; the shared library links against
+the shared CUDA runtime so it uses the same runtime instance as the process's
+PyTorch, and the binding against both.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
+BINDING = os.path.join(HERE, "_paged.so")
 SOURCES = ["gemm.cu", "attention.cu", "misc.cu", "api.cu", "noalloc.cu", "sampling.cu", "pages.cu",
            "paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -32,9 +36,9 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "spec.h"),
                                                                 os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
@@ -57,6 +61,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         objs.append(obj)
         cmd = [cc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    bobj = os.path.join(objdir, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(cc)), "include"),
+           "-I", os.path.join(ROOT, "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", bobj]
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -67,13 +78,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             failed.append((cmd, text))
     if failed:
         msg = "\n".join("$ %s\n%s" % (" ".join(c), t) for c, t in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
+        raise RuntimeError("compilation failed:\n" + msg)
     tmp = LIB + ".tmp%d" % os.getpid()
     link = [cc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + ["-Xlinker", "-rpath,/usr/local/cuda/lib64"]
     r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    torch_lib = os.path.join(torch_dir, "lib")
+    link = ["g++", "-shared", "-o", tmp, bobj, "-L" + HERE, "-l:libspecverify.so", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
+            "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+    os.replace(tmp, BINDING)
     shutil.rmtree(objdir, ignore_errors=True)
     return LIB
 
