@@ -380,7 +380,7 @@ template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <int HD, int RP>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_kernel(const __grid_constant__ PagedParams p) {
     using L = Plan<HD, RP>;
     constexpr bool kStream = L::kStream, kStack = L::kStack;
     constexpr int NK = L::NK, NV = L::NV, NP = L::NP, NQ = L::NQ;

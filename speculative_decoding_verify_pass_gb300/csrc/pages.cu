@@ -22,7 +22,7 @@
 namespace sv {
 namespace {
 
-constexpr int kStepThreads = 1024;    // one sequence per thread
+constexpr int kStepThreads = 1024, kFewThreads = 128;   // one sequence per thread
 static_assert(kStepThreads >= SPEC_MAX_SEQS, "one sequence per thread");
 constexpr int kPoolTicket = 2;        // header word: CTAs done (0 between launches)
 
@@ -67,10 +67,11 @@ __device__ __forceinline__ int owner(const int* s, int nseq, int i) {
 // rows) are dealt to all CTAs' threads.  The last CTA to finish (ticket in the
 // pool's header, back at zero afterwards) writes the lengths and the header,
 // which every CTA has read by then.
-__global__ void __launch_bounds__(kStepThreads) pages_step_kernel(const __grid_constant__ StepParams p) {
-    __shared__ int rel[SPEC_MAX_SEQS + 1], alc[SPEC_MAX_SEQS + 1], row[SPEC_MAX_SEQS + 1];
-    __shared__ int held[SPEC_MAX_SEQS], need[SPEC_MAX_SEQS], keep[SPEC_MAX_SEQS];
-    __shared__ Sum3 part[kStepThreads / 32];
+template <int T>
+__global__ void __launch_bounds__(T) pages_step_kernel(const __grid_constant__ StepParams p) {
+    __shared__ int rel[T + 1], alc[T + 1], row[T + 1];
+    __shared__ int held[T], need[T], keep[T];
+    __shared__ Sum3 part[T / 32];
     __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -102,17 +103,17 @@ __global__ void __launch_bounds__(kStepThreads) pages_step_kernel(const __grid_c
     if (lane == 31) part[warp] = inc;
     const int bad = __syncthreads_or(code);
     if (warp == 0) {
-        Sum3 w = part[lane];
+        Sum3 w = part[lane < T / 32 ? lane : 0];
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+        for (int d = 1; d < T / 32; d <<= 1) {
             const Sum3 o = shfl_up(w, d);
             if (lane >= d) w = w + o;
         }
-        part[lane] = w;
+        if (lane < T / 32) part[lane] = w;
     }
     __syncthreads();
     if (warp > 0) inc = inc + part[warp - 1];
-    const Sum3 all = part[kStepThreads / 32 - 1];
+    const Sum3 all = part[T / 32 - 1];
     const int count = p.pool[SPEC_POOL_FREE];
     int err = bad;
     if (!err && all.rows > p.row_cap) err = SPEC_PAGED_BAD_ROWS;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kStepThreads) pages_step_kernel(const __grid_c
     if (!err) {
         int* stack = p.pool + SPEC_POOL_HEADER;
         const int R = all.rel, A = all.alc;
-        const int t0 = blockIdx.x * kStepThreads + tid, step = gridDim.x * kStepThreads;
+        const int t0 = blockIdx.x * T + tid, step = gridDim.x * T;
         constexpr int kGroup = 4;
         const bool aligned = (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0;
         auto entry = [&](int q, int j) -> int& { return p.tables[(size_t)q * p.table_pages + j]; };
@@ -298,14 +299,18 @@ spec_status spec_pages_step(int32_t* d_pool, int32_t num_pages, int32_t* d_table
         misaligned(d_add, 4) || misaligned(d_row_start, 4) || misaligned(d_slots, 4))
         return bad("spec_pages_step: a pointer is not 4-byte aligned");
     StepParams p{d_pool, num_pages, d_tables, table_pages, d_len, d_keep, d_add, nseq, d_row_start, d_slots, row_cap};
-    // one CTA up to 4096 rows (4 a thread), then more, up to two per SM: the 2 million
-    // slots of 1024 prompts take 9.7 us (16.3 with one row a thread step on 128 CTAs);
-    // a verify cycle of 200 sequences 3.9 us and one sequence 2.8, which is the launch,
-    // a round trip for the lengths and the sums
+    // Few sequences and rows: a small CTA starts and synchronises sooner (30 or 128
+    // sequences of 4 rows 3.0 us against 3.5 with 1024 threads, one sequence 2.5
+    // against 2.9).  Else one CTA up to 4096 rows (4 a thread), then more, up to two
+    // per SM: the 2 million slots of 1024 prompts take 9.7 us (16.3 with one row a
+    // thread step on 128 CTAs), a verify cycle of 200 sequences 3.8.
+    void* args[] = {&p};
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    if (nseq <= kFewThreads && row_cap <= 4 * kFewThreads)
+        return done(launch((const void*)pages_step_kernel<kFewThreads>, 1, kFewThreads, s, args));
     int grid = row_cap / (4 * kStepThreads) + (row_cap % (4 * kStepThreads) != 0);
     grid = grid < 1 ? 1 : grid > 304 ? 304 : grid;
-    void* args[] = {&p};
-    return done(launch((const void*)pages_step_kernel, (unsigned)grid, kStepThreads, static_cast<cudaStream_t>(cuda_stream), args));
+    return done(launch((const void*)pages_step_kernel<kStepThreads>, (unsigned)grid, kStepThreads, s, args));
 }
 
 spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_slots,
