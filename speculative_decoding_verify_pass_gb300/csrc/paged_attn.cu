@@ -52,6 +52,7 @@ constexpr float kLimit = 40.f;          // log2 by which a score may exceed its 
 constexpr float kNone = -1e30f;         // reference of a row that has seen no key
 constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
 constexpr int kSegs = 4;                    // segments listed ahead
+constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
 
 // A segment, as the roles need it.
 struct Seg {
@@ -283,18 +284,20 @@ struct Ring {
 struct Walk {
     const PagedParams& p;
     const int* first;           // [nseq + 1] in shared memory
+    const int *start, *lens;    // row starts and lengths: in shared memory when they are few
     int u, end;                 // next unit, end of the CTA's range
     int q = 0, q1 = 0;          // sequence, the end of its units
     int rows = 0, len = 0, row_base = 0, chunks = 1;
     // the segment
     int head = 0, block = 0, c0 = 0, c1 = 0, R = 0, seg = -1;
 
-    __device__ Walk(const PagedParams& pp, const int* f, int begin, int e) : p(pp), first(f), u(begin), end(e) {}
+    __device__ Walk(const PagedParams& pp, const int* f, const int* s, const int* n, int begin, int e)
+        : p(pp), first(f), start(s), lens(n), u(begin), end(e) {}
     __device__ __forceinline__ void sequence() {
         q1 = first[q + 1];
-        row_base = p.row_start[q];
-        rows = p.row_start[q + 1] - row_base;
-        len = p.len[q];
+        row_base = start[q];
+        rows = start[q + 1] - row_base;
+        len = lens[q];
         chunks = split::chunks_of(len);
     }
     __device__ __forceinline__ bool next() {
@@ -399,6 +402,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
     __shared__ int dead, total;
     __shared__ int poison[2];                           // 1 + the last segment (by parity) that silenced a value
     __shared__ int first[split::kMaxSeqs + 1];
+    __shared__ int few_start[kFewSeqs + 1], few_len[kFewSeqs];   // a batch this small is not read from memory twice
     __shared__ long long warp_sum[kWarps];
     __shared__ __align__(16) Seg segs[kSegs];
     __shared__ __align__(16) float nref[2][kGroups][RP];    // by segment parity: minus each row's reference
@@ -471,6 +475,11 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                 const int r0 = p.row_start[q], r1 = p.row_start[q + 1], n = p.len[q];
                 const bool bad_rows = r0 < 0 || r1 < r0 || r1 > p.rows;
                 const bool bad_len = n < 0 || n > (long long)p.table_pages * SPEC_PAGE;
+                if (p.nseq <= kFewSeqs) {
+                    few_start[q] = r0;
+                    few_start[q + 1] = r1;      // the next sequence's r0, the same word
+                    few_len[q] = n;
+                }
                 if (bad_rows || bad_len) {
                     if (blockIdx.x == 0 && p.err) atomicCAS(p.err, 0, bad_rows ? SPEC_PAGED_BAD_ROWS : SPEC_PAGED_BAD_LENGTH);
                 } else {
@@ -480,8 +489,8 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
             sum += v[k];
         }
         long long inc = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll 1
+        for (int d = 1; d < 32 && 2 * d < p.nseq; d <<= 1) {   // as far as there are sequences
             const long long o = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += o;
         }
@@ -523,7 +532,8 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
         regs_down<L::kIssueRegs>();
         if (warp == kLoadKWarp) {
             // ---------------- the list of segments, Q and K copies, and what the join kernel has to do here ----------------
-            Walk w(p, first, begin, end);
+            const bool few = p.nseq <= kFewSeqs;
+            Walk w(p, first, few ? few_start : p.row_start, few ? few_len : p.len, begin, end);
             Meta into = {}, from = {};
             Ring<NK> kr;
             Ring<NQ> qr;
