@@ -630,7 +630,7 @@ def test_cycles_of_step_append_attention():
 def test_cycles_replayed_from_a_graph():
     """One captured cycle, replayed with other lengths, accepts and rows."""
     torch = torch_cuda()
-    cyc = Cycle(5, 16, 4, 128, 60, 12, 400, 3)
+    cyc = Cycle(5, 12, 4, 128, 60, 12, 400, 3)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
