@@ -464,6 +464,11 @@ spec_status spec_pages_init(int32_t* d_pool, int32_t num_pages, void* cuda_strea
  * All or nothing: with a bad length, more than row_cap rows or too few free
  * pages the call sets d_pool[SPEC_POOL_ERROR] and d_row_start to zeros (later
  * calls of the cycle then find no rows) and changes nothing else.
+ * A page outside the pool among the entries that the call reads (those given
+ * back, those that new rows fall on) or on the stack sets the error to
+ * SPEC_PAGED_BAD_PAGE; rows on it get slots behind the pool, which
+ * spec_paged_append refuses, and the rest is done.  A page belongs to one
+ * sequence: one that two rows of d_tables hold would be given back twice.
  * 0 <= nseq <= SPEC_MAX_SEQS (0: nothing is done); 1 <= table_pages <=
  * SPEC_MAX_TABLE; row_cap >= 0 (d_slots may be NULL when 0).  Calls on one pool
  * must not overlap.  Errors: SPEC_ERR_INVALID_ARG, nothing enqueued. */

@@ -145,7 +145,18 @@ __global__ void __launch_bounds__(T) pages_step_kernel(const __grid_constant__ S
             const int at = count + R - 1 - k;
             return at < count ? stack[at] : released(at - count);
         };
-        for (int i = t0; i < R; i += step) stack[count + i] = released(i);
+        // a page as the slots use it: one outside the pool is reported, and its slots lie
+        // behind the pool, where the append refuses them (page * 64 could wrap into it)
+        auto checked = [&](int page) {
+            if ((unsigned)page < (unsigned)p.num_pages) return page;
+            atomicCAS(p.pool + SPEC_POOL_ERROR, 0, SPEC_PAGED_BAD_PAGE);
+            return p.num_pages;
+        };
+        for (int i = t0; i < R; i += step) {
+            const int page = released(i);
+            stack[count + i] = page;
+            checked(page);
+        }
         for (int k = t0; k < A; k += step) {
             const int q = owner(alc, p.nseq, k);
             entry(q, held[q] + k - alc[q]) = taken(k);
@@ -167,7 +178,7 @@ __global__ void __launch_bounds__(T) pages_step_kernel(const __grid_constant__ S
                 const int pos = keep[q] + r0 + e - row[q], j = pos / SPEC_PAGE;
                 if (j != at) {
                     at = j;
-                    base = (j < held[q] ? entry(q, j) : taken(alc[q] + j - held[q])) * SPEC_PAGE;
+                    base = checked(j < held[q] ? entry(q, j) : taken(alc[q] + j - held[q])) * SPEC_PAGE;
                 }
                 slot[e] = base + pos % SPEC_PAGE;
             }

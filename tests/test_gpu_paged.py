@@ -163,6 +163,50 @@ def test_init_hands_out_page_zero_first():
     assert dev.tables.tolist() == [[0, 1, 2, 0]]
 
 
+@pytest.mark.parametrize("page", [-1, -2 ** 31, 9, 2 ** 25, 2 ** 26 + 3, 2 ** 31 - 1])
+@pytest.mark.parametrize("nseq", [3, 1024])
+def test_step_reports_pages_outside_the_pool(page, nseq):
+    """A bad page that is held, taken or given back is reported, no slot on it lies in the
+    pool (2^26 + 3 times 64 is 192 in 32 bits), and the append writes nothing through it."""
+    sv = sv_()
+    torch = torch_cuda()
+    lens, rows = [60, 70, 64] + [0] * (nseq - 3), 30000 if nseq > 3 else 300
+
+    def fresh():
+        dev = DevicePool(9, nseq, 3, 0, rows)
+        dev.step(i32([0] * nseq), i32(lens))
+        assert dev.pool[1].item() == 0
+        dev.slots.fill_(-9)
+        return dev
+
+    dev = fresh()                              # held: the entry that sequence 1's new rows fall on
+    dev.tables[1, 1] = page
+    dev.step(dev.len, i32([2, 3, 1] + [0] * (nseq - 3)))
+    assert dev.pool[1].item() == sv.SPEC_PAGED_BAD_PAGE
+    assert dev.start.tolist() == [0, 2, 5] + [6] * (nseq - 2)
+    slots = dev.slots.tolist()
+    assert slots[:2] == [60, 61] and slots[5] == 4 * 64 and slots[6:] == [-9] * (rows - 6)
+    assert all(s >= 9 * 64 for s in slots[2:5])
+    assert dev.len.tolist() == [62, 73, 65] + [0] * (nseq - 3)
+    k = torch.ones((6, 1, 64), dtype=torch.bfloat16, device="cuda")
+    kp = torch.zeros((9, 1, PAGE, 64), dtype=torch.bfloat16, device="cuda")
+    vp, err = torch.zeros_like(kp), i32([0])
+    sv.spec_paged_append(k, k, dev.slots[:6], dev.start[nseq:], kp, vp, err)
+    assert err.item() == sv.SPEC_PAGED_BAD_PAGE
+    assert kp.sum().item() == 3 * 64 and torch.equal(kp, vp)
+
+    dev = fresh()                              # taken: the top of the stack
+    dev.pool[HEADER + dev.pool[0].item() - 1] = page
+    dev.step(dev.len, i32([0, 0, 2] + [0] * (nseq - 3)))
+    assert dev.pool[1].item() == sv.SPEC_PAGED_BAD_PAGE
+    assert all(s >= 9 * 64 for s in dev.slots.tolist()[:2])
+
+    dev = fresh()                              # given back
+    dev.tables[1, 1] = page
+    dev.step(i32([60, 3, 64] + [0] * (nseq - 3)), i32([0] * nseq))
+    assert dev.pool[1].item() == sv.SPEC_PAGED_BAD_PAGE and dev.pool[0].item() == 6
+
+
 # ----------------------------------------------------------------- append ---
 @pytest.mark.parametrize("rows,hkv,hd,count,fused", [(1, 1, 64, None, False), (3, 8, 128, 2, True), (77, 5, 64, 77, True),
                                                      (1000, 8, 128, 999, False), (5000, 2, 128, 9000, True), (6, 3, 64, 0, False),
