@@ -437,6 +437,19 @@ def test_attention_rising_scores():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("exponent", [60, -100])
+def test_attention_large_and_small_values(exponent):
+    """Values of 2^60 under a weight of about 2^32 times the first key's, and of 2^-100."""
+    c = Case([700], [2], 8, 2, 128, seed=12)
+    c.v[0] *= 2.0 ** exponent
+    c.d["vp"] *= 2.0 ** exponent
+    for h in range(2):
+        k = c.k[0][300].clone()
+        k[h] = (0.5 * c.q[0].view(2, 4, 128)[h, 0].float()).bfloat16()
+        c.put(0, 300, k=k)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("n", [130, 136, 128, 300])
