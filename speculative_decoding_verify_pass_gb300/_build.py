@@ -1,5 +1,6 @@
 """Builds libspecverify.so (sm_103a) in-tree with nvcc, and beside it _paged.so,
 the native half of the Python binding of the paged-cache calls, with g++.
+Without torch the library is built alone: users of the C ABI need no torch.
 
 Each translation unit compiles in parallel; the shared library links against
 the shared CUDA runtime so it uses the same runtime instance as the process's
@@ -35,10 +36,18 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the library")
 
 
+def _torch_dir():
+    """Where a torch with CUDA is installed (it is not imported); None without one."""
+    spec = importlib.util.find_spec("torch")
+    path = os.path.dirname(spec.origin) if spec and spec.origin else None
+    return path if path and os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    built = [LIB, BINDING] if _torch_dir() else [LIB]
+    if not all(os.path.exists(p) for p in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(p) for p in built)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "spec.h"),
                                                                 os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
@@ -54,45 +63,53 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     cc = nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", CSRC,
                     "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"] + list(extra_flags or [])
+    def start(cmd):
+        return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+    def finish(procs):
+        failed = []
+        for cmd, p in procs:
+            out, _ = p.communicate()
+            text = out.decode(errors="replace")
+            if verbose and text.strip():
+                sys.stdout.write(text)
+            if p.returncode != 0:
+                failed.append((cmd, text))
+        if failed:
+            raise RuntimeError("compilation failed:\n" + "\n".join("$ %s\n%s" % (" ".join(c), t) for c, t in failed))
+
     procs = []
     objs = []
     for src in SOURCES:
         obj = os.path.join(objdir, src.replace(".cu", ".o"))
         objs.append(obj)
         cmd = [cc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+        procs.append(start(cmd))
+    torch_dir = _torch_dir()
     bobj = os.path.join(objdir, "binding.o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(torch_dir, "include"),
-           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(cc)), "include"),
-           "-I", os.path.join(ROOT, "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", bobj]
-    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    for cmd, p in procs:
-        out, _ = p.communicate()
-        text = out.decode(errors="replace")
-        if verbose and text.strip():
-            sys.stdout.write(text)
-        if p.returncode != 0:
-            failed.append((cmd, text))
-    if failed:
-        msg = "\n".join("$ %s\n%s" % (" ".join(c), t) for c, t in failed)
-        raise RuntimeError("compilation failed:\n" + msg)
+    if torch_dir:
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(torch_dir, "include"),
+               "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(cc)), "include"),
+               "-I", os.path.join(ROOT, "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", bobj]
+        binding = start(cmd)
+    finish(procs)
     tmp = LIB + ".tmp%d" % os.getpid()
     link = [cc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + ["-Xlinker", "-rpath,/usr/local/cuda/lib64"]
     r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
-    tmp = BINDING + ".tmp%d" % os.getpid()
-    torch_lib = os.path.join(torch_dir, "lib")
-    link = ["g++", "-shared", "-o", tmp, bobj, "-L" + HERE, "-l:libspecverify.so", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
-            "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
-    r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-    os.replace(tmp, BINDING)
+    if torch_dir:                               # after the library, which stands without it
+        finish([binding])
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        torch_lib = os.path.join(torch_dir, "lib")
+        link = ["g++", "-shared", "-o", tmp, bobj, "-L" + HERE, "-l:libspecverify.so", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
+                "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+        r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+        os.replace(tmp, BINDING)
     shutil.rmtree(objdir, ignore_errors=True)
     return LIB
 
