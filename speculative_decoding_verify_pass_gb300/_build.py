@@ -43,10 +43,26 @@ def _torch_dir():
     return path if path and os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
 
 
+def _stamp() -> str:
+    return os.path.join(BUILD, "paged.abi")
+
+
+def _abi(torch_dir) -> str:
+    """What _paged.so is compiled against and its sources' times do not show (kept in
+    _stamp()): the interpreter's ABI and the torch that is installed."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "%s %s\n%s" % (sysconfig.get_config_var("SOABI"), torch_dir, f.read())
+
+
 def _stale() -> bool:
-    built = [LIB, BINDING] if _torch_dir() else [LIB]
+    torch_dir = _torch_dir()
+    built = [LIB, BINDING, _stamp()] if torch_dir else [LIB]
     if not all(os.path.exists(p) for p in built):
         return True
+    if torch_dir:
+        with open(_stamp()) as f:
+            if f.read() != _abi(torch_dir):
+                return True
     t = min(os.path.getmtime(p) for p in built)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "spec.h"),
                                                                 os.path.abspath(__file__)]
@@ -110,6 +126,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
         os.replace(tmp, BINDING)
+        tmp = os.path.join(objdir, "paged.abi")
+        with open(tmp, "w") as f:
+            f.write(_abi(torch_dir))
+        os.replace(tmp, _stamp())
     shutil.rmtree(objdir, ignore_errors=True)
     return LIB
 

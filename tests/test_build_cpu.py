@@ -87,3 +87,36 @@ def test_a_source_that_fails_is_reported(tools):
     with pytest.raises(RuntimeError, match="pages.cu"):
         _build.build()
     assert not os.path.exists(_build.LIB)
+
+
+@pytest.mark.parametrize("what", ["torch", "python", "place"])
+def test_a_binding_of_another_torch_or_python_is_rebuilt(tools, monkeypatch, tmp_path, what):
+    """No source changes, but the ABI that _paged.so was compiled for does."""
+    root = tmp_path / "site" / "torch"
+    (root / "lib").mkdir(parents=True)
+    (root / "lib" / "libc10_cuda.so").write_text("")
+    (root / "version.py").write_text("__version__ = '2.9.1'\n")
+    (root / "__init__.py").write_text("")
+    place = [root]
+    find = importlib.util.find_spec
+
+    class Spec:
+        @property
+        def origin(self):
+            return str(place[0] / "__init__.py")
+    monkeypatch.setattr(_build.importlib.util, "find_spec", lambda name, *a: Spec() if name == "torch" else find(name, *a))
+    _build.build()
+    n = len(tools.commands)
+    _build.build()
+    assert len(tools.commands) == n and os.path.exists(_build.BINDING)
+    if what == "torch":
+        (root / "version.py").write_text("__version__ = '2.11.0'\n")
+    elif what == "python":
+        monkeypatch.setattr(_build.sysconfig, "get_config_var", lambda name: "cpython-313-other")
+    else:
+        place[0] = root.rename(tmp_path / "site" / "torch2")
+    _build.build()
+    assert made(tools.commands[n:], _build.BINDING)
+    n = len(tools.commands)
+    _build.build()
+    assert len(tools.commands) == n
