@@ -59,6 +59,7 @@ using split::kChunk;
 
 constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12, kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
+constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -1e30f;         // reference of a row that has seen no key
 constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
@@ -755,7 +756,6 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
         const int col0 = kStream ? 0 : wg * NC; // the thread's first row
         const int gi = kStream ? wg : 0;        // its reference and O^T
         const int bar = kSoftBar + wg;
-        const F2 k2(p.scale_log2, p.scale_log2);
         int i = 0;                              // unit
         Ring<NV> vs;                            // slot of the next unit's V
         bool ok = true;
@@ -769,7 +769,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
             F2 l[NC / 2];
 #pragma unroll
             for (int j = 0; j < NC / 2; ++j) l[j] = F2(0.f, 0.f);
-            bool fresh = true;
+            bool fresh = true, wide = false;   // wide: a reference past 2^24, every chunk takes its scores again
 #pragma unroll 1
             for (int c = w.c0; c < w.c0 + w.units; ++c, ++i) {
                 const Ring<NV> v0 = vs;         // the slots of the chunk's V: its first page's,
@@ -806,6 +806,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                             if (j < hidden) s[j] = -INFINITY;
                     }
                     if (rows <= 0) break;
+                    bool big = wide;
                     if (fresh) {                // references: the scores of the chunk's first key
                         if (key == 0) {
 #pragma unroll
@@ -816,9 +817,12 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                         if (key < NC) {
                             const float m = mine[col0 + key] * p.scale_log2;
                             mine[col0 + key] = key >= rows ? -INFINITY : m > kNone ? -m : -kNone;   // rows past R weigh nothing
+                            big = fabsf(m) > kWide && m > kNone && key < rows;
                         }
                         named_bar_sync(bar, 128);
                     }
+                    const float k = moved ? 1.f : p.scale_log2;
+                    const F2 k2(k, k);
                     float top[2] = {kNone, kNone};
 #pragma unroll
                     for (int j0 = 0; j0 < NC; j0 += kSpan)
@@ -831,9 +835,12 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                                 top[j / 4 & 1] = fmaxf(top[j / 4 & 1], fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
                             }
                         }
-                    if (moved || !bar_any(bar, 128, fmaxf(top[0], top[1]) > kLimit)) break;
+                    if (moved || !bar_any(bar, 128, big || fmaxf(top[0], top[1]) > kLimit)) break;
                     // The references move up to the chunk's maxima, the sums and O^T
-                    // with them, and the scores are taken again.
+                    // with them, and the scores are taken again.  So that a reference and the
+                    // score that it comes from cancel whatever their size, the scores are then
+                    // rounded products, as it is: the fused product of a score past 2^24 differs
+                    // from it by powers of two, past 2^31 by more than a weight can hold.
                     product_done();
                     tc_fence_after();
                     float (*const mx)[RP] = xl[par][gi];
@@ -843,20 +850,26 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                         tmem_ld8_async(st + j, x);
                         tmem_wait_ld();
 #pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] *= p.scale_log2;
+                        tmem_st8(st + j, x);
+#pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float m = warp_max_exact(kp > last0 + tok[col0 + j + e] ? -INFINITY : x[e]);
                             if (lane == 0) mx[qd][col0 + j + e] = m;
                         }
                     }
                     named_bar_sync(bar, 128);
+                    tmem_wait_st();
+                    float now = 0.f;
                     if (key < NC) {             // one thread per row: the new reference, and what the old weights shrink by
                         const int r = col0 + key;
-                        const float m = fmaxf(fmaxf(mx[0][r], mx[1][r]), fmaxf(mx[2][r], mx[3][r])) * p.scale_log2;
-                        const float old = -mine[r], now = key < rows ? fmaxf(old, m) : INFINITY;
+                        const float m = fmaxf(fmaxf(mx[0][r], mx[1][r]), fmaxf(mx[2][r], mx[3][r]));
+                        const float old = -mine[r];
+                        now = key < rows ? fmaxf(old, m) : INFINITY;
                         mine[r] = -now;
                         mx[0][r] = key < rows ? ex2_approx(old - now) : 0.f;
                     }
-                    named_bar_sync(bar, 128);
+                    wide = bar_any(bar, 128, key < rows && fabsf(now) > kWide && now > kNone);
 #pragma unroll
                     for (int j = 0; j < NC; j += 2) {
                         float x, y;

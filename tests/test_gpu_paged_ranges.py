@@ -1,7 +1,7 @@
 """Attention over the pages where its state moves: references that follow rising
 scores over sums and outputs already formed, non-finite drafts on every tile and
-over split pairs, batches too large for the lengths kept on chip.  The tolerance is
-test_gpu_paged's, computed here in 64 bits on the GPU."""
+over split pairs, batches too large for the lengths kept on chip, scores
+of any size.  The tolerance is test_gpu_paged's, computed here in 64 bits on the GPU."""
 import random
 
 import pytest
@@ -237,3 +237,32 @@ def test_split_batches_around_the_lengths_kept_on_chip(nseq, heads):
     got = c.run(d_error=err)
     assert err.item() == 0
     check(c, got)
+
+
+@pytest.mark.parametrize("sign", [1, -1], ids=["high", "low"])
+@pytest.mark.parametrize("exponent", [14, 15, 17, 30])
+@pytest.mark.parametrize("heads,lens,new", [((4, 2, 128), [700], [2]), ((8, 1, 64), [130, 5000], [16, 4]), ((4, 4, 64), [6000, 1, 64], [1, 1, 2]),
+                                            ((16, 2, 128), [2600, 300], [16, 3]), ((12, 3, 64), [900, 250], [16, 5])])
+def test_scores_of_any_size(sign, exponent, heads, lens, new):
+    """Scores of +-2^30 to +-2^65, whose steps in fp32 reach far past the softmax's range: one key
+    (or two equal ones) has all of the weight, and the result is its value (the mean of two), exactly."""
+    torch = torch_cuda()
+    hq, hkv, hd = heads
+    c = Case(lens, new, hq, hkv, hd, seed=40)
+    g = torch.Generator().manual_seed(exponent)
+    c.q.zero_()
+    c.q[:, :, 0] = 2.0 ** exponent
+    c.d["q"].copy_(c.q)
+    want = torch.zeros((c.rows, hq, hd), dtype=torch.float64)
+    for q, (n, m) in enumerate(zip(lens, new)):
+        times = torch.randint(5, 30, (n, hkv), generator=g).double()
+        for h in range(hkv):
+            seen = max(1, n - m + 1)                   # what all rows of the block see
+            at = random.Random(h * 7 + q).sample(range(seen), min(seen, 1 + h % 2))
+            times[at, h] = 30.0 if sign > 0 else 4.0
+            o = torch.stack([c.v[q][t, h].double() for t in at]).mean(0)
+            want[c.start[q]:c.start[q + 1], h * (hq // hkv):(h + 1) * (hq // hkv)] = o
+        c.k[q][:, :, 0] = (sign * times * 2.0 ** exponent).bfloat16()
+    repage(c)
+    got = c.run(scale=1.0)
+    assert torch.equal(got.cpu(), want.bfloat16())
