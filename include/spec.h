@@ -516,6 +516,8 @@ spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v
  * infinite or NaN makes that dimension of the rows that see it non-finite.
  * Weights of up to 2^40 are summed in 32 bits before the division, so visible
  * values should stay below 2^62 in magnitude (2^26 positions' worth fits).
+ * Scores may be as large and as low as fp32 holds: one whose products, sum or
+ * multiple by scale * log2(e) passes 2^128 is infinite, as in any fp32 form.
  * A sequence with a bad length or row range is skipped (its rows stay as they
  * were); a bad page reads as zeros.  Both set the error word.
  * The same call gives the same bits; how keys are grouped depends on the

@@ -46,6 +46,7 @@
 // instruction fetch for many short sequences of 64-wide heads (200 of up to 1500
 // positions with ragged blocks 40 us against 19.5 of HBM time).
 #include <cuda.h>
+#include <float.h>
 #include <math.h>
 
 #include "internal.h"
@@ -61,7 +62,7 @@ constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, 
 constexpr int kThreads = 32 * kWarps;
 constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
-constexpr float kNone = -1e30f;         // reference of a row that has seen no key
+constexpr float kNone = -FLT_MAX;       // reference of a row that has seen no key: no score lies below it
 constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
 constexpr int kSegs = 4;                    // segments listed ahead
 constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
