@@ -50,34 +50,26 @@
 #include <math.h>
 
 #include "internal.h"
+#include "paged_plan.h"
 #include "paged_split.h"
 #include "spec.h"
 
 namespace sv {
 namespace {
 
+using plan::kFewSeqs;
+using plan::kSegs;
+using plan::kWarps;
+using plan::Plan;
+using plan::Seg;
 using split::kChunk;
 
-constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12, kWarps = 16;
+constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -FLT_MAX;       // reference of a row that has seen no key: no score lies below it
 constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
-constexpr int kSegs = 4;                    // segments listed ahead
-constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
-
-// A segment, as the roles need it.
-struct Seg {
-    int c0, units;              // first chunk, number of chunks (0: the list ends)
-    int R;                      // rows
-    int last0;                  // last position that the first token sees
-    int len;                    // of the sequence
-    int q, head;                // sequence, kv head
-    int row0;                   // first row of the call
-    int slot;                   // where its partial goes; -1: it covers its pair
-    int pad[3];
-};
 
 // A split pair, as the join kernel sees it from one of its CTAs.
 struct Meta {
@@ -105,37 +97,6 @@ struct PagedParams {
     float* part_o;              // [2 * ctas][RP][HD]
     float2* part_ml;            // [2 * ctas][RP] (reference, sum)
     Meta* meta;                 // [ctas][2]: the pair that goes on into the CTA, the pair that begins in it and goes on
-};
-
-// Shared-memory plan: NQ query tiles, NP pairs of P^T parts, NK slots for a
-// chunk's K and NV for its V.  K and V do not share slots: different threads wait
-// for them, and a barrier's parity is only sound for one that sees every phase.
-template <int HD, int RP>
-struct Plan {
-    static constexpr bool kStream = RP <= 64;               // warpgroups take alternate chunks
-    static constexpr bool kStack = RP <= 32;                // P^T's parts in one product
-    static constexpr int kSlot = kChunk * HD * 2;
-    static constexpr int kQ = RP * HD * 2;
-    static constexpr int kP = kChunk * RP * 2;              // one part
-    static constexpr int NQ = RP <= 32 ? 2 : 1;
-    static constexpr int NP = kStream ? 2 : 1;
-    static constexpr int kFixed = NQ * kQ + NP * 2 * kP + 2048;   // alignment, pad after the last slot
-    static constexpr int kMost = 227 * 1024 - (6656 + 64 * RP) - kFixed; // less the static arrays
-    static constexpr int NS = kMost / kSlot < 8 ? kMost / kSlot : 8;
-    // V slots hold a chunk, or from 64 rows on, where there is room for few, a page:
-    // the next chunk's first page then loads while this one's is still in use.
-    // Of an odd number of pages K takes the rounded up half.
-    static constexpr int kPieces = RP >= 64 ? 2 : 1, kPiece = kSlot / kPieces;
-    static constexpr int NK = kPieces == 2 ? (kMost / kPiece + 2) / 4 : NS / 2;
-    static constexpr int NV = (kMost - NK * kSlot) / kPiece < 8 ? (kMost - NK * kSlot) / kPiece : 8;
-    static constexpr int kBytes = kFixed + NK * kSlot + NV * kPiece;
-    static constexpr int kO = kStack ? 2 * RP : RP;         // tensor-memory columns of one O^T
-    static constexpr int kUsed = 2 * RP + (kStream ? 4 : 2) * kO;   // S^T x 2, O^T x 2 (per warpgroup)
-    static constexpr int kCols = kUsed <= 256 ? 256 : 512;
-    // registers of a thread, by role: 128 each at launch, moved to where S^T and P^T live
-    static constexpr int kSoftRegs = RP <= 32 ? 160 : 184, kIssueRegs = 64, kResultRegs = RP <= 32 ? 128 : 80;
-    static_assert(2 * kSoftRegs + kIssueRegs + kResultRegs <= 4 * 128, "more registers than the block was launched with");
-    static_assert(NK >= 1 && NV >= kPieces + 1 && kUsed <= 512, "a K, and a V beyond the one in use");
 };
 
 __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -404,25 +365,20 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
     // rows that a softmax thread handles or skips together: more make longer runs of
     // independent instructions, fewer waste less on tiles that are not full
     constexpr int kSpan = NC <= 16 ? 8 : NC <= 32 ? 16 : 32;
-    constexpr int kGroups = kStream ? 2 : 1;    // O^T's (and references) of a segment
+    constexpr int kGroups = L::kGroups;
     constexpr int kArrive = kStream ? 4 : 8;    // warps that read an S^T and write a P^T
     constexpr int kReaders = kSoftWarps + 3 + 4;    // warps that read the list of segments
     constexpr int kPieces = L::kPieces, kPieceRows = kChunk / kPieces;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[NQ], q_empty[NQ], s_full[2], s_empty[2], p_full[NP], p_empty[NP],
-        o_full[2], o_empty[2], l_full[2], l_empty[2], seg_full[kSegs], seg_empty[kSegs], fin[2];
-    __shared__ uint32_t tmem_base;
-    __shared__ int dead, total;
-    __shared__ int poison[2];                           // 1 + the last segment (by parity) that silenced a value
-    __shared__ int first[split::kMaxSeqs + 1];
-    __shared__ int few_start[kFewSeqs + 1], few_len[kFewSeqs];   // a batch this small is not read from memory twice
-    __shared__ long long warp_sum[kWarps];
-    __shared__ __align__(16) Seg segs[kSegs];
-    __shared__ __align__(16) float nref[2][kGroups][RP];    // by segment parity: minus each row's reference
-    __shared__ __align__(16) float xl[2][kGroups][4][RP];   // per lane quadrant: sums (and, while a reference moves, maxima)
-    __shared__ float2 weight[2][RP];                        // what the two O^T's of a row are multiplied with
-    __shared__ __align__(16) int tok[RP];                   // token of each row
-    __shared__ long long col_off[RP];                       // its offset in the output
+    __shared__ plan::Fixed<RP> sh;
+    auto& k_full = sh.k_full; auto& k_empty = sh.k_empty; auto& v_full = sh.v_full; auto& v_empty = sh.v_empty;
+    auto& q_full = sh.q_full; auto& q_empty = sh.q_empty; auto& s_full = sh.s_full; auto& s_empty = sh.s_empty;
+    auto& p_full = sh.p_full; auto& p_empty = sh.p_empty; auto& o_full = sh.o_full; auto& o_empty = sh.o_empty;
+    auto& l_full = sh.l_full; auto& l_empty = sh.l_empty; auto& seg_full = sh.seg_full; auto& seg_empty = sh.seg_empty;
+    auto& fin = sh.fin; auto& tmem_base = sh.tmem_base; auto& dead = sh.dead; auto& total = sh.total;
+    auto& poison = sh.poison; auto& first = sh.first; auto& few_start = sh.few_start; auto& few_len = sh.few_len;
+    auto& warp_sum = sh.warp_sum; auto& segs = sh.segs; auto& nref = sh.nref; auto& xl = sh.xl;
+    auto& weight = sh.weight; auto& tok = sh.tok; auto& col_off = sh.col_off;
 
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* kslots = base;
@@ -1025,7 +981,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                 } else {
                     p.part_ml[(size_t)w.slot * RP + r] = make_float2(ma, la);
                 }
-                weight[par][r] = make_float2(fa, fb);
+                weight[par][r] = {fa, fb};
             }
             named_bar_sync(kResultBar, 128);
             const bool bad = poison[par] == seg + 1;
@@ -1051,7 +1007,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < kStep; ++e) {
-                    const float2 f = weight[par][j0 + e];
+                    const plan::Pair f = weight[par][j0 + e];
                     o[e] = (kStack ? o[e] + x[e] : o[e]) * f.x;
                     if (two) o[e] += (kStack ? y[e] + z[e] : y[e]) * f.y;
                 }

@@ -1,0 +1,58 @@
+"""Paged attention's shared memory, compiled for the host from the kernels' own
+header: what a CTA keeps in static memory and the tiles beside it fit for every
+instance, by the declarations themselves, and the buffer counts are those that
+the pipeline's model runs with."""
+import os
+import subprocess
+
+import pytest
+
+from test_paged_pipeline_cpu import plan
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SRC = r"""
+#include <stdio.h>
+#include "paged_plan.h"
+using namespace sv::plan;
+template <int HD, int RP> void line() {
+    using L = Plan<HD, RP>;
+    printf("%d %d %d %d %d %d %d %d %d %d\n", HD, RP, (int)sizeof(Fixed<RP>), L::kBytes, L::NK, L::NV, L::NQ, L::NP, L::kPieces, (int)L::kStream);
+}
+int main() {
+    line<64, 16>(); line<64, 32>(); line<64, 64>(); line<64, 128>();
+    line<128, 16>(); line<128, 32>(); line<128, 64>(); line<128, 128>();
+}
+"""
+NAMES = ["HD", "RP", "fixed", "bytes", "NK", "NV", "NQ", "NP", "pieces", "stream"]
+
+
+@pytest.fixture(scope="module")
+def plans(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text(SRC)
+    inc = os.path.join(ROOT, "speculative_decoding_verify_pass_gb300", "csrc")
+    subprocess.check_call(["g++", "-std=c++17", "-I", inc, str(d / "plan.cpp"), "-o", str(d / "plan")])
+    out = subprocess.check_output([str(d / "plan")]).decode().split("\n")
+    rows = [dict(zip(NAMES, map(int, x.split()))) for x in out if x]
+    return {(r["HD"], r["RP"]): r for r in rows}
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rp", [16, 32, 64, 128])
+def test_static_memory_and_tiles_fit(plans, hd, rp):
+    r = plans[hd, rp]
+    assert r["fixed"] + r["bytes"] <= 227 * 1024
+    # the tiles: K, V, queries, both parts of P^T, up to 1 KB of alignment and 1 KB behind the last V
+    chunk = 128 * hd * 2
+    assert r["bytes"] >= r["NK"] * chunk + r["NV"] * chunk // r["pieces"] + r["NQ"] * rp * hd * 2 + r["NP"] * 2 * 128 * rp * 2 + 2048
+    # per row: reference and four sums of two segment parities and up to two groups, weights, token, offset
+    groups = 2 if r["stream"] else 1
+    assert r["fixed"] >= rp * (2 * groups * 5 * 4 + 2 * 8 + 4 + 8) + 4 * 1025
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rp", [16, 32, 64, 128])
+def test_buffer_counts_are_the_model_s(plans, hd, rp):
+    r, model = plans[hd, rp], plan(hd, rp)
+    assert {k: r[k] for k in ("NK", "NV", "NQ", "NP", "pieces")} == {k: model[k] for k in ("NK", "NV", "NQ", "NP", "pieces")}
+    assert bool(r["stream"]) == model["stream"]
