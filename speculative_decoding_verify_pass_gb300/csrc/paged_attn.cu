@@ -1012,9 +1012,9 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
                     if (two) o[e] += (kStack ? y[e] + z[e] : y[e]) * f.y;
                 }
                 if (d < HD) {
-                    if (bad)
+                    if (bad)                    // of the positions that some row of the block sees and some does not
 #pragma unroll 1
-                        for (int t = max(last0 + 1, w.c0 * kChunk); t < min(w.len, (w.c0 + w.units) * kChunk); ++t) {
+                        for (int t = max(last0 + 1, w.c0 * kChunk); t < min(last0 + tok[w.R - 1] + 1, (w.c0 + w.units) * kChunk); ++t) {
                             const int page = p.tables[(size_t)w.q * p.table_pages + t / SPEC_PAGE];
                             if (page < 0 || page >= p.num_pages) continue;
                             const float v = bf2f(p.vpool[(((size_t)page * p.hkv + w.head) * SPEC_PAGE + t % SPEC_PAGE) * HD + d]);

@@ -221,6 +221,40 @@ def test_nonfinite_drafts_on_every_tile(tile, hd, n):
         check(c, got, ref, rows=[r for r in range(c.start[-1]) if r != m - 1])
 
 
+def test_nonfinite_values_of_a_prompt_cost_little():
+    """A prompt whose last values are not finite, in every head: the blocks before them hide them and
+    need no look at each of the positions behind (which took a hundred times the call's time)."""
+    torch = torch_cuda()
+    n, hq, hkv, hd = 6000, 32, 8, 128
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pages = pages_of(n)
+    q = torch.randn((n, hq, hd), generator=g, device="cuda").bfloat16()
+    kp = torch.randn((pages, hkv, PAGE, hd), generator=g, device="cuda").bfloat16()
+    vp = torch.randn((pages, hkv, PAGE, hd), generator=g, device="cuda").bfloat16()
+    tables = torch.arange(pages, device="cuda", dtype=torch.int32)[None]
+    start, length = i32([0, n]), i32([n])
+
+    def run():
+        return sv_().spec_paged_attention(q, start, length, tables, kp, vp, n)
+
+    def timed():
+        best = float("inf")
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            run()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    clean, t_clean = run(), timed()
+    vp[(n - 2) // PAGE, :, (n - 2) % PAGE:(n - 1) % PAGE + 1] = float("nan")
+    got, t_nan = run(), timed()
+    assert torch.equal(got[:n - 2].view(torch.int16), clean[:n - 2].view(torch.int16))
+    assert got[n - 2:].isnan().all()
+    assert t_nan < 4 * t_clean, (t_nan, t_clean)
+
+
 @pytest.mark.parametrize("nseq", [64, 65, 200, 1024])
 @pytest.mark.parametrize("heads", [(8, 2, 64), (8, 1, 128)])
 def test_split_batches_around_the_lengths_kept_on_chip(nseq, heads):
