@@ -219,8 +219,8 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Wait bounded in time (2^31 cycles, about a second, whatever one poll takes);
-// one that gives up raises `dead`.  Inline (a call would fix the registers that
+// Wait bounded in time (2^31 cycles, about a second, whatever one poll takes; more
+// rounds of that while nothing else has given up); one that gives up raises `dead`.  Inline (a call would fix the registers that
 // setmaxnreg moves) and short: the roles' loops share one instruction cache.
 // A role whose wait failed waits no more.
 __device__ __forceinline__ uint32_t cycles() {
@@ -228,11 +228,15 @@ __device__ __forceinline__ uint32_t cycles() {
     asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
     return c;
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    const uint32_t t0 = cycles();
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead, int rounds = 1) {
+    uint32_t t0 = cycles();
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity))
         if (cycles() - t0 > 0x7fffffffu) {
+            if (--rounds > 0 && !*dead) {
+                t0 = cycles();
+                continue;
+            }
             *dead = 1;
             return false;
         }
@@ -959,7 +963,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
             const int ga = kStream ? i & 1 : 0; // the warpgroup of the first unit; the other has none in a segment of one
             const bool two = kStream && w.units > 1, whole = w.slot < 0;
             i += w.units;
-            bool ok = wait(&l_full[par], (seg >> 1) & 1, deadp);
+            bool ok = wait(&l_full[par], (seg >> 1) & 1, deadp, plan::wait_rounds(w.units));
             if (d < w.R) {
                 const int r = d;
                 float ma = -nref[par][ga][r], la = xl[par][ga][0][r] + xl[par][ga][1][r] + xl[par][ga][2][r] + xl[par][ga][3][r];

@@ -17,6 +17,11 @@ constexpr int kSegs = 4;                    // segments listed ahead
 constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
 constexpr int kWarps = 16;
 
+// Limits of one wait (2^31 cycles each) that the results of a segment are waited for.
+// Other waits last a few chunks at most, this one all of them: up to 2^19, at 3000
+// cycles each (8000 where references move in every one, more beside other kernels).
+constexpr int wait_rounds(int units) { return 1 + (units >> 15); }
+
 // A segment, as the roles need it.
 struct alignas(16) Seg {
     int c0, units;              // first chunk, number of chunks (0: the list ends)
