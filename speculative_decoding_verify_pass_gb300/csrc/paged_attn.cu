@@ -86,7 +86,7 @@ struct Meta {
 struct PagedParams {
     CUtensorMap mq, mk, mv;
     const int *row_start, *len, *tables;
-    int table_pages, nseq, rows, hq, hkv, group, tokens;
+    int table_pages, nseq, rows, hkv, group, tokens;
     int whole;                  // pairs are not split: a CTA takes those that begin in its range
     float scale_log2;
     const uint16_t* vpool;
@@ -1354,7 +1354,6 @@ spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_
     p.table_pages = table_pages;
     p.nseq = nseq;
     p.rows = rows;
-    p.hq = n_heads;
     p.hkv = n_kv_heads;
     p.group = group;
     p.tokens = tokens;
