@@ -487,7 +487,8 @@ spec_status spec_pages_step(int32_t* d_pool, int32_t num_pages, int32_t* d_table
  *   d_row_count_opt  NULL, or a device int32: only rows below it are written
  *              (e.g. d_row_start + nseq);
  *   d_kpool, d_vpool  16-byte aligned pools of num_pages pages.
- * head_dim is 64 or 128. */
+ * head_dim is 64 or 128; 1 <= n_kv_heads <= 1024.  Errors:
+ * SPEC_ERR_INVALID_ARG, nothing enqueued. */
 spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_slots,
                               const int32_t* d_row_count_opt, int32_t rows, int32_t n_kv_heads, int32_t head_dim,
                               void* d_kpool, void* d_vpool, int32_t num_pages, int32_t* d_error_opt, void* cuda_stream);
@@ -505,7 +506,10 @@ spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v
  *   d_len      int32 [nseq], lengths with the new positions, at most
  *              table_pages * SPEC_PAGE;
  *   max_new    the most rows of any sequence, 1 or more: it picks the tile
- *              height and is no bound (larger blocks are right, only slower);
+ *              height and is no bound (larger blocks are right, only slower).  A
+ *              block of more rows than a tile is cut, and each piece works
+ *              through all positions of the sequence, those that it hides too:
+ *              the call is made for blocks of drafts, a prompt is right but slow;
  *   d_work     work_bytes of scratch, 256-byte aligned, at least what
  *              spec_paged_attention_workspace says for the same heads, max_new
  *              and table_pages on the same device (0 for short tables: d_work
@@ -524,9 +528,13 @@ spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v
  * lengths in the call, so a sequence's last bits may differ from batch to
  * batch.
  * Pointers 16-byte aligned, strides multiples of 8 and at least n_heads *
- * head_dim; head_dim 64 or 128; n_heads a multiple of n_kv_heads, at most 128
- * query heads per kv head; scale positive and finite; 0 <= nseq <=
- * SPEC_MAX_SEQS (nseq or rows 0: nothing is done). */
+ * head_dim and below 2^38; head_dim 64 or 128; n_heads a multiple of
+ * n_kv_heads, at most 128 query heads per kv head; 1 <= n_kv_heads <= 1024;
+ * scale positive and finite; 0 <= nseq <= SPEC_MAX_SEQS (nseq or rows 0:
+ * nothing is done); num_pages * n_kv_heads below 2^31, and so is the work:
+ * with t = T / (query heads per kv head), T the smallest of 16, 32, 64 and 128
+ * that holds max_new tokens' rows, else 128, (nseq + rows / t) * n_kv_heads *
+ * ceil(table_pages / 2).  Errors: SPEC_ERR_INVALID_ARG, nothing enqueued. */
 spec_status spec_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
                                            int32_t table_pages, size_t* out_bytes);
 spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_t* d_row_start, const int32_t* d_len,

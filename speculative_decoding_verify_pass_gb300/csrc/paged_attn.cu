@@ -15,9 +15,9 @@
 // costs the same for 16 columns as for 64), with a column each in tensor memory.
 //
 // The softmax needs no maximum: m is a reference that a row takes from the score
-// of one key, the first of its first chunk.  Any score may exceed it by up to
-// 2^40 (fp32 and bf16 hold that), and only when one exceeds it by more do the
-// row's reference, sum and O^T move to the chunk's maximum.  So per chunk and
+// of one key, the first of its first chunk.  A score may exceed it by 40 in log2
+// units (a weight of 2^40, which fp32 and bf16 hold), and only when one exceeds it
+// by more do the row's reference, sum and O^T move to the chunk's maximum.  So per chunk and
 // element there is one multiply-add, one exp2, one add to the thread's own
 // partial sum and the two roundings; nothing crosses lanes until the segment
 // ends.
@@ -36,15 +36,21 @@
 //
 // What bounds it, on a GB300 whose copies reach 6.8 TB/s (K and V of 8 heads of 128,
 // GPU time): HBM for long caches and full batches (64 ragged decodes up to 8192
-// positions 169 us, 6.6 TB/s; one sequence of 100003 positions 65.8 us, 6.2 TB/s, of
+// positions 168 us, 6.7 TB/s; one sequence of 100003 positions 65.3 us, 6.3 TB/s, of
 // which about 5 us are the launch, the first copies' latency, the results and the
-// join); the softmax warps' instructions at 128 rows (100003 positions 84 us, a
-// chunk 3000 cycles against 2870 of HBM time); latency for short ones (one sequence
-// of 128 positions 5.8 us, 300 7.1, 4104 with 8 rows 12.0: about 1 us each for the
+// join); the chain through a chunk at 128 rows (100003 positions 85 us): of about 3050
+// cycles at 1.93 GHz, against 2830 of HBM time, scores and the vote on references take
+// 1200, weights and P^T 1080, the wait for the chunk before's product 280 (there is one
+// P^T), for S^T 320; latency for short ones (one sequence
+// of 128 positions 5.7 us, 300 6.9, 4104 with 8 rows 11.8: about 1 us each for the
 // launch, the lengths, the page table, the first tile, the chain through the two
-// products and, where pairs are split, 3 us for the join); per-segment work and
-// instruction fetch for many short sequences of 64-wide heads (200 of up to 1500
-// positions with ragged blocks 40 us against 19.5 of HBM time).
+// products and, where pairs are split, 3 us for the join); work per segment, since
+// CTAs share chunks evenly and not segments: at 128 rows each one more makes a CTA
+// about 7000 cycles later (24 sequences of up to 8000: 75 us with one segment, 102
+// with eight, cycle counters included), and instruction fetch for many short sequences
+// of 64-wide heads (200 of up to 1500 positions with ragged blocks 39 us against 19.5
+// of HBM time); hidden chunks for blocks longer than a tile (6000 rows of a prompt
+// 1.5 ms against 0.15 of arithmetic).
 #include <cuda.h>
 #include <float.h>
 #include <math.h>

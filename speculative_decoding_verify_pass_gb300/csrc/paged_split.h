@@ -68,10 +68,11 @@ SPLIT_HD int sequence_of(const int* first, int nseq, int u) {
 
 // Whether pairs are left whole: a CTA then takes the pairs that begin in its
 // range, nothing is joined and no scratch is used.  Measured on the GPU, split
-// against whole (8 kv heads of 128, decode): tables of 512 positions 9.3 / 7.8 us
-// with one sequence, 25.3 / 21.2 with 64; 1024 positions 9.5 / 10.4 and 41.6 / 37.7;
-// 2048 positions 10.0 / 15.2 and 69.1 / 67.5.  The caller also saves a launch and
-// the scratch, so tables of up to 1024 positions stay whole.
+// against whole (8 kv heads of 128, decode, every sequence full): tables of 512
+// positions 7.9 / 7.2 us with one sequence, 10.9 / 8.7 with 16, 28.3 / 26.3 with 64;
+// 1024 positions 8.3 / 8.9, 13.1 / 10.8 and 47.8 / 45.6; 2048 positions 9.0 / 12.3,
+// 27.6 / 24.8 and 85.2 / 83.6.  The caller also saves a launch and the scratch (4.3
+// us of host time for a call against 7.0), so tables of up to 1024 positions stay whole.
 SPLIT_HD bool whole_pairs(int table_pages) { return table_pages <= 16; }
 
 // Tile height (rows per kv head) for blocks of max_new tokens of G query
