@@ -544,6 +544,115 @@ spec_status spec_paged_attention(const void* d_q, int64_t q_stride, const int32_
                                  int64_t out_stride, int32_t* d_error_opt, void* d_work, size_t work_bytes,
                                  void* cuda_stream);
 
+/* ---- rotary positions ----
+ *
+ * What a caller of the paged cache does with its queries and keys before the
+ * append: each head's first rotary_dim elements are turned by the row's
+ * position, pair i by the angle position * f_i,
+ *   u' = gain * (u cos - v sin),  v' = gain * (v cos + u sin)
+ * (u, v) = (x[i], x[i + rotary_dim / 2]), or (x[2i], x[2i + 1]) when
+ * interleaved; elements from rotary_dim on are kept.  A frequency is given in
+ * turns per position as a 64-bit fraction (2^64 = one circle), so that the
+ * angle is as exact at position 2^30 as at position 1. */
+enum { SPEC_BF16 = 0, SPEC_FP16 = 1, SPEC_FP32 = 2 }; /* element types */
+enum {
+    SPEC_ROPE_PLAIN = 0,      /* f_i = base^(-2i / rotary_dim)                                             */
+    SPEC_ROPE_LINEAR = 1,     /* f_i / factor                                                              */
+    SPEC_ROPE_BASE = 2,       /* base * factor^(rotary_dim / (rotary_dim - 2)) instead of base             */
+    SPEC_ROPE_WAVELENGTH = 3, /* f_i / factor where it turns at most `low` times in the context, f_i from
+                                 `high` times on, in between a blend linear in the number of turns         */
+    SPEC_ROPE_PARTS = 4       /* the same blend, linear in i between the pairs that turn `high` and `low`
+                                 times (rounded outwards), and a gain of 0.1 ln(factor) + 1                */
+};
+#define SPEC_ROPE_MAX_DIM 1024
+
+/* Frequencies of rotary_dim / 2 pairs, computed in fp64 on the host:
+ * out_turns uint64[rotary_dim / 2] and *out_gain (1 but for
+ * SPEC_ROPE_PARTS).  Host call, touches no device.  rotary_dim even,
+ * 2..1024; base above 1; factor at least 1 (ignored by SPEC_ROPE_PLAIN);
+ * 0 < low < high and context >= 1 for the last two kinds (else ignored).
+ * Errors: SPEC_ERR_INVALID_ARG. */
+spec_status spec_rope_table(int32_t rotary_dim, double base, int32_t scaling, double factor, double low, double high,
+                            int32_t context, uint64_t* out_turns, float* out_gain);
+
+/* Turn the rows of a call.
+ *   d_x, d_out  rows of [heads][head_dim] elements of `type`, consecutive rows
+ *              x_stride (out_stride) elements apart, e.g. the queries and keys
+ *              of a fused QKV output as one range of heads.  d_out may be d_x
+ *              itself with the same stride; otherwise they must not overlap;
+ *   d_turns    uint64 [rotary_dim / 2] on the device;
+ *   positions  either d_pos int32 [rows] (any value, negative too), or
+ *              d_row_start int32 [nseq + 1] and d_len int32 [nseq] as
+ *              spec_paged_attention takes them: row j of a sequence's m rows
+ *              stands at len - m + j, and rows outside every sequence are
+ *              left as they were (where row starts do not rise it is not said
+ *              which rows those are).  Exactly one of the two;
+ *   inverse    turns by the negative angle: the gradient of the call without
+ *              it, or (with 1 / gain) its undoing;
+ *   gain       finite; 1 or what spec_rope_table gave.
+ * Arithmetic is fp32, rounded once.  It needs no handle, runs on the current
+ * device, is asynchronous on cuda_stream, allocates nothing and can be
+ * captured into a graph.  rows >= 0 (0: nothing is done); heads 1..4096;
+ * head_dim a multiple of 8, 8..1024; rotary_dim even, 2..head_dim; pointers
+ * 16-byte aligned, strides multiples of 16 bytes, at least heads * head_dim
+ * and below 2^38; 0 <= nseq <= SPEC_MAX_SEQS.  Errors: SPEC_ERR_INVALID_ARG,
+ * nothing enqueued. */
+spec_status spec_rope(const void* d_x, int64_t x_stride, void* d_out, int64_t out_stride, int32_t type, int32_t rows,
+                      int32_t heads, int32_t head_dim, int32_t rotary_dim, int32_t interleaved, int32_t inverse, float gain,
+                      const uint64_t* d_turns, const int32_t* d_row_start_opt, const int32_t* d_len_opt, int32_t nseq,
+                      const int32_t* d_pos_opt, void* cuda_stream);
+
+/* ---- the paged cache in 8 bits ----
+ *
+ * The same pages, tables and slots with keys and values in e4m3: pools of
+ * bytes [num_pages][n_kv_heads][SPEC_PAGE][head_dim], and one array of scale
+ * bytes for both, [num_pages][n_kv_heads][2][SPEC_PAGE] (keys' scales, then
+ * values').  Code c of a position and kv head stands for c * 2^(b - 127), b its
+ * scale byte; b = 255 and the codes 0x7F and 0xFF stand for NaN.  (As torch
+ * types: float8_e4m3fn and float8_e8m0fnu, or uint8.)
+ *
+ * A scale belongs to one position: writing a position changes no other, so a
+ * rejected draft leaves nothing behind when its sequence is cropped.  Scales
+ * are powers of two, so the only rounding is that of the codes.
+ * The calls' conventions are those of the paged cache above. */
+
+/* Write new keys and values at their slots: with e the least integer, at least
+ * -126, such that every finite element of the (row, kv head) is at most 448 *
+ * 2^e in magnitude, its scale byte is e + 127 and its codes are x * 2^-e
+ * rounded to the nearest e4m3 (ties to even).  Infinities and NaN become NaN.
+ * Arguments as spec_paged_append's; d_kpool, d_vpool and d_scales are 16-byte
+ * aligned; strides below 2^38.  Errors: SPEC_ERR_INVALID_ARG, nothing
+ * enqueued. */
+spec_status spec_paged_append_fp8(const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_slots,
+                                  const int32_t* d_row_count_opt, int32_t rows, int32_t n_kv_heads, int32_t head_dim,
+                                  void* d_kpool, void* d_vpool, void* d_scales, int32_t num_pages, int32_t* d_error_opt,
+                                  void* cuda_stream);
+
+/* Read the positions at d_slots back: bf16 rows d_k and d_v as
+ * spec_paged_append_fp8 takes them, each element c * 2^(b - 127) (exact for
+ * what that call wrote, but for elements above 1.9375 * 2^127, which round to
+ * 2^128 and read as infinities).  Rows with a negative slot, from *d_row_count_opt on, or
+ * with a slot outside the pool (which sets the error word) are left as they
+ * were; a slot may be read twice.  Errors: SPEC_ERR_INVALID_ARG, nothing
+ * enqueued. */
+spec_status spec_paged_read_fp8(const int32_t* d_slots, const int32_t* d_row_count_opt, int32_t rows, int32_t n_kv_heads,
+                                int32_t head_dim, const void* d_kpool, const void* d_vpool, const void* d_scales,
+                                int32_t num_pages, void* d_k, int64_t k_stride, void* d_v, int64_t v_stride,
+                                int32_t* d_error_opt, void* cuda_stream);
+
+/* spec_paged_attention over such pools: out[row][h] = sum_i softmax_i(scale *
+ * q[row][h] . k_i) v_i with k_i and v_i as the codes and scales give them.
+ * Arguments, layouts, limits and errors as there, with d_scales (16-byte
+ * aligned) beside the pools, and a workspace of its own. */
+spec_status spec_paged_attention_fp8_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
+                                               int32_t table_pages, size_t* out_bytes);
+spec_status spec_paged_attention_fp8(const void* d_q, int64_t q_stride, const int32_t* d_row_start, const int32_t* d_len,
+                                     const int32_t* d_tables, int32_t table_pages, int32_t nseq, int32_t rows,
+                                     int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale,
+                                     const void* d_kpool, const void* d_vpool, const void* d_scales, int32_t num_pages,
+                                     void* d_out, int64_t out_stride, int32_t* d_error_opt, void* d_work, size_t work_bytes,
+                                     void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

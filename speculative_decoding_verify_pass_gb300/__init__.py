@@ -23,6 +23,9 @@ SPEC_CACHE_TARGET, SPEC_CACHE_DRAFT = 0, 1
 SPEC_MAX_BLOCK = 16
 SPEC_PAGE, SPEC_MAX_SEQS, SPEC_MAX_PAGES, SPEC_MAX_TABLE = 64, 1024, 33554431, 1048576
 SPEC_POOL_HEADER, SPEC_POOL_FREE, SPEC_POOL_ERROR = 8, 0, 1
+SPEC_BF16, SPEC_FP16, SPEC_FP32 = range(3)
+SPEC_ROPE_PLAIN, SPEC_ROPE_LINEAR, SPEC_ROPE_BASE, SPEC_ROPE_WAVELENGTH, SPEC_ROPE_PARTS = range(5)
+SPEC_ROPE_MAX_DIM = 1024
 (SPEC_PAGED_BAD_LENGTH, SPEC_PAGED_BAD_ROWS, SPEC_PAGED_NO_PAGES, SPEC_PAGED_BAD_PAGE,
  SPEC_PAGED_TIMEOUT) = range(1, 6)
 
@@ -35,7 +38,8 @@ EXPORTED = ["spec_model_create", "spec_model_destroy", "spec_set_draft_plan", "s
             "spec_batch_kv_load", "spec_batch_kv_export", "spec_batch_set_len", "spec_batch_len",
             "spec_verify_batch", "spec_share_prefix", "spec_draft_step_logits", "spec_accept_sampled",
             "spec_pages_init", "spec_pages_step", "spec_paged_append", "spec_paged_attention_workspace",
-            "spec_paged_attention"]
+            "spec_paged_attention", "spec_rope_table", "spec_rope", "spec_paged_append_fp8", "spec_paged_read_fp8",
+            "spec_paged_attention_fp8_workspace", "spec_paged_attention_fp8"]
 
 
 class SpecError(RuntimeError):
@@ -121,6 +125,14 @@ def library():
         "spec_paged_attention_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "spec_paged_attention": [vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32,
                                  vp, i64, vp, vp, ctypes.c_size_t, vp],
+        "spec_rope_table": [i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double, ctypes.c_double, i32, vp,
+                            ctypes.POINTER(ctypes.c_float)],
+        "spec_rope": [vp, i64, vp, i64, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, vp, i32, vp, vp],
+        "spec_paged_append_fp8": [vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp],
+        "spec_paged_read_fp8": [vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, i64, vp, i64, vp, vp],
+        "spec_paged_attention_fp8_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "spec_paged_attention_fp8": [vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, vp, i32,
+                                     vp, i64, vp, vp, ctypes.c_size_t, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -347,12 +359,15 @@ def _refuse(msg):
     raise SpecError(SPEC_ERR_INVALID_ARG, msg)
 
 
-def _explain(call, i32=(), pools=(), rows=(), dims=()):
+def _explain(call, i32=(), pools=(), rows=(), dims=(), scales=None, types=None):
     """Raises for the first argument that is not what its call needs.  i32:
-    (name, tensor, entries); pools: the key and the value pool; rows: (name,
-    tensor, shape or None); dims: (name, tensor, dimensions, what they are)."""
+    (name, tensor, entries); pools: the key and the value pool (in 8 bits when
+    there are scales); rows: (name, tensor, shape or None), of one of types
+    (bfloat16); dims: (name, tensor, dimensions, what they are)."""
     T = _torch
     tensors = [(n, t) for n, t, _ in i32] + [(n, t) for n, t, _ in rows] + list(zip(("d_kpool", "d_vpool"), pools))
+    if scales is not None:
+        tensors.append(("d_scales", scales))
     for name, t in tensors:
         if not isinstance(t, T.Tensor) or t.get_device() < 0 or t.get_device() != T._C._cuda_getDevice():
             _refuse("%s: %s must be a tensor on the current CUDA device" % (call, name))
@@ -362,13 +377,20 @@ def _explain(call, i32=(), pools=(), rows=(), dims=()):
     for name, t, need in i32:
         if t.dtype is not T.int32 or not t.is_contiguous() or t.numel() < need:
             _refuse("%s: %s must be a contiguous int32 tensor of at least %d entries" % (call, name, need))
+    allowed, what = ((T.bfloat16,), "bfloat16") if scales is None else ((T.float8_e4m3fn, T.uint8), "float8_e4m3fn (or uint8)")
     for name, t in zip(("d_kpool", "d_vpool"), pools):
-        if t.dtype is not T.bfloat16 or not t.is_contiguous() or t.shape[2] != SPEC_PAGE or t.shape != pools[0].shape:
-            _refuse("%s: %s must be a contiguous bfloat16 tensor [pages][kv heads][%d][head_dim], both pools alike"
-                    % (call, name, SPEC_PAGE))
+        if t.dtype not in allowed or not t.is_contiguous() or t.shape[2] != SPEC_PAGE or t.shape != pools[0].shape:
+            _refuse("%s: %s must be a contiguous %s tensor [pages][kv heads][%d][head_dim], both pools alike"
+                    % (call, name, what, SPEC_PAGE))
+    if scales is not None:
+        want = (pools[0].shape[0], pools[0].shape[1], 2, SPEC_PAGE)
+        if scales.dtype not in (T.uint8, T.float8_e8m0fnu) or not scales.is_contiguous() or tuple(scales.shape) != want:
+            _refuse("%s: d_scales must be a contiguous uint8 (or float8_e8m0fnu) tensor %s" % (call, list(want)))
+    types = types or (T.bfloat16,)
     for name, t, shape in rows:
-        if t.dtype is not T.bfloat16 or tuple(t.shape) != tuple(shape):
-            _refuse("%s: %s must be a bfloat16 tensor %s" % (call, name, list(shape)))
+        if t.dtype not in types or tuple(t.shape) != tuple(shape):
+            _refuse("%s: %s must be a %s tensor %s" % (call, name, " or ".join(str(x).replace("torch.", "") for x in types),
+                                                       list(shape)))
         (_, s1, s2), (_, heads, hd) = t.stride(), t.shape
         if (s2 != 1 and hd > 1) or (s1 != hd and heads > 1):
             _refuse("%s: the rows of %s must be contiguous [heads][head_dim] blocks" % (call, name))
@@ -452,6 +474,138 @@ def spec_paged_attention(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, ma
         if d_work is not None:
             _refuse("spec_paged_attention: d_work must be a contiguous uint8 tensor on the current CUDA device")
         _refuse("spec_paged_attention: an argument has more than 2147483647 entries")
+    _check(out)
+
+
+# ----------------------------------------------------------------------------
+# Rotary positions, and the paged cache in 8 bits
+# ----------------------------------------------------------------------------
+def spec_rope_table(rotary_dim: int, base: float = 10000.0, scaling: int = SPEC_ROPE_PLAIN, factor: float = 1.0,
+                    low: float = 1.0, high: float | None = None, context: int = 8192, device=None):
+    """(d_turns, gain) for spec_rope: the frequencies of rotary_dim / 2 pairs as
+    an int64 tensor of 2^-64 turns per position, and the factor on cos and sin.
+    scaling is one of SPEC_ROPE_*; low and high (default 4, with
+    SPEC_ROPE_PARTS 32) are numbers of turns in the context."""
+    import torch
+    n = int(rotary_dim)
+    out = np.zeros(max(1, min(n, SPEC_ROPE_MAX_DIM) // 2), dtype=np.int64)
+    gain = ctypes.c_float(0)
+    high = (32.0 if scaling == SPEC_ROPE_PARTS else 4.0) if high is None else high
+    _check(library().spec_rope_table(n, float(base), int(scaling), float(factor), float(low), float(high), int(context),
+                                     ctypes.c_void_p(out.ctypes.data), ctypes.byref(gain)))
+    return torch.from_numpy(out).to("cuda" if device is None else device), float(gain.value)
+
+
+def spec_rope(d_x, d_turns, d_row_start=None, d_len=None, d_pos=None, interleaved=False, inverse=False, gain=1.0, d_out=None):
+    """Turn the first 2 * len(d_turns) elements of every head of d_x (bf16, fp16
+    or fp32 [rows][heads][head_dim], rows any distance apart) by the row's
+    position: d_pos int32 [rows], or each sequence's newest rows as
+    spec_paged_attention takes them.  Returns d_out (a new tensor when None,
+    whose rows outside every sequence are then unset; d_x turns in place)."""
+    out = (_native or _load_native()).rope(d_x, d_turns, d_row_start, d_len, d_pos, interleaved, inverse, gain, d_out)
+    if out.__class__ is not int:
+        return out
+    if out < 0:
+        T = _torch
+        if not isinstance(d_x, T.Tensor) or d_x.dim() != 3:
+            _refuse("spec_rope: d_x must be [rows][heads][head_dim]")
+        _explain("spec_rope", rows=(("d_x", d_x, d_x.shape),), types=(T.bfloat16, T.float16, T.float32))
+        if d_out is not None:
+            _explain("spec_rope", rows=(("d_out", d_out, d_x.shape),), types=(d_x.dtype,))
+        if (not isinstance(d_turns, T.Tensor) or d_turns.dtype not in (T.int64, T.uint64) or d_turns.device != d_x.device
+                or d_turns.dim() != 1 or not d_turns.is_contiguous() or d_turns.numel() > SPEC_ROPE_MAX_DIM):
+            _refuse("spec_rope: d_turns must be a contiguous int64 tensor [rotary_dim / 2] on the current CUDA device")
+        if (d_pos is None) != (d_row_start is not None) or (d_row_start is None) != (d_len is None):
+            _refuse("spec_rope: positions come from d_pos, or from d_row_start and d_len (one of the two)")
+        if d_pos is not None:
+            _explain("spec_rope", i32=(("d_pos", d_pos, d_x.shape[0]),))
+        else:
+            _explain("spec_rope", i32=(("d_len", d_len, 0),))
+            _explain("spec_rope", i32=(("d_row_start", d_row_start, d_len.numel() + 1),))
+        _refuse("spec_rope: an argument has more than 2147483647 entries")
+    _check(out)
+
+
+def spec_paged_append_fp8(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_scales, d_error=None):
+    """spec_paged_append into an 8-bit cache: the rows' e4m3 codes to the pools
+    (float8_e4m3fn or uint8), the exponents of their scales to d_scales (uint8
+    or float8_e8m0fnu [pages][kv heads][2][64])."""
+    st = (_native or _load_native()).paged_append_fp8(d_k, d_v, d_slots, d_row_count, d_kpool, d_vpool, d_scales, d_error)
+    if st < 0:
+        more = tuple((n, t, 1) for n, t in (("d_row_count", d_row_count), ("d_error", d_error)) if t is not None)
+        _explain8("spec_paged_append_fp8", d_kpool, d_vpool, d_scales, (("d_slots", d_slots, 0),) + more)
+        for name, t in (("d_k", d_k), ("d_v", d_v)):
+            if not isinstance(t, _torch.Tensor) or t.dim() != 3:
+                _refuse("spec_paged_append_fp8: %s must be [rows][kv heads][head_dim]" % name)
+        want = (d_k.shape[0], d_kpool.shape[1], d_kpool.shape[3])
+        _explain("spec_paged_append_fp8", rows=(("d_k", d_k, want), ("d_v", d_v, want)), i32=(("d_slots", d_slots, want[0]),))
+        _refuse("spec_paged_append_fp8: an argument has more than 2147483647 entries")
+    if st:
+        _check(st)
+
+
+def _explain8(call, d_kpool, d_vpool, d_scales, i32, dims=()):
+    if not isinstance(d_scales, _torch.Tensor):
+        _refuse("%s: d_scales must be a tensor on the current CUDA device" % call)
+    _explain(call, pools=(d_kpool, d_vpool), scales=d_scales, i32=i32,
+             dims=(("d_kpool", d_kpool, 4, "4-D"), ("d_vpool", d_vpool, 4, "4-D"), ("d_scales", d_scales, 4, "4-D")) + dims)
+
+
+def spec_paged_read_fp8(d_slots, d_row_count, d_kpool, d_vpool, d_scales, d_k=None, d_v=None, d_error=None):
+    """The positions at d_slots (int32 [rows]) of an 8-bit cache as bf16 rows;
+    returns (d_k, d_v), [rows][kv heads][head_dim] each (new tensors when None,
+    whose skipped rows are then unset)."""
+    out = (_native or _load_native()).paged_read_fp8(d_slots, d_row_count, d_kpool, d_vpool, d_scales, d_k, d_v, d_error)
+    if out.__class__ is not int:
+        return out
+    if out < 0:
+        more = tuple((n, t, 1) for n, t in (("d_row_count", d_row_count), ("d_error", d_error)) if t is not None)
+        _explain8("spec_paged_read_fp8", d_kpool, d_vpool, d_scales, (("d_slots", d_slots, 0),) + more,
+                  dims=(("d_slots", d_slots, 1, "1-D"),))
+        want = (d_slots.numel(), d_kpool.shape[1], d_kpool.shape[3])
+        for name, t in (("d_k", d_k), ("d_v", d_v)):
+            if t is not None:
+                if not isinstance(t, _torch.Tensor) or t.dim() != 3:
+                    _refuse("spec_paged_read_fp8: %s must be [rows][kv heads][head_dim]" % name)
+                _explain("spec_paged_read_fp8", rows=((name, t, want),))
+        _refuse("spec_paged_read_fp8: an argument has more than 2147483647 entries")
+    _check(out)
+
+
+def spec_paged_attention_fp8_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int, table_pages: int) -> int:
+    """Bytes of scratch a spec_paged_attention_fp8 call with these heads and
+    table width needs on the current device."""
+    out = ctypes.c_size_t(0)
+    _check(library().spec_paged_attention_fp8_workspace(int(n_heads), int(n_kv_heads), int(head_dim), int(max_new),
+                                                        int(table_pages), ctypes.byref(out)))
+    return int(out.value)
+
+
+def spec_paged_attention_fp8(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, d_scales, max_new, scale=None, d_out=None,
+                             d_error=None, d_work=None):
+    """spec_paged_attention over an 8-bit cache (pools and scales as
+    spec_paged_append_fp8 writes them)."""
+    native = _native or _load_native()
+    out = native.paged_attention_fp8(d_q, d_row_start, d_len, d_tables, d_kpool, d_vpool, max_new, scale, d_out, d_error, d_work,
+                                     d_scales)
+    if out.__class__ is not int:
+        return out
+    if out < 0:
+        call = "spec_paged_attention_fp8"
+        more = () if d_error is None else (("d_error", d_error, 1),)
+        _explain8(call, d_kpool, d_vpool, d_scales, (("d_tables", d_tables, 0),) + more,
+                  dims=(("d_tables", d_tables, 2, "[nseq][table_pages]"),))
+        n = d_tables.shape[0]
+        _explain(call, i32=(("d_row_start", d_row_start, n + 1), ("d_len", d_len, n)))
+        if not isinstance(d_q, _torch.Tensor) or d_q.dim() != 3:
+            _refuse(call + ": d_q must be [rows][heads][head_dim]")
+        want = (d_q.shape[0], d_q.shape[1], d_kpool.shape[3])
+        for name, t in (("d_q", d_q), ("d_out", d_out)):
+            if t is not None:
+                _explain(call, rows=((name, t, want),))
+        if d_work is not None:
+            _refuse(call + ": d_work must be a contiguous uint8 tensor on the current CUDA device")
+        _refuse(call + ": an argument has more than 2147483647 entries")
     _check(out)
 
 

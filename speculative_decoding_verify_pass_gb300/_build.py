@@ -22,7 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
 BINDING = os.path.join(HERE, "_paged.so")
 SOURCES = ["gemm.cu", "attention.cu", "misc.cu", "api.cu", "noalloc.cu", "sampling.cu", "pages.cu",
-           "paged_attn.cu"]
+           "paged_attn.cu", "rope.cu", "pages8.cu", "paged_attn8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
