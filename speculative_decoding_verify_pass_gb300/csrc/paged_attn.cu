@@ -51,78 +51,17 @@
 // of 64-wide heads (200 of up to 1500 positions with ragged blocks 39 us against 19.5
 // of HBM time); hidden chunks for blocks longer than a tile (6000 rows of a prompt
 // 1.5 ms against 0.15 of arithmetic).
-#include <cuda.h>
-#include <float.h>
-#include <math.h>
-
-#include "internal.h"
-#include "paged_plan.h"
-#include "paged_split.h"
-#include "spec.h"
+#include "paged_core.cuh"
 
 namespace sv {
 namespace {
 
-using plan::kFewSeqs;
-using plan::kSegs;
-using plan::kWarps;
 using plan::Plan;
-using plan::Seg;
-using split::kChunk;
 
-constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12;
-constexpr int kThreads = 32 * kWarps;
-constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
-constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
-constexpr float kNone = -FLT_MAX;       // reference of a row that has seen no key: no score lies below it
-constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
-
-// A split pair, as the join kernel sees it from one of its CTAs.
-struct Meta {
-    int count;                  // partials (0: no such pair)
-    int owner;                  // the CTA where it begins
-    int slot;                   // the owner's slot
-    int rows;                   // R
-    int head;                   // first query head
-    int row0;                   // first row of the call
-    int last0;                  // last visible position of the first token
-    int pad;
-};
-
-struct PagedParams {
+struct PagedParams : PagedCommon {
     CUtensorMap mq, mk, mv;
-    const int *row_start, *len, *tables;
-    int table_pages, nseq, rows, hkv, group, tokens;
-    int whole;                  // pairs are not split: a CTA takes those that begin in its range
-    float scale_log2;
     const uint16_t* vpool;
-    int num_pages;
-    uint16_t* out;
-    long long out_stride;
-    int* err;
-    float* part_o;              // [2 * ctas][RP][HD]
-    float2* part_ml;            // [2 * ctas][RP] (reference, sum)
-    Meta* meta;                 // [ctas][2]: the pair that goes on into the CTA, the pair that begins in it and goes on
 };
-
-__device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// Shared-memory matrix descriptor with the 128-byte swizzle.  K-major: 8-row
-// groups sbo apart (lbo unused).  MN-major: 64-element column blocks lbo apart,
-// 8-row (k) groups sbo apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-
-// The upper half of such a descriptor (stride, version, swizzle).
-constexpr uint32_t hi_sw128(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 
 // D[tmem] (+)= A B^T with descriptors in halves: the upper one is a constant of the
 // operand's layout, so that stepping along k is one 32-bit addition.
@@ -134,237 +73,6 @@ __device__ __forceinline__ void umma_lo(uint32_t d, uint32_t alo, uint32_t ahi, 
         "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-
-// 8, 16 or 32 consecutive fp32 columns of this warp's 32 lanes, not waited for.
-__device__ __forceinline__ void tmem_ld8_async(uint32_t t, float* v) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(t)
-                 : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld16_async(uint32_t t, float* v) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld32_async(uint32_t t, float* v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(t)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st8(uint32_t t, const float* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t),
-                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Two floats rounded to nearest even, a in the low half.
-__device__ __forceinline__ uint32_t cvt_bf16x2(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-// Two fp32 operations in one instruction.
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ F2() {}
-    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-
-// True in every one of n threads of barrier id when any of them says so.
-__device__ __forceinline__ bool bar_any(int id, int n, bool any) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(n), "r"((uint32_t)any)
-        : "memory");
-    return r != 0;
-}
-
-// True in one lane of a converged warp, always the same one.  Issuing MMAs and
-// copies under this predicate (and not under lane == 0) tells the compiler that
-// one thread issues them; otherwise every issue pays for finding that out.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-// Wait bounded in time (2^31 cycles, about a second, whatever one poll takes; more
-// rounds of that while nothing else has given up); one that gives up raises `dead`.  Inline (a call would fix the registers that
-// setmaxnreg moves) and short: the roles' loops share one instruction cache.
-// A role whose wait failed waits no more.
-__device__ __forceinline__ uint32_t cycles() {
-    uint32_t c;
-    asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
-    return c;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead, int rounds = 1) {
-    uint32_t t0 = cycles();
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (cycles() - t0 > 0x7fffffffu) {
-            if (--rounds > 0 && !*dead) {
-                t0 = cycles();
-                continue;
-            }
-            *dead = 1;
-            return false;
-        }
-    return true;
-}
-// After a failed wait: let what is in flight finish before the CTA ends.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) __nanosleep(64);
-}
-
-// Position in a ring of N buffers: index and the parity of its current round.
-template <int N>
-struct Ring {
-    int at = 0;
-    uint32_t round = 0;
-    __device__ __forceinline__ void step() {
-        if (++at == N) at = 0, round ^= 1;
-    }
-};
-
-// A CTA's segments in order.
-struct Walk {
-    const PagedParams& p;
-    const int* first;           // [nseq + 1] in shared memory
-    const int *start, *lens;    // row starts and lengths: in shared memory when they are few
-    int u, end;                 // next unit, end of the CTA's range
-    int q = 0, q1 = 0;          // sequence, the end of its units
-    int rows = 0, len = 0, row_base = 0, chunks = 1;
-    // the segment
-    int head = 0, block = 0, c0 = 0, c1 = 0, R = 0, seg = -1;
-
-    __device__ Walk(const PagedParams& pp, const int* f, const int* s, const int* n, int begin, int e)
-        : p(pp), first(f), start(s), lens(n), u(begin), end(e) {}
-    __device__ __forceinline__ void sequence() {
-        q1 = first[q + 1];
-        row_base = start[q];
-        rows = start[q + 1] - row_base;
-        len = lens[q];
-        chunks = split::chunks_of(len);
-    }
-    __device__ __forceinline__ bool next() {
-        if (u >= end) return false;
-        if (seg < 0) {                          // where the range begins
-            q = split::sequence_of(first, p.nseq, u);
-            sequence();
-            const int at = u - first[q], pair = at / chunks;
-            block = pair / p.hkv;
-            head = pair - block * p.hkv;
-            c0 = at - pair * chunks;
-            if (p.whole && c0 > 0) {            // this pair begins in another CTA's range, which takes it
-                u += chunks - c0;
-                if (u >= end) return false;
-                step();
-            }
-        } else {
-            step();
-        }
-        c1 = p.whole ? chunks : min(chunks, c0 + end - u);
-        R = min(p.tokens, rows - block * p.tokens) * p.group;
-        u += c1 - c0;
-        ++seg;
-        return true;
-    }
-    // the pair after the current one
-    __device__ __forceinline__ void step() {
-        c0 = 0;
-        if (u >= q1) {
-            do ++q;
-            while (first[q + 1] <= u);          // sequences without units
-            sequence();
-            block = head = 0;
-        } else if (++head == p.hkv) {
-            head = 0;
-            ++block;
-        }
-    }
-    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
-    // last position that the block's first token sees
-    __device__ __forceinline__ int last0() const { return len - rows + block * p.tokens; }
-    // the segment's pair, for the join
-    __device__ Meta meta(const split::Deal& deal) const {
-        const int pair_begin = u - c1, owner = deal.cta(pair_begin);
-        Meta m;
-        m.count = deal.parts(owner, pair_begin + chunks);
-        m.owner = owner;
-        m.slot = 2 * owner + (pair_begin == deal.begin(owner) ? 0 : 1);
-        m.rows = R;
-        m.head = head * p.group;
-        m.row0 = row_base + block * p.tokens;
-        m.last0 = last0();
-        m.pad = 0;
-        return m;
-    }
-};
-
-// The pages of a segment's chunks, looked up 32 chunks at a time, one a lane.
-struct PageWalk {
-    int y0 = -1, y1 = -1;       // the lane's chunk: tensor-map rows of its two pages
-    int z0 = -1, z1 = -1;       // the current chunk's (a bad page's -1 lies outside the pool and reads as zeros)
-    int count = 0;              // and how many of them exist
-    __device__ __forceinline__ void at(const PagedParams& p, const Seg& s, int k, int lane) {
-        const int held = (s.len + SPEC_PAGE - 1) / SPEC_PAGE, c = s.c0 + k;
-        if ((k & 31) == 0) {
-            const int* tab = p.tables + (size_t)s.q * p.table_pages + 2 * (c + lane);
-            const int have = k + lane < s.units ? held - 2 * (c + lane) : 0;
-            const int a = have > 0 ? tab[0] : -1, b = have > 1 ? tab[1] : -1;
-            const bool oka = a >= 0 && a < p.num_pages, okb = b >= 0 && b < p.num_pages;
-            if (p.err && ((have > 0 && !oka) || (have > 1 && !okb))) atomicCAS(p.err, 0, SPEC_PAGED_BAD_PAGE);
-            y0 = oka ? a * p.hkv + s.head : -1;
-            y1 = okb ? b * p.hkv + s.head : -1;
-        }
-        z0 = __shfl_sync(0xffffffffu, y0, k & 31);
-        z1 = __shfl_sync(0xffffffffu, y1, k & 31);
-        count = max(0, min(2, held - 2 * c));
-    }
-};
-
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <int HD, int RP>
 __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_kernel(const __grid_constant__ PagedParams p) {
@@ -1073,131 +781,6 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_ker
     }
 }
 
-// Joins the partials of each pair that CTAs shared: CTA (c, y) works for the pair
-// that goes on into attention CTA c (y even) or begins in it and goes on (odd).
-// The CTAs of a pair deal its rows among themselves (t of n takes rows t, t + n,
-// ..): the more partials a row has, the more CTAs read them.  Up to 8 partials a warp joins a row, its
-// loads all in flight at once; above, the CTA's 8 warps share the row's partials.
-constexpr int kJoinFew = 8, kJoinWarps = 8;
-
-template <int HD>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedParams p, int rp) {
-    constexpr int V = HD / 32;
-    __shared__ float so[kJoinWarps][HD];
-    __shared__ float ssum[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_launch_dependents();
-    {
-        const Meta m = p.meta[2 * blockIdx.x + (blockIdx.y & 1)];
-        if (m.count == 0) return;
-        const int mine = blockIdx.x - m.owner, y0 = blockIdx.y >> 1, ny = gridDim.y >> 1;
-        // partial t of the pair: the owner's slot, then the first slots of the CTAs after it
-        auto at = [&](int r, int t) { return (size_t)(t ? 2 * (m.owner + t) : m.slot) * rp + r; };
-        auto store = [&](int r, const float* o, float sum) {
-            const int t = r / p.group;
-            const bool any = m.last0 + t >= 0;
-            uint16_t* out = p.out + (long long)(m.row0 + t) * p.out_stride + (long long)(m.head + r - t * p.group) * HD + lane * V;
-            const float inv = any ? 1.f / sum : 0.f;
-            if constexpr (V == 4)
-                *reinterpret_cast<uint2*>(out) = any ? make_uint2(cvt_bf16x2(o[0] * inv, o[1] * inv), cvt_bf16x2(o[2] * inv, o[3] * inv))
-                                                     : make_uint2(0u, 0u);
-            else
-                *reinterpret_cast<uint32_t*>(out) = any ? cvt_bf16x2(o[0] * inv, o[1] * inv) : 0u;
-        };
-        auto load = [&](size_t i, float* v) {
-            if constexpr (V == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(p.part_o + i * HD + lane * 4);
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(p.part_o + i * HD + lane * 2);
-                v[0] = x.x, v[1] = x.y;
-            }
-        };
-        if (m.count <= kJoinFew) {
-            for (int r = mine + m.count * (warp + kJoinWarps * y0); r < m.rows; r += m.count * kJoinWarps * ny) {
-                float v[kJoinFew][V];
-                float2 ml[kJoinFew];
-#pragma unroll
-                for (int t = 0; t < kJoinFew; ++t)
-                    if (t < m.count) {
-                        ml[t] = p.part_ml[at(r, t)];
-                        load(at(r, t), v[t]);
-                    }
-                float M = kNone, sum = 0.f, o[V] = {};
-#pragma unroll
-                for (int t = 0; t < kJoinFew; ++t)
-                    if (t < m.count) M = fmaxf(M, ml[t].x);
-#pragma unroll
-                for (int t = 0; t < kJoinFew; ++t)
-                    if (t < m.count) {
-                        const float f = ex2_approx(ml[t].x - M);
-                        sum += f * ml[t].y;
-#pragma unroll
-                        for (int e = 0; e < V; ++e) o[e] += f * v[t][e];
-                    }
-                store(r, o, sum);
-            }
-        } else {
-            for (int r = mine + m.count * y0; r < m.rows; r += m.count * ny) {
-                float M = kNone, sum = 0.f, o[V] = {};
-                for (int t = lane; t < m.count; t += 32) M = fmaxf(M, p.part_ml[at(r, t)].x);
-#pragma unroll
-                for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                for (int t0 = warp; t0 < m.count; t0 += 4 * kJoinWarps) {
-                    float v[4][V];
-                    float2 ml[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = t0 + i * kJoinWarps;
-                        if (t < m.count) {
-                            ml[i] = p.part_ml[at(r, t)];
-                            load(at(r, t), v[i]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (t0 + i * kJoinWarps < m.count) {
-                            const float f = ex2_approx(ml[i].x - M);
-                            sum += f * ml[i].y;
-#pragma unroll
-                            for (int e = 0; e < V; ++e) o[e] += f * v[i][e];
-                        }
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
-                if (lane == 0) ssum[warp] = sum;
-                __syncthreads();
-                if (warp == 0) {
-                    sum = 0.f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kJoinWarps; ++w) {
-                        sum += ssum[w];
-#pragma unroll
-                        for (int e = 0; e < V; ++e) o[e] += so[w][lane * V + e];
-                    }
-                    store(r, o, sum);
-                }
-                __syncthreads();
-            }
-        }
-    }
-}
-
-spec_status bad(const char* msg) {
-    set_last_error(msg);
-    return SPEC_ERR_INVALID_ARG;
-}
-
-spec_status failed(cudaError_t e) {
-    set_last_error(cudaGetErrorString(e));
-    return SPEC_ERR_CUDA;
-}
-
-bool misaligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
 // What the head layout has to satisfy; null when it does.
 const char* head_error(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new) {
     if (head_dim != 64 && head_dim != 128) return "spec_paged_attention: head_dim must be 64 or 128";
@@ -1206,40 +789,6 @@ const char* head_error(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, in
     if (n_heads / n_kv_heads > 128) return "spec_paged_attention: at most 128 query heads per kv head";
     if (max_new < 1) return "spec_paged_attention: max_new must be at least 1";
     return nullptr;
-}
-
-// Workspace: partial outputs, (reference, sum) pairs, two Metas per CTA.
-struct Work {
-    size_t o, ml, meta, bytes;
-    Work(int ctas, int rp, int hd) {
-        o = 0;
-        ml = (size_t)2 * ctas * rp * hd * 4;
-        meta = ml + (size_t)2 * ctas * rp * 8;
-        bytes = (meta + (size_t)2 * ctas * sizeof(Meta) + 255) & ~(size_t)255;
-    }
-};
-
-// SMs of the current device, its index checked; 0 on an error.
-int current_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms;
-}
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeFn>(f);
-    }();
-    return fn;
 }
 
 // bf16 [d2][d1][d0] with strides s1, s2 (elements), read in boxes of [b2][b1][64], 128-byte swizzle.
@@ -1252,20 +801,6 @@ bool encode(CUtensorMap* map, const void* p, uint64_t d0, uint64_t d1, uint64_t 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch(const void* fn, dim3 grid, unsigned block, size_t smem, cudaStream_t s, void** args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
 template <int HD, int RP>
 cudaError_t run(PagedParams& p, int ctas, cudaStream_t s) {
     const void* fn = (const void*)paged_attn_kernel<HD, RP>;
@@ -1274,7 +809,7 @@ cudaError_t run(PagedParams& p, int ctas, cudaStream_t s) {
     void* args[] = {&p};
     if ((e = launch(fn, dim3((unsigned)ctas), kThreads, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess || p.whole) return e;
     int rp = RP;
-    void* jargs[] = {&p, &rp};
+    void* jargs[] = {static_cast<PagedCommon*>(&p), &rp};
     return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, 2 * (RP <= 16 ? 1 : RP / 16)), 32 * kJoinWarps, 0, s, jargs);
 }
 
