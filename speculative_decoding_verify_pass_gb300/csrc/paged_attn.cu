@@ -52,11 +52,21 @@
 // of HBM time); hidden chunks for blocks longer than a tile (6000 rows of a prompt
 // 1.5 ms against 0.15 of arithmetic).
 #include "paged_core.cuh"
+#include "paged_plan.h"
 
 namespace sv {
 namespace {
 
+using plan::kFewSeqs;
+using plan::kSegs;
+using plan::kWarps;
 using plan::Plan;
+using plan::Seg;
+
+constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
+constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
 
 struct PagedParams : PagedCommon {
     CUtensorMap mq, mk, mv;
@@ -73,6 +83,81 @@ __device__ __forceinline__ void umma_lo(uint32_t d, uint32_t alo, uint32_t ahi, 
         "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// A CTA's segments in order.
+struct Walk {
+    const PagedParams& p;
+    const int* first;           // [nseq + 1] in shared memory
+    const int *start, *lens;    // row starts and lengths: in shared memory when they are few
+    int u, end;                 // next unit, end of the CTA's range
+    int q = 0, q1 = 0;          // sequence, the end of its units
+    int rows = 0, len = 0, row_base = 0, chunks = 1;
+    // the segment
+    int head = 0, block = 0, c0 = 0, c1 = 0, R = 0, seg = -1;
+
+    __device__ Walk(const PagedParams& pp, const int* f, const int* s, const int* n, int begin, int e)
+        : p(pp), first(f), start(s), lens(n), u(begin), end(e) {}
+    __device__ __forceinline__ void sequence() {
+        q1 = first[q + 1];
+        row_base = start[q];
+        rows = start[q + 1] - row_base;
+        len = lens[q];
+        chunks = split::chunks_of(len);
+    }
+    __device__ __forceinline__ bool next() {
+        if (u >= end) return false;
+        if (seg < 0) {                          // where the range begins
+            q = split::sequence_of(first, p.nseq, u);
+            sequence();
+            const int at = u - first[q], pair = at / chunks;
+            block = pair / p.hkv;
+            head = pair - block * p.hkv;
+            c0 = at - pair * chunks;
+            if (p.whole && c0 > 0) {            // this pair begins in another CTA's range, which takes it
+                u += chunks - c0;
+                if (u >= end) return false;
+                step();
+            }
+        } else {
+            step();
+        }
+        c1 = p.whole ? chunks : min(chunks, c0 + end - u);
+        R = min(p.tokens, rows - block * p.tokens) * p.group;
+        u += c1 - c0;
+        ++seg;
+        return true;
+    }
+    // the pair after the current one
+    __device__ __forceinline__ void step() {
+        c0 = 0;
+        if (u >= q1) {
+            do ++q;
+            while (first[q + 1] <= u);          // sequences without units
+            sequence();
+            block = head = 0;
+        } else if (++head == p.hkv) {
+            head = 0;
+            ++block;
+        }
+    }
+    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
+    // last position that the block's first token sees
+    __device__ __forceinline__ int last0() const { return len - rows + block * p.tokens; }
+    // the segment's pair, for the join
+    __device__ Meta meta(const split::Deal& deal) const {
+        const int pair_begin = u - c1, owner = deal.cta(pair_begin);
+        Meta m;
+        m.count = deal.parts(owner, pair_begin + chunks);
+        m.owner = owner;
+        m.slot = 2 * owner + (pair_begin == deal.begin(owner) ? 0 : 1);
+        m.rows = R;
+        m.head = head * p.group;
+        m.row0 = row_base + block * p.tokens;
+        m.last0 = last0();
+        m.skip = 0;
+        return m;
+    }
+};
 
 template <int HD, int RP>
 __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn_kernel(const __grid_constant__ PagedParams p) {

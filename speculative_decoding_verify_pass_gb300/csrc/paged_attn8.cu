@@ -9,25 +9,38 @@
 //                       of two for each row: bf16's 8 significant bits are two times
 //                       e4m3's 4 (the second part carries a sign), so that nothing of
 //                       q is lost but below 2^-17 of the row's largest element.  The
-//                       parts lie one behind the other along the product's k.
+//                       parts are two products into the same S^T.
 //     P^T = exp2(2^(a + ek) scale log2e S^T - m)    ek: the key's scale
-//     O^T += V8^T P'^T  P' = 2^(ev - r + 8) P, three e5m2 parts      ev: the value's scale
+//     O^T += V8^T P'^T  P' = 2^(ev - r + 3) P as a half, in three e5m2 parts; ev: the value's scale
 // A value's scale goes into its weight, relative to r, the largest scale seen, so
 // that the codes enter the product as they are.  Weights need more range than bits
 // (a key far down still counts when there are 100000 like it), so their parts are
-// e5m2: 3 significant bits each, 9 together, and 2^-17 to 57344 where e4m3 ends at
-// 2^-10 and 448.  Relative to the reference's weight, what is lost lies below 2^-25.
+// e5m2, a half's upper byte: 3 significant bits each, which is cheap to cut a half into
+// (an and, a subtraction, a byte permutation).  What a part leaves is kept times 4, then
+// times 8 more, so that together they end at 2^-25 of the reference's weight.  The parts
+// lie side by side in the product's N (3 RP columns of O^T, joined by the results): one
+// product for all costs as much as one part's as long as N is this small.
 //
-// That range is what decides the softmax's references: a weight may exceed its row's
-// reference by 2^7.75 only (fp32 and bf16 bear 2^40).  So a row takes the maximum of
-// its segment's first chunk (redux over each warp's 32 keys), and r that chunk's
-// largest scale; when a later score or scale exceeds them, row references, sums and O^T
-// move to the chunk's.
+// A half overflows 2^13 above the references.  So a segment's first chunk gives them (the
+// rows' maxima, the largest value scale), and a later chunk in which some half is
+// infinite makes its warpgroup move references, sums and O^T up to its maxima, and is
+// taken again; the vote on it rides on the barrier that the P^T buffer needs anyway.
 //
-// Roles, by warpgroup: 0 and 1 softmax (thread = key); 2 one warp each for the MMAs of
-// S^T, those of O^T, the copies of V, and the list of segments with the copies of K
-// and the scales; 3 splits the next segment's queries into their parts, then writes
-// this segment's results (thread = head dimension).
+// Roles, by warpgroup: softmax (thread = key, 16 rows; 2 of them for tiles of 16 rows,
+// which take alternate chunks, else 4: two teams of 2, or one of 4); then one warp each
+// for the MMAs of S^T, those of O^T, the copies of V, and the list of segments with the
+// copies of K and the scales; last a warpgroup that splits the next segment's queries
+// into their parts, then writes this segment's results (thread = head dimension).
+// 16 rows a thread in 4 warpgroups took what 32 rows in 2 did (24 sequences of 16 new at
+// 8 heads a kv head: 206 against 210 us then, 200 short ones 62 and 62), and one code
+// serves every tile.
+//
+// What bounds it: long caches memory (100003 positions of 8 kv heads: 39.6 us, 30.3 at
+// the copy rate; 64 ragged decodes 95, of 83), short sequences a segment's way through the
+// roles (200 of them 61 us: about 8 go to the results, 10 to the weights), many rows the
+// softmax's issue (24 x 16 new rows 154 us: a weight costs 8 instructions beside its
+// exp2, and the conversions to halves share its pipe).
+#include <stddef.h>
 #include <stdio.h>
 
 #include "paged_core.cuh"
@@ -36,21 +49,100 @@
 namespace sv {
 namespace {
 
+using plan8::kFewSeqs;
 using plan8::kParts;
 using plan8::kScaleSlots;
+using plan8::kSegs;
 using plan8::Plan;
+using plan8::Seg;
 
-constexpr float kLimit8 = 7.75f;        // log2 by which a weight, its value's scale included, may exceed the references
-constexpr int kShift8 = 8;              // weights are kept times 2^8: 2^(8 + 7.75) is below e5m2's 57344
-constexpr int kFarScale = 60;           // a scale this far above the reference moves it: 2^60 times a small weight still is one
+constexpr int kShift8 = 3;              // weights are kept times 2^3, so that they overflow a half 2^13 above the references
+constexpr float kPart2 = 4.f, kPart3 = 8.f;     // the second part is kept times 4, the third times 4 * 8
+constexpr int kNearScale = 12;          // where references move, the values' does if a scale is more than this above it
+constexpr int kFarScale = 100;          // and a scale this far above it moves it in any case (powers of two end there)
+constexpr int kLowScale = -60;          // one further below counts as that: 2^-60 of a value that counts is nothing
 
 struct Paged8Params : PagedCommon {
     CUtensorMap mk, mv;
+    int tile;                   // rows of a block
     const uint16_t* q;
     long long q_stride;
     const uint8_t *vpool, *scales;
 };
 
+// Barriers and shared memory by 32-bit addresses: the roles' loops are short enough for
+// a conversion per access to be much of what they do.  `kept` makes a value stay in its
+// register: a shared address is otherwise formed anew wherever it is used.
+__device__ __forceinline__ uint32_t kept(uint32_t v) {
+    asm volatile("mov.b32 %0, %0;" : "+r"(v));
+    return v;
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// Wait bounded in time (2^31 cycles, about a second, `rounds` of them): one that gives
+// up raises dead, and no wait lasts once that is raised.  For whole warps: a try by
+// part of a warp does not suspend it, and a spinning warp takes its neighbours' turns.
+// The lanes may leave it apart: they join (__syncwarp, a vote, a named barrier) before
+// one of them does what lets the barrier's next phase end.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* dead, int rounds = 1) {
+    if (try_wait(bar, parity)) return true;
+    uint32_t t0 = cycles();
+#pragma unroll 1
+    while (!*dead) {
+        if (try_wait(bar, parity)) return true;
+        if (cycles() - t0 > 0x7fffffffu) {
+            if (--rounds <= 0) *dead = 1;
+            t0 = cycles();
+        }
+    }
+    return false;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool one) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"((uint32_t)one) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void give_up(uint32_t bar, uint32_t parity) {  // after a failed wait: let what is in flight finish
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 20) && !try_wait(bar, parity); ++i) __nanosleep(64);
+}
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int lds_u8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return (int)v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 // D[tmem] (+)= A B^T in 8-bit floats, descriptors in halves.
 __device__ __forceinline__ void umma8_lo(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -102,19 +194,28 @@ __device__ __forceinline__ uint32_t split_e4m3(float& a, float& b) {
     b -= y;
     return c;
 }
-// The next e5m2 part of two halves (an e5m2 code is a half's upper byte), and what it leaves.
-__device__ __forceinline__ uint32_t part_e5m2(uint32_t& h) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
-    uint32_t t;
-    asm("prmt.b32 %0, %1, 0, 0x1404;" : "=r"(t) : "r"((uint32_t)c));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(t));
-    return c;
+// Halves: an e5m2 code is a half's upper byte.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
-__device__ __forceinline__ uint32_t last_e5m2(uint32_t h) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
-    return c;
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {    // a NaN counts only among NaN
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+constexpr uint32_t kHalves2 = 0x44004400u, kHalves3 = 0x48004800u;  // kPart2 and kPart3 twice
+static_assert(kPart2 == 4.f && kPart3 == 8.f, "as halves");
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, 0x7531;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t cvt_f16x2(F2 x) {
     float a, b;
@@ -124,18 +225,110 @@ __device__ __forceinline__ uint32_t cvt_f16x2(F2 x) {
     return r;
 }
 
+// A CTA's segments in order.
+struct Walk {
+    const Paged8Params& p;
+    const int* first;           // [nseq + 1] in shared memory
+    const int *start, *lens;    // row starts and lengths: in shared memory when they are few
+    int u, end;                 // next unit, end of the CTA's range
+    int q = 0, q1 = 0;          // sequence, the end of its units
+    int rows = 0, len = 0, row_base = 0, chunks = 1;
+    // the segment
+    int head = 0, block = 0, c0 = 0, c1 = 0, seg = -1;
+    int pair0 = 0;              // first unit of its pair
+
+    __device__ Walk(const Paged8Params& pp, const int* f, const int* s, const int* n, int begin, int e)
+        : p(pp), first(f), start(s), lens(n), u(begin), end(e) {}
+    __device__ __forceinline__ void sequence() {
+        q1 = first[q + 1];
+        row_base = start[q];
+        rows = start[q + 1] - row_base;
+        len = lens[q];
+        chunks = split8::chunks_of(len);
+    }
+    __device__ __forceinline__ bool next() {
+#pragma unroll 1
+        for (;;) {
+            if (u >= end) return false;
+            int u0 = 0;                             // the pair's first unit in the range
+            if (q1 == 0) {                          // where the range begins
+                q = split::sequence_of(first, p.nseq, u);
+                sequence();
+                const int span = chunks + split8::kHead, at = u - first[q], pair = at / span;
+                block = pair / p.hkv;
+                head = pair - block * p.hkv;
+                u0 = at - pair * span;
+            } else {
+                step();
+            }
+            pair0 = u - u0;
+            const int span = chunks + split8::kHead, u1 = p.whole ? span : min(span, u0 + end - u);
+            u += u1 - u0;
+            if (p.whole && u0 > 0) continue;        // it begins in another CTA's range, which takes it
+            const split8::Part part = split8::part_of(u0, u1);
+            c0 = part.c0;
+            c1 = part.c1;
+            if (c1 > c0) break;                     // (else not one of its chunks lies in the range)
+        }
+        ++seg;
+        return true;
+    }
+    // the pair after the current one
+    __device__ __forceinline__ void step() {
+        if (u >= q1) {
+            do ++q;
+            while (first[q + 1] <= u);              // sequences without units
+            sequence();
+            block = head = 0;
+        } else if (++head == p.hkv) {
+            head = 0;
+            ++block;
+        }
+    }
+    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
+    __device__ __forceinline__ Seg segment() const {
+        const long long row = (long long)block * p.tile;    // of the sequence's rows and query heads
+        const int t = (int)(row / p.group);
+        Seg s = {};
+        s.c0 = c0;
+        s.units = c1 - c0;
+        s.R = (int)min((long long)p.tile, (long long)rows * p.group - row);
+        s.last0 = len - rows + t;
+        s.len = len;
+        s.q = q;
+        s.head = head;
+        s.row0 = row_base + t;
+        s.skip = (int)(row - (long long)t * p.group);
+        s.slot = whole() ? -1 : 2 * (int)blockIdx.x + (c0 > 0 ? 0 : 1);
+        return s;
+    }
+    // the segment's pair, for the join
+    __device__ Meta meta(const split::Deal& deal) const {
+        const Seg s = segment();
+        Meta m;
+        m.count = split8::parts_of(deal, pair0, chunks);
+        m.owner = split8::owner_of(deal, pair0);
+        m.slot = 2 * m.owner + 1;
+        m.rows = s.R;
+        m.head = head * p.group;
+        m.row0 = s.row0;
+        m.last0 = s.last0;
+        m.skip = s.skip;
+        return m;
+    }
+};
+
 template <int HD, int RP>
-__global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_kernel(const __grid_constant__ Paged8Params p) {
+__global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((Plan<HD, RP>::kLaunchRegs)) paged_attn8_kernel(const __grid_constant__ Paged8Params p) {
     using L = Plan<HD, RP>;
-    constexpr bool kStream = L::kStream, kStack = L::kStack;
-    constexpr int NK = L::NK, NV = L::NV, NP = L::NP, NQ = L::NQ;
-    constexpr int NC = kStream ? RP : RP / 2;   // rows of a softmax thread
-    // rows that a softmax thread handles or skips together: more make longer runs of
-    // independent instructions, fewer waste less on tiles that are not full
-    constexpr int kSpan = NC <= 16 ? 8 : NC <= 32 ? 16 : 32;
-    constexpr int kGroups = L::kGroups;
-    constexpr int kArrive = kStream ? 4 : 8;    // warps that read an S^T and write a P^T
+    constexpr bool kStream = L::kStream;
+    constexpr int NK = L::NK, NV = L::NV, NS = L::NS, NC = L::NC;
+    constexpr int kGroups = L::kGroups, kTeam = L::kTeam;
+    constexpr int kArrive = kTeam;              // warpgroups that read an S^T and write a P^T
+    constexpr int kThreads = 32 * L::kWarps, kSoftWarps = 4 * L::kSoftGroups;
+    constexpr int kScoreWarp = kSoftWarps, kLoadVWarp = kScoreWarp + 2, kLoadKWarp = kScoreWarp + 3, kResultWarp = kScoreWarp + 4;
     constexpr int kReaders = kSoftWarps + 3 + 4;    // warps that read the list of segments
+    constexpr int kSoftBar = 1, kResultBar = kSoftBar + L::kSoftGroups;     // named barriers: one per softmax warpgroup, the results' warpgroup
     extern __shared__ uint8_t smem_raw[];
     __shared__ plan8::Fixed<RP> sh;
 
@@ -143,7 +336,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
     uint8_t* kslots = base;
     uint8_t* vslots = kslots + NK * L::kSlot;
     uint8_t* qs = vslots + NV * L::kSlot + L::kPad;
-    uint8_t* ps = qs + NQ * L::kQ;
+    uint8_t* ps = qs + 2 * L::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -155,28 +348,26 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
             mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.v_empty[i], 1);
         }
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_empty[i], kArrive);
+        }
         for (int i = 0; i < kScaleSlots; ++i) {
             mbar_init(&sh.c_full[i], 1);
             mbar_init(&sh.c_empty[i], kArrive);
         }
-        for (int i = 0; i < NQ; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 4);
             mbar_init(&sh.q_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.r_full[i], 4);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_empty[i], kArrive);
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.o_empty[i], 4);
             mbar_init(&sh.l_full[i], kSoftWarps);
             mbar_init(&sh.l_empty[i], 4);
-            mbar_init(&sh.fin[i], 1);
-            sh.poison[i] = 0;
-        }
-        for (int i = 0; i < NP; ++i) {
             mbar_init(&sh.p_full[i], kArrive);
             mbar_init(&sh.p_empty[i], 1);
+            mbar_init(&sh.fin[i], 1);
+            sh.poison[i] = 0;
         }
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&sh.seg_full[i], 1);
@@ -187,11 +378,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
         sh.first[0] = 0;
     }
 #pragma unroll 1
-    for (int i = tid; i < RP; i += kThreads) {
-        const int t = i / p.group;
-        sh.tok[i] = t;
-        sh.col_off[i] = t * p.out_stride + (long long)(i - t * p.group) * HD;
-    }
+    for (int i = tid; i < RP; i += kThreads) sh.tok[i] = i / p.group;
     if (warp == kScoreWarp) tmem_alloc(&sh.tmem_base, L::kCols);
     pdl_wait();
     pdl_launch_dependents();
@@ -216,7 +403,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
                 if (bad_rows || bad_len) {
                     if (blockIdx.x == 0 && p.err) atomicCAS(p.err, 0, bad_rows ? SPEC_PAGED_BAD_ROWS : SPEC_PAGED_BAD_LENGTH);
                 } else {
-                    v[k] = split::units_of(r1 - r0, n, p.tokens, p.hkv);
+                    v[k] = split8::units_of(r1 - r0, n, p.group, p.tile, p.hkv);
                 }
             }
             sum += v[k];
@@ -250,13 +437,19 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
     const uint32_t tmem = sh.tmem_base;
     const split::Deal deal(sh.total, gridDim.x);
     const int begin = deal.begin(blockIdx.x), end = deal.begin(blockIdx.x + 1);
-    volatile int* deadp = &sh.dead;
+    // shared memory by address: barrier i of an array of them is BAR(array, i)
+    using F = plan8::Fixed<RP>;
+    const uint32_t shb = kept(smem_u32(&sh));
+#define BAR(x, i) (shb + (uint32_t)offsetof(F, x) + (uint32_t)(i) * 8u)
+    volatile int* const dead = &sh.dead;
+    // token of row r of a block, counted from its first row's (which the block may begin in the middle of)
+    auto token = [&](const Seg& s, int r) { return p.group > RP ? (int)(s.skip + r >= p.group) : sh.tok[r]; };
     Ring<kSegs> sr;                             // every role's place in the list of segments
-    auto take = [&](bool one) {                 // the next segment; `one`: this thread alone stands for its warp
-        wait(&sh.seg_full[sr.at], sr.round, deadp);
+    auto take = [&]() {                         // the next segment
+        wait(BAR(seg_full, sr.at), sr.round, dead);
         const Seg s = sh.segs[sr.at];
-        if (!one) __syncwarp();
-        if (one || lane == 0) mbar_arrive(&sh.seg_empty[sr.at]);
+        __syncwarp();
+        arrive_if(BAR(seg_empty, sr.at), lane == 0);
         sr.step();
         return s;
     };
@@ -270,27 +463,18 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
             Meta into = {}, from = {};
             Ring<NK> kr;
             Ring<kScaleSlots> cr;
+            const uint32_t ka = kept(smem_u32(kslots));
             bool ok = true;
 #pragma unroll 1
             for (bool more = true; more && ok;) {
                 more = w.next();
                 Seg s = {};                     // no units: the list ends
-                if (more) {
-                    s.c0 = w.c0;
-                    s.units = w.c1 - w.c0;
-                    s.R = w.R;
-                    s.last0 = w.last0();
-                    s.len = w.len;
-                    s.q = w.q;
-                    s.head = w.head;
-                    s.row0 = w.row_base + w.block * p.tokens;
-                    s.slot = w.whole() ? -1 : 2 * (int)blockIdx.x + (w.u - s.units == begin ? 0 : 1);
-                }
-                ok = __all_sync(0xffffffffu, wait(&sh.seg_empty[sr.at], sr.round ^ 1, deadp));
-                if (!ok) break;
+                if (more) s = w.segment();
+                ok = wait(BAR(seg_empty, sr.at), sr.round ^ 1, dead);
+                if (!__all_sync(0xffffffffu, ok)) break;
                 if (lane == 0) {
                     sh.segs[sr.at] = s;
-                    mbar_arrive(&sh.seg_full[sr.at]);
+                    arrive(BAR(seg_full, sr.at));
                 }
                 sr.step();
                 if (!more) break;
@@ -298,25 +482,28 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
 #pragma unroll 1
                 for (int k = 0; k < s.units; ++k) {
                     pages.at(p, s, k, lane);
-                    ok = __all_sync(0xffffffffu, wait(&sh.c_empty[cr.at], cr.round ^ 1, deadp) && wait(&sh.k_empty[kr.at], kr.round ^ 1, deadp));
+                    ok = wait(BAR(c_empty, cr.at), cr.round ^ 1, dead);
+                    ok = wait(BAR(k_empty, kr.at), kr.round ^ 1, dead) && ok;
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (elect_one()) {
-                        uint64_t* cf = &sh.c_full[cr.at];
+                        const uint32_t cf = BAR(c_full, cr.at), full = BAR(k_full, kr.at);
+                        const uint32_t to = shb + (uint32_t)offsetof(F, scale) + cr.at * 4 * SPEC_PAGE, dst = ka + kr.at * L::kSlot;
                         // a bad page (it reads as zeros) has no scales: ones
                         const bool c0 = pages.count > 0 && pages.z0 >= 0, c1 = pages.count > 1 && pages.z1 >= 0;
-                        if (pages.count > 0 && !c0)
-                            for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(sh.scale[cr.at][0])[i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                        if (pages.count > 1 && !c1)
-                            for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(sh.scale[cr.at][1])[i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                        fence_proxy_async_smem();
-                        mbar_arrive_expect_tx(cf, (c0 ? 2 * SPEC_PAGE : 0) + (c1 ? 2 * SPEC_PAGE : 0));
-                        if (c0) bulk_g2s(sh.scale[cr.at][0], p.scales + (size_t)pages.z0 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, cf);
-                        if (c1) bulk_g2s(sh.scale[cr.at][1], p.scales + (size_t)pages.z1 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, cf);
-                        uint64_t* full = &sh.k_full[kr.at];
-                        uint8_t* dst = kslots + kr.at * L::kSlot;
-                        mbar_arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD));
-                        if (pages.count > 0) tma3(dst, &p.mk, 0, 0, pages.z0, full);
-                        if (pages.count > 1) tma3(dst + SPEC_PAGE * HD, &p.mk, 0, 0, pages.z1, full);
+                        constexpr uint32_t kOnes = 0x7F7F7F7Fu;
+                        if ((pages.count > 0 && !c0) || (pages.count > 1 && !c1)) {
+#pragma unroll 1
+                            for (int i = 0; i < 16; ++i)
+                                if (i < 8 ? !c0 : !c1) sts4(to + i * 16, kOnes, kOnes, kOnes, kOnes);
+                            fence_proxy_async_smem();
+                        }
+                        arrive_expect_tx(cf, (c0 ? 2 * SPEC_PAGE : 0) + (c1 ? 2 * SPEC_PAGE : 0));
+                        if (c0) bulk_load(to, p.scales + (size_t)pages.z0 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, cf);
+                        if (c1) bulk_load(to + 2 * SPEC_PAGE, p.scales + (size_t)pages.z1 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, cf);
+                        arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD));
+                        if (pages.count > 0) tile_load(dst, &p.mk, pages.z0, full);
+                        if (pages.count > 1) tile_load(dst + SPEC_PAGE * HD, &p.mk, pages.z1, full);
                     }
                     __syncwarp();
                     kr.step();
@@ -325,133 +512,139 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
                 if (w.seg == 0 && w.c0 > 0) into = w.meta(deal);
             }
             if (lane == 0 && !p.whole) {
-                if (w.seg >= 0 && w.c1 < w.chunks && w.u - w.c1 >= begin) from = w.meta(deal);
+                if (w.seg >= 0 && w.c0 == 0 && w.c1 > 0 && w.c1 < w.chunks) from = w.meta(deal);
                 p.meta[2 * blockIdx.x] = into;
                 p.meta[2 * blockIdx.x + 1] = from;
             }
-            if (lane == 0 && *deadp) {          // every buffer's last copy, as far as one was issued
+            if (lane == 0 && *dead) {          // every buffer's last copy, as far as one was issued
 #pragma unroll 1
-                for (int i = 0; i < NK; ++i) drain(&sh.k_full[i], i < kr.at ? kr.round : kr.round ^ 1);
+                for (int i = 0; i < NK; ++i) give_up(BAR(k_full, i), i < kr.at ? kr.round : kr.round ^ 1);
 #pragma unroll 1
-                for (int i = 0; i < kScaleSlots; ++i) drain(&sh.c_full[i], i < cr.at ? cr.round : cr.round ^ 1);
+                for (int i = 0; i < kScaleSlots; ++i) give_up(BAR(c_full, i), i < cr.at ? cr.round : cr.round ^ 1);
             }
         } else if (warp == kLoadVWarp) {
             // ---------------- V copies ----------------
             Ring<NV> vr;
+            const uint32_t va = kept(smem_u32(vslots));
             bool ok = true;
 #pragma unroll 1
             for (;;) {
-                const Seg s = take(false);
-                ok = __all_sync(0xffffffffu, !*deadp);
+                const Seg s = take();
+                ok = __all_sync(0xffffffffu, !*dead);
                 if (!ok || s.units == 0) break;
                 PageWalk pages;
 #pragma unroll 1
                 for (int k = 0; k < s.units; ++k) {
                     pages.at(p, s, k, lane);
-                    ok = __all_sync(0xffffffffu, wait(&sh.v_empty[vr.at], vr.round ^ 1, deadp));
+                    ok = wait(BAR(v_empty, vr.at), vr.round ^ 1, dead);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (elect_one()) {
-                        uint64_t* full = &sh.v_full[vr.at];
-                        uint8_t* dst = vslots + vr.at * L::kSlot;
-                        mbar_arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD));
-                        if (pages.count > 0) tma3(dst, &p.mv, 0, 0, pages.z0, full);
-                        if (pages.count > 1) tma3(dst + SPEC_PAGE * HD, &p.mv, 0, 0, pages.z1, full);
+                        const uint32_t full = BAR(v_full, vr.at), dst = va + vr.at * L::kSlot;
+                        arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD));
+                        if (pages.count > 0) tile_load(dst, &p.mv, pages.z0, full);
+                        if (pages.count > 1) tile_load(dst + SPEC_PAGE * HD, &p.mv, pages.z1, full);
                     }
                     __syncwarp();
                     vr.step();
                 }
                 if (!ok) break;
             }
-            if (lane == 0 && *deadp) {
+            if (lane == 0 && *dead) {
 #pragma unroll 1
-                for (int i = 0; i < NV; ++i) drain(&sh.v_full[i], i < vr.at ? vr.round : vr.round ^ 1);
+                for (int i = 0; i < NV; ++i) give_up(BAR(v_full, i), i < vr.at ? vr.round : vr.round ^ 1);
             }
         } else if (warp == kScoreWarp) {
-            // ---------------- MMAs of S^T (one elected thread) ----------------
-            if (elect_one()) {
-                Ring<NK> ks;
-                Ring<NQ> qr;
-                Ring<2> sb;
-                const uint32_t sa = smem_u32(kslots), qa = smem_u32(qs);
-                bool ok = true;
+            // ---------------- MMAs of S^T (the warp waits, one elected thread issues) ----------------
+            Ring<NK> ks;
+            Ring<2> qr;
+            Ring<NS> sb;
+            const uint32_t sa = kept(smem_u32(kslots)), qa = kept(smem_u32(qs));
+            bool ok = true;
 #pragma unroll 1
-                while (ok) {
-                    const Seg s = take(true);
-                    ok = !*deadp;
-                    if (!ok || s.units == 0) break;
-                    ok = wait(&sh.q_full[qr.at], qr.round, deadp);
-                    const uint32_t id = idesc8(128, (s.R + 15) & ~15, 0, 0);
-                    const uint32_t dq = lo_desc(qa + qr.at * L::kQ, 16);
-                    constexpr uint32_t kHi = hi_swizzled<HD>(8 * HD);
+            while (ok) {
+                const Seg s = take();
+                ok = __all_sync(0xffffffffu, !*dead);
+                if (!ok || s.units == 0) break;
+                ok = wait(BAR(q_full, qr.at), qr.round, dead);
+                const uint32_t id = idesc8(128, (s.R + 15) & ~15, 0, 0);
+                const uint32_t dq = lo_desc(qa + qr.at * L::kQ, 16);
+                constexpr uint32_t kHi = hi_swizzled<HD>(8 * HD);
 #pragma unroll 1
-                    for (int k = 0; k < s.units && ok; ++k) {
-                        ok = wait(&sh.k_full[ks.at], ks.round, deadp) && wait(&sh.s_empty[sb.at], sb.round ^ 1, deadp);
-                        if (!ok) break;
-                        tc_fence_after();
+                for (int k = 0; k < s.units; ++k) {
+                    ok = wait(BAR(k_full, ks.at), ks.round, dead) && ok;
+                    ok = wait(BAR(s_empty, sb.at), sb.round ^ 1, dead) && ok;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
                         const uint32_t dk = lo_desc(sa + ks.at * L::kSlot, 16);
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
                             for (int e = 0; e < HD / 32; ++e)
                                 umma8_lo(tmem + sb.at * RP, dk + e * 2, kHi, dq + part * (L::kQPart >> 4) + e * 2, kHi, id, (part | e) != 0);
-                        umma_commit(&sh.s_full[sb.at]);
-                        umma_commit(&sh.k_empty[ks.at]);
-                        ks.step();
-                        sb.step();
+                        commit(BAR(s_full, sb.at));
+                        commit(BAR(k_empty, ks.at));
+                        if (k == s.units - 1) commit(BAR(q_empty, qr.at));
                     }
-                    if (ok) umma_commit(&sh.q_empty[qr.at]);
-                    qr.step();
+                    __syncwarp();
+                    ks.step();
+                    sb.step();
                 }
-                if (!ok || *deadp) {
-                    umma_commit(&sh.fin[0]);
-                    drain(&sh.fin[0], 0);
-                }
+                qr.step();
             }
-        } else {   // warp 9
-            // ---------------- MMAs of O^T (one elected thread) ----------------
-            if (elect_one()) {
-                Ring<NV> vs;
-                Ring<NP> pr;
-                const uint32_t sa = smem_u32(vslots), pa = smem_u32(ps);
-                bool ok = true;
-                int j = 0;                      // unit
+            if (*dead) {
+                if (elect_one()) commit(BAR(fin, 0));
+                __syncwarp();
+                give_up(BAR(fin, 0), 0);
+            }
+        } else {
+            // ---------------- MMAs of O^T (the same) ----------------
+            Ring<NV> vs;
+            Ring<2> pr;
+            const uint32_t sa = kept(smem_u32(vslots)), pa = kept(smem_u32(ps));
+            bool ok = true;
+            int j = 0;                          // unit
 #pragma unroll 1
-                for (int seg = 0; ok; ++seg) {
-                    const Seg s = take(true);
-                    ok = !*deadp;
-                    if (!ok || s.units == 0) break;
-                    ok = wait(&sh.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1, deadp);
-                    // A = V^T and B = P^T, both MN-major
-                    const uint32_t id = idesc8(128, kStack ? kParts * RP : (s.R + 15) & ~15, 0, 1) | (1u << 15) | (1u << 16);
+            for (int seg = 0; ok; ++seg) {
+                const Seg s = take();
+                ok = __all_sync(0xffffffffu, !*dead);
+                if (!ok || s.units == 0) break;
+                ok = wait(BAR(o_empty, seg & 1), ((seg >> 1) & 1) ^ 1, dead);
+                // A = V^T and B = P^T, both MN-major
+                constexpr uint32_t id = idesc8(128, kParts * RP, 0, 1) | (1u << 15) | (1u << 16);
 #pragma unroll 1
-                    for (int k = 0; k < s.units && ok; ++k, ++j) {
-                        ok = wait(&sh.p_full[pr.at], pr.round, deadp) && wait(&sh.v_full[vs.at], vs.round, deadp);
-                        if (!ok) break;
-                        tc_fence_after();
+                for (int k = 0; k < s.units; ++k, ++j) {
+                    ok = wait(BAR(v_full, vs.at), vs.round, dead) && ok;
+                    ok = wait(BAR(p_full, pr.at), pr.round, dead) && ok;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
                         // P^T: core matrices of 16 rows (of the product's N) x 8 keys, 128 bytes apart along the keys
                         const uint32_t dp = lo_desc(pa + pr.at * kParts * L::kP, 128);
                         const uint32_t dv = lo_desc(sa + vs.at * L::kSlot, 1024);
                         constexpr uint32_t kHiV = hi_swizzled<HD>(8 * HD), kHiP = (kChunk * 16 >> 4) | (1u << 14);
                         const int og = kStream ? (seg & 1) * 2 + (j & 1) : seg & 1;
-                        const uint32_t o = tmem + 2 * RP + og * L::kO;
+                        const uint32_t o = tmem + NS * RP + og * L::kO;
                         const bool more = k >= kGroups;     // this O^T holds earlier chunks
 #pragma unroll
-                        for (int part = 0; part < (kStack ? 1 : kParts); ++part)
-#pragma unroll
-                            for (int e = 0; e < kChunk / 32; ++e)
-                                umma8_lo(o, dv + e * (32 * HD >> 4), kHiV, dp + part * (L::kP >> 4) + e * (32 * 16 >> 4), kHiP, id,
-                                         more || (part | e) != 0);
-                        umma_commit(&sh.v_empty[vs.at]);
-                        umma_commit(&sh.p_empty[pr.at]);
-                        vs.step();
-                        pr.step();
+                        for (int e = 0; e < kChunk / 32; ++e)
+                            umma8_lo(o, dv + e * (32 * HD >> 4), kHiV, dp + e * (32 * 16 >> 4), kHiP, id, more || e != 0);
+                        commit(BAR(v_empty, vs.at));
+                        commit(BAR(p_empty, pr.at));
+                        if (k == s.units - 1) commit(BAR(o_full, seg & 1));
                     }
-                    if (ok) umma_commit(&sh.o_full[seg & 1]);
+                    __syncwarp();
+                    vs.step();
+                    pr.step();
                 }
-                if (!ok || *deadp) {
-                    umma_commit(&sh.fin[1]);
-                    drain(&sh.fin[1], 0);
-                }
+            }
+            if (*dead) {
+                if (elect_one()) commit(BAR(fin, 1));
+                __syncwarp();
+                give_up(BAR(fin, 1), 0);
             }
         }
         __syncwarp();
@@ -459,285 +652,268 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
         // ---------------- softmax: thread = key ----------------
         regs_up<L::kSoftRegs>();
         const int wg = warp >> 2, qd = warp & 3;
-        const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
+        const uint32_t lanes = kept(tmem + ((uint32_t)(qd * 32) << 16));
         const int key = qd * 32 + lane;
-        const int col0 = kStream ? 0 : wg * NC; // the thread's first row
-        const int gi = kStream ? wg : 0;        // its reference and O^T
+        const int gi = kStream ? wg / kTeam : 0;    // its team: which chunks, references and O^T
+        const int col0 = (wg % kTeam) * NC;         // the thread's first row
         const int bar = kSoftBar + wg;
-        int i = 0;                              // unit
-        Ring<NV> vs;                            // slot of the next unit's V
-        Ring<kScaleSlots> cs;                   // and of its scales
-        bool ok = true;
+        const uint32_t scales = kept(shb + (uint32_t)offsetof(F, scale) + (key >> 6) * 2 * SPEC_PAGE + (key & 63));
+        const uint32_t weights = kept(smem_u32(ps) + (col0 >> 4) * (kChunk * 16) + key * 16);
+        int unit = 0;                           // the segment's first unit
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
-            const Seg w = take(false);
-            if (bar_any(bar, 128, *deadp != 0) || w.units == 0) break;   // after a wait that gave up, all of the warpgroup leaves
+            const Seg w = take();
+            if (bar_any(bar, 128, *dead != 0) || w.units == 0) break;   // after a wait that gave up, all of the warpgroup leaves
             const int par = seg & 1, last0 = w.last0, rows = w.R - col0;   // live rows of this thread
-            float* const mine = sh.nref[par][gi];
-            const float* const qmul = sh.qmul[par];
-            ok = ok && wait(&sh.l_empty[par], ((seg >> 1) & 1) ^ 1, deadp);   // the results of two segments ago have been read
-            ok = ok && wait(&sh.r_full[par], (seg >> 1) & 1, deadp);          // the query rows' powers of two are there
-            F2 l[NC / 2];
+            const int active = min((w.R + NC - 1) / NC, kTeam);     // warpgroups of the team with rows
+            const bool speaks = key == 0;       // for the warpgroup
+            const uint32_t mine = kept(shb + (uint32_t)offsetof(F, nref) + ((par * kGroups + gi) * RP + col0) * 4);
+            const uint32_t qmul = kept(shb + (uint32_t)offsetof(F, qmul) + (par * RP + col0) * 4);
+            wait(BAR(l_empty, par), ((seg >> 1) & 1) ^ 1, dead);     // the results of two segments ago have been read
+            wait(BAR(r_full, par), (seg >> 1) & 1, dead);            // the query rows' powers of two are there
+            F2 l[NC / 2];                       // the rows' sums over this thread's keys
 #pragma unroll
             for (int j = 0; j < NC / 2; ++j) l[j] = F2(0.f, 0.f);
-            bool fresh = true, wide = false;    // wide: a reference past 2^24, every chunk takes rounded products
+            bool fresh = true;
             int vref = 0;                       // scale byte that O^T is relative to
 #pragma unroll 1
-            for (int c = w.c0; c < w.c0 + w.units; ++c, ++i) {
-                const Ring<NV> v0 = vs;         // the chunk's V
-                vs.step();
-                const Ring<kScaleSlots> c0 = cs;
-                cs.step();
-                if (kStream && (i & 1) != wg) continue;
-                const uint32_t st = lanes + (i & 1) * RP + col0;
-                const int kp = c * kChunk + key;
-                const bool masked = (c + 1) * kChunk - 1 > last0;   // some row does not see all of the chunk
-                ok = ok && wait(&sh.c_full[c0.at], c0.round, deadp);
-                int kb = sh.scale[c0.at][key >> 6][0][key & 63], vb = sh.scale[c0.at][key >> 6][1][key & 63];
-                if (kp >= w.len) kb = 127, vb = 0;      // no position: whatever stands there
-                const bool nan = kb == 255 || vb == 255;
-                if (nan) kb = 127, vb = 0;
-                const float km = scale_of(kb);
-                const F2 km2(km, km);
-                ok = ok && wait(&sh.s_full[i & 1], (i >> 1) & 1, deadp);
+            for (int i = unit + (kStream ? (unit ^ gi) & 1 : 0); i < unit + w.units; i += kGroups) {
+                const uint32_t b = i & 1, use = (i >> 1) & 1;       // P^T buffer, its round
+                if (rows <= 0) {
+                    // No rows here: one warp keeps up with the team's barriers (a barrier's
+                    // parity is only sound for one that sees every phase: its lanes join
+                    // before one arrives, or the phase is over before the last has looked).
+                    if (qd == 0) {
+                        wait(BAR(s_full, i % NS), (i / NS) & 1, dead);
+                        __syncwarp();
+                        arrive_if(BAR(s_empty, i % NS), speaks);
+                        arrive_if(BAR(c_empty, i % kScaleSlots), speaks);
+                        wait(BAR(p_empty, b), use ^ 1, dead);
+                        __syncwarp();
+                        arrive_if(BAR(p_full, b), speaks);
+                    }
+                    continue;
+                }
+                const uint32_t st = lanes + i % NS * RP + col0;
+                const int kp = (w.c0 + i - unit) * kChunk + key;
+                const bool masked = kp - key + kChunk - 1 > last0;  // some row does not see all of the chunk
+                // One warp waits for the warpgroup.
+                if (qd == 0) {
+                    wait(BAR(c_full, i % kScaleSlots), (i / kScaleSlots) & 1, dead);
+                    wait(BAR(s_full, i % NS), (i / NS) & 1, dead);
+                }
+                named_bar_sync(bar, 128);
                 tc_fence_after();
-                float s[NC];
-                // this thread's P^T buffer is free (and its rows' O^T complete) once their last product is
-                auto product_done = [&]() {
-                    ok = ok && wait(&sh.p_empty[kStream ? i & 1 : 0], ((kStream ? i >> 1 : i) & 1) ^ 1, deadp);
-                };
-                // the chunk's products, NaN under a scale that is none, -inf where a row does not see the key
-                auto load = [&]() {
-#pragma unroll
-                    for (int j = 0; j < NC; j += kSpan)
-                        if (j < rows) {
-                            if constexpr (kSpan == 8) tmem_ld8_async(st + j, s + j);
-                            else if constexpr (kSpan == 16) tmem_ld16_async(st + j, s + j);
-                            else tmem_ld32_async(st + j, s + j);
-                        }
+                // the key's scales; NaN ones make its visible scores NaN, behind the length they are whatever stands there
+                const uint32_t sc = scales + i % kScaleSlots * 4 * SPEC_PAGE;
+                int vb = 0;
+                float x[NC];                    // the rows' scores, then weights
+#pragma unroll 1
+                for (bool move = fresh;; move = true) {
+                    tmem_ld16_async(st, x);
+                    const int kb = lds_u8(sc);
+                    vb = lds_u8(sc + SPEC_PAGE);
+                    const float km = max(kb, vb) == 255 ? __uint_as_float(0x7FC00000u) : scale_of(kb);
+                    if (vb == 255 || kp >= w.len) vb = 0;
+                    const F2 km2(km, km);
+                    // rows are in token order: the key is hidden from the tokens before it
+                    const int hidden = min(max(kp - last0, 0), RP) * p.group - w.skip - col0;
                     tmem_wait_ld();
-                    if (nan) {
-#pragma unroll
-                        for (int j = 0; j < NC; ++j) s[j] = __uint_as_float(0x7FC00000u);
-                    }
-                    if (masked) {
-                        // rows are in token order: the key is hidden from the tokens before it
-                        const int hidden = min(max(kp - last0, 0), RP) * p.group - col0;
-#pragma unroll
-                        for (int j = 0; j < NC; ++j)
-                            if (j < hidden) s[j] = -INFINITY;
-                    }
-                };
-                load();
-                if (rows > 0) {
-                    bool move = fresh || wide;
-                    if (!move) {
-                        float top[2] = {kNone, kNone};
-#pragma unroll
-                        for (int j0 = 0; j0 < NC; j0 += kSpan)
-                            if (j0 < rows) {
-#pragma unroll
-                                for (int j = j0; j < j0 + kSpan; j += 4) {
-                                    const float4 m = *reinterpret_cast<const float4*>(&mine[col0 + j]);
-                                    const float4 f = *reinterpret_cast<const float4*>(&qmul[col0 + j]);
-                                    fma2(mul2(F2(s[j], s[j + 1]), km2), F2(f.x, f.y), F2(m.x, m.y)).get(s[j], s[j + 1]);
-                                    fma2(mul2(F2(s[j + 2], s[j + 3]), km2), F2(f.z, f.w), F2(m.z, m.w)).get(s[j + 2], s[j + 3]);
-                                    top[j / 4 & 1] = fmaxf(top[j / 4 & 1], fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
-                                }
-                            }
-                        const float above = fmaxf(top[0], top[1]);
-                        move = bar_any(bar, 128, above + (float)max(vb - vref, 0) > kLimit8 && above > -1e30f || vb - vref > kFarScale);
-                        if (move) load();
-                    }
                     if (move) {
                         // The references move up to the chunk's maxima (a first chunk's become
-                        // them), the sums and O^T with them.  So that a reference and the score
-                        // that it comes from cancel whatever their size, the scores are here
-                        // rounded products, as it is: the fused product of a score past 2^24
-                        // differs from it by powers of two, past 2^31 by more than a weight can hold.
+                        // them), the sums and O^T with them.
                         float (*const mx)[RP] = sh.xl[par][gi];
+#pragma unroll 1
+                        for (int j = 0; j < NC && j < rows; j += 8) {
+                            float v[8], keep = 0.f;
+                            tmem_ld8_async(st + j, v);
+                            const float4 f = lds4(qmul + j * 4), g = lds4(qmul + j * 4 + 16);
+                            const float fs[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int j0 = 0; j0 < NC; j0 += kSpan)
-                            if (j0 < rows) {
-                                float keep = 0.f;
-#pragma unroll
-                                for (int j = j0; j < j0 + kSpan; j += 4) {
-                                    const float4 f = *reinterpret_cast<const float4*>(&qmul[col0 + j]);
-                                    mul2(mul2(F2(s[j], s[j + 1]), km2), F2(f.x, f.y)).get(s[j], s[j + 1]);
-                                    mul2(mul2(F2(s[j + 2], s[j + 3]), km2), F2(f.z, f.w)).get(s[j + 2], s[j + 3]);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float m = warp_max(s[j + e]);
-                                        if (lane == ((j + e) & (kSpan - 1))) keep = m;
-                                    }
-                                }
-                                if (lane < kSpan) mx[qd][col0 + j0 + lane] = keep;
+                            for (int e = 0; e < 8; ++e) {
+                                const float m = warp_max(j + e < hidden ? -INFINITY : v[e] * km * fs[e]);
+                                if (lane == e) keep = m;
                             }
+                            if (lane < 8) mx[qd][col0 + j + lane] = keep;
+                        }
                         const int vt = __reduce_max_sync(0xffffffffu, vb);
                         if (lane == 0) sh.vtop[wg][qd] = vt;
-                        if (!fresh) {
-                            product_done();
-                            tc_fence_after();
-                        }
+                        // the last product into this O^T: of this team's chunk before
+                        if (!fresh && qd == 0) wait(BAR(p_empty, (i - kGroups) & 1), ((i - kGroups) >> 1) & 1, dead);
                         named_bar_sync(bar, 128);
-                        const int vnow = max(max(max(sh.vtop[wg][0], sh.vtop[wg][1]), max(sh.vtop[wg][2], sh.vtop[wg][3])), fresh ? 0 : vref);
-                        float now = 0.f;
+                        tc_fence_after();
+                        int vnow = max(max(sh.vtop[wg][0], sh.vtop[wg][1]), max(sh.vtop[wg][2], sh.vtop[wg][3]));
+                        if (!fresh && vnow <= vref + kNearScale) vnow = vref;
+                        const float vshrink = scale_of(max(vref - vnow + 127, 0));      // 1 or less (not used at first)
                         if (key < NC) {         // one thread per row: the new reference, and what the old weights shrink by
                             const int r = col0 + key;
                             const float m = fmaxf(fmaxf(mx[0][r], mx[1][r]), fmaxf(mx[2][r], mx[3][r]));
-                            const float old = fresh ? kNone : -mine[r];
-                            now = key < rows ? fmaxf(old, m) : INFINITY;      // rows past R weigh nothing
-                            mine[r] = -now;
-                            mx[0][r] = key < rows ? ex2_approx(old - now) : 0.f;
+                            const float old = fresh ? kNone : -sh.nref[par][gi][r];
+                            const float now = key < rows ? fmaxf(old, m) : INFINITY;      // rows past R weigh nothing
+                            sh.nref[par][gi][r] = -now;
+                            const float f = key < rows ? ex2_approx(old - now) : 0.f;
+                            sh.shrink[gi][r] = f;
+                            sh.oshrink[gi][r] = f * vshrink;
                         }
                         if (key == 0) sh.vref[par][wg] = vnow;
-                        wide = bar_any(bar, 128, key < rows && fabsf(now) > kWide && now > kNone);
+                        named_bar_sync(bar, 128);
                         if (!fresh) {
-                            const float vshrink = scale_of(max(vref - vnow + 127, 0));      // 1 or less
+                            const uint32_t shrink = shb + (uint32_t)offsetof(F, shrink) + (gi * RP + col0) * 4;
+                            const uint32_t oshrink = shb + (uint32_t)offsetof(F, oshrink) + (gi * RP + col0) * 4;
+                            const uint32_t ot = lanes + NS * RP + (kStream ? par * 2 + gi : par) * L::kO + col0;
 #pragma unroll
-                            for (int j = 0; j < NC; j += 2) {
-                                float x, y;
-                                l[j / 2].get(x, y);
-                                l[j / 2] = F2(x * mx[0][col0 + j], y * mx[0][col0 + j + 1]);
+                            for (int j = 0; j < NC; j += 4) {
+                                const float4 f = lds4(shrink + j * 4);
+                                l[j / 2] = mul2(l[j / 2], F2(f.x, f.y));
+                                l[j / 2 + 1] = mul2(l[j / 2 + 1], F2(f.z, f.w));
                             }
-                            const uint32_t ot = lanes + 2 * RP + (kStream ? par * 2 + wg : par) * L::kO + col0;
 #pragma unroll 1
-                            for (int j = 0; j < (kStack ? kParts * NC : NC); j += 8)   // stacked: the other parts' columns follow
-                                if ((kStack ? j & (NC - 1) : j) < rows) {
-                                    float o[8];
-                                    tmem_ld8_async(ot + j, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) o[e] *= mx[0][col0 + (j & (NC - 1)) + e] * vshrink;
-                                    tmem_st8(ot + j, o);
-                                }
+                            for (int j = 0; j < kParts * NC; j += 8) {      // NC rows of each part
+                                if (j % NC >= rows) continue;
+                                const uint32_t at = ot + j / NC * RP + j % NC;
+                                float o[8];
+                                tmem_ld8_async(at, o);
+                                const float4 f = lds4(oshrink + j % NC * 4), g = lds4(oshrink + j % NC * 4 + 16);
+                                tmem_wait_ld();
+                                o[0] *= f.x, o[1] *= f.y, o[2] *= f.z, o[3] *= f.w;
+                                o[4] *= g.x, o[5] *= g.y, o[6] *= g.z, o[7] *= g.w;
+                                tmem_st8(at, o);
+                            }
                             tmem_wait_st();
                         }
                         vref = vnow;
-#pragma unroll
-                        for (int j0 = 0; j0 < NC; j0 += kSpan)
-                            if (j0 < rows) {
-#pragma unroll
-                                for (int j = j0; j < j0 + kSpan; j += 4) {
-                                    const float4 m = *reinterpret_cast<const float4*>(&mine[col0 + j]);
-                                    add2(F2(s[j], s[j + 1]), F2(m.x, m.y)).get(s[j], s[j + 1]);
-                                    add2(F2(s[j + 2], s[j + 3]), F2(m.z, m.w)).get(s[j + 2], s[j + 3]);
-                                }
-                            }
-                        if (!fresh) named_bar_sync(bar, 128);   // everyone has read mx
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh.s_empty[i & 1]);
-                    mbar_arrive(&sh.c_empty[c0.at]);
-                }
-                fresh = false;
-                const int ve = vb - vref + kShift8 + 127;
-                const float vm = __uint_as_float((uint32_t)min(max(ve, 0), 254) << 23);
-                const F2 vm2(vm, vm);
-                product_done();
-                uint8_t* ph = ps + (kStream ? i & 1 : 0) * kParts * L::kP + (col0 >> 4) * (kChunk * 16) + key * 16;
+                    const int dv = vb - vref;
+                    const float vm = __uint_as_float((uint32_t)(min(max(dv, kLowScale), kFarScale) + kShift8 + 127) << 23);
+                    const F2 vm2(vm, vm);
+                    // Scores less their references: rounded products, as a reference is, so that a
+                    // reference and the score that it comes from cancel whatever their size (a fused
+                    // product of a score past 2^24 differs from it by powers of two, past 2^31 by more
+                    // than a weight can hold).
 #pragma unroll
-                for (int j0 = 0; j0 < NC; j0 += kSpan)
-                    if (j0 < rows) {
+                    for (int j = 0; j < NC; j += 4) {
+                        const float4 m = lds4(mine + j * 4), f = lds4(qmul + j * 4);
+                        add2(mul2(mul2(F2(x[j], x[j + 1]), km2), F2(f.x, f.y)), F2(m.x, m.y)).get(x[j], x[j + 1]);
+                        add2(mul2(mul2(F2(x[j + 2], x[j + 3]), km2), F2(f.z, f.w)), F2(m.z, m.w)).get(x[j + 2], x[j + 3]);
+                    }
+                    if (masked && __any_sync(0xffffffffu, hidden > 0)) {        // -inf where a row does not see the key
 #pragma unroll
-                        for (int j = j0; j < j0 + kSpan; j += 8) {
-                            uint32_t c1[4], c2[4], c3[4];
+                        for (int j = 0; j < NC; ++j)
+                            if (j < hidden) x[j] = -INFINITY;
+                    }
+                    wait(BAR(p_empty, b), use ^ 1, dead);       // this P^T buffer's last product is done
+                    uint32_t top = 0;           // the largest halves
+                    static_assert(NC == 16, "a thread's rows are one 16-byte piece of each part");
+                    uint32_t c1[4], c2[4], c3[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const F2 x(ex2_approx(s[j + 2 * e]), ex2_approx(s[j + 2 * e + 1]));
-                                l[j / 2 + e] = add2(l[j / 2 + e], x);
-                                uint32_t h = cvt_f16x2(mul2(x, vm2));
-                                c1[e] = part_e5m2(h);
-                                c2[e] = part_e5m2(h);
-                                c3[e] = last_e5m2(h);
-                            }
-                            uint8_t* dst = ph + (j >> 4) * (kChunk * 16) + (j & 8);
-                            *reinterpret_cast<uint2*>(dst) = make_uint2(c1[0] | c1[1] << 16, c1[2] | c1[3] << 16);
-                            *reinterpret_cast<uint2*>(dst + L::kP) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
-                            *reinterpret_cast<uint2*>(dst + 2 * L::kP) = make_uint2(c3[0] | c3[1] << 16, c3[2] | c3[3] << 16);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t h[2], t1[2], t2[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float &u = x[4 * e + 2 * k], &v = x[4 * e + 2 * k + 1];
+                            u = ex2_approx(u);
+                            v = ex2_approx(v);
+                            h[k] = cvt_f16x2(mul2(F2(u, v), vm2));
+                            top = max_f16x2(top, h[k]);
+                            t1[k] = h[k] & 0xFF00FF00u;                                     // cut to e5m2
+                            h[k] = mul_f16x2(sub_f16x2(h[k], t1[k]), kHalves2);
+                            t2[k] = (h[k] + 0x00800080u) & 0xFF00FF00u;                     // rounded to it
+                            h[k] = mul_f16x2(sub_f16x2(h[k], t2[k]), kHalves3) + 0x00800080u;   // the last part's upper bytes, rounded
                         }
+                        c1[e] = upper_bytes(t1[0], t1[1]);
+                        c2[e] = upper_bytes(t2[0], t2[1]);
+                        c3[e] = upper_bytes(h[0], h[1]);
                     }
-                if (masked && (kStream || wg == 0)) {
-                    // Values of positions that some row does not see: behind the
-                    // length they become zero (a weight of zero does not silence a
-                    // NaN), between the rows' last positions NaN do, and are added at
-                    // the end to the rows that see them.
-                    // (The slot's last V has been consumed: product_done.)
-                    ok = ok && wait(&sh.v_full[v0.at], v0.round, deadp);
-                    uint8_t* const tile = vslots + v0.at * L::kSlot;
-                    if (kp >= w.len) {          // a thread's own row; lanes start at different banks
+                    const uint32_t to = weights + b * kParts * L::kP;
+                    sts4(to, c1[0], c1[1], c1[2], c1[3]);
+                    sts4(to + L::kP, c2[0], c2[1], c2[2], c2[3]);
+                    sts4(to + 2 * L::kP, c3[0], c3[1], c3[2], c3[3]);
+                    if (masked && wg % kTeam == active - 1) {
+                        // Values of positions that some row does not see: behind the
+                        // length they become zero (a weight of zero does not silence a
+                        // NaN), between the rows' last positions NaN do, and are added at
+                        // the end to the rows that see them.
+                        // (The slot's last V has been consumed: its product came before this P^T buffer's last.)
+                        wait(BAR(v_full, i % NV), (i / NV) & 1, dead);
+                        uint8_t* const tile = vslots + i % NV * L::kSlot;
+                        if (kp >= w.len) {          // a thread's own row; lanes start at different banks
 #pragma unroll
-                        for (int e = 0; e < HD / 16; ++e)
-                            *reinterpret_cast<uint4*>(tile + key * HD + (((e + lane) & (HD / 16 - 1)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    const int from = max(0, last0 + 1 - c * kChunk), to = min(kChunk, w.len - c * kChunk);
+                            for (int e = 0; e < HD / 16; ++e)
+                                *reinterpret_cast<uint4*>(tile + key * HD + (((e + lane) & (HD / 16 - 1)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        const int from = max(0, last0 + 1 - (kp - key)), to = min(kChunk, w.len - (kp - key));
 #pragma unroll 1
-                    for (int t = from * (HD / 16) + key; t < to * (HD / 16); t += 128) {
-                        uint4* const at = reinterpret_cast<uint4*>(tile + t * 16);
-                        uint4 x = *at;
-                        uint32_t* y = &x.x;
-                        bool hit = false;
+                        for (int t = from * (HD / 16) + key; t < to * (HD / 16); t += 128) {
+                            uint4* const at = reinterpret_cast<uint4*>(tile + t * 16);
+                            uint4 x = *at;
+                            uint32_t* y = &x.x;
+                            bool hit = false;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t n = ((y[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;    // the bytes that are NaN
-                            if (n) hit = true, y[k] &= ~((n >> 7) * 255u);
-                        }
-                        if (hit) {
-                            *at = x;
-                            sh.poison[par] = seg + 1;
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t n = ((y[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;    // the bytes that are NaN
+                                if (n) hit = true, y[k] &= ~((n >> 7) * 255u);
+                            }
+                            if (hit) {
+                                *at = x;
+                                sh.poison[par] = seg + 1;
+                            }
                         }
                     }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    // Weights that overflow a half: the references move, and the chunk is taken again.
+                    const bool over = ((top + 0x04000400u) & 0x80008000u) != 0 || dv > kFarScale;
+                    if (!bar_any(bar, 128, over && !move) || move) break;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[kStream ? i & 1 : 0]);
+#pragma unroll
+                for (int j = 0; j < NC; j += 2) l[j / 2] = add2(l[j / 2], F2(x[j], x[j + 1]));
+                fresh = false;
+                arrive_if(BAR(s_empty, i % NS), speaks);
+                arrive_if(BAR(c_empty, i % kScaleSlots), speaks);
+                arrive_if(BAR(p_full, b), speaks);
             }
-            // sums over the warp's keys, a span of rows at a time: lanes exchange halves
-            // until lane r holds row r, then lanes of the same row are added
+            unit += w.units;
+            // sums over the warp's keys: lanes exchange halves until lane r holds row r, then
+            // lanes of the same row are added
+            if (rows > 0) {
+                float v[NC];
 #pragma unroll
-            for (int j = 0; j < NC; j += kSpan)
-                if (j < rows) {
-                    float x[kSpan];
+                for (int e = 0; e < NC; e += 2) l[e / 2].get(v[e], v[e + 1]);
 #pragma unroll
-                    for (int e = 0; e < kSpan; e += 2) l[(j + e) / 2].get(x[e], x[e + 1]);
+                for (int h = NC / 2; h >= 1; h >>= 1) {
+                    const bool up = lane & h;
 #pragma unroll
-                    for (int h = kSpan / 2; h >= 1; h >>= 1) {
-                        const bool up = lane & h;
-#pragma unroll
-                        for (int e = 0; e < h; ++e) {
-                            const float give = up ? x[e] : x[e + h], keep = up ? x[e + h] : x[e];
-                            x[e] = keep + __shfl_xor_sync(0xffffffffu, give, h);
-                        }
+                    for (int e = 0; e < h; ++e) {
+                        const float give = up ? v[e] : v[e + h], keep = up ? v[e + h] : v[e];
+                        v[e] = keep + __shfl_xor_sync(0xffffffffu, give, h);
                     }
-#pragma unroll
-                    for (int h = kSpan; h < 32; h <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], h);
-                    if (lane < kSpan) sh.xl[par][gi][qd][col0 + j + lane] = x[0];
                 }
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+                if (lane < NC) sh.xl[par][gi][qd][col0 + lane] = v[0];
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.l_full[par]);
+            arrive_if(BAR(l_full, par), lane == 0);
         }
     } else {
         // ---------------- the next segment's queries, and results: thread = head dimension ----------------
-        if constexpr (L::kResultRegs < 128) regs_down<L::kResultRegs>();
+        regs_down<L::kResultRegs>();
         const int qd = warp & 3, d = qd * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
-        Ring<NQ> qr;
+        Ring<2> qr;
         // Queries in two e4m3 parts with a power of two for each row, 8 elements a thread.
         auto split_queries = [&](const Seg& s, int par) {
             constexpr int kRowThreads = HD / 8, kPass = 128 / kRowThreads;
-            bool ok = wait(&sh.q_empty[qr.at], qr.round ^ 1, deadp);
+            wait(BAR(q_empty, qr.at), qr.round ^ 1, dead);
             uint8_t* const tile = qs + qr.at * L::kQ;
             const int b = d & (kRowThreads - 1);
 #pragma unroll 1
             for (int r0 = 0; r0 < s.R; r0 += kPass) {
-                const int r = r0 + d / kRowThreads, t = sh.tok[min(r, s.R - 1)];
+                const int r = r0 + d / kRowThreads, t = token(s, min(r, s.R - 1));
                 uint4 x = {};
                 if (r < s.R)
                     x = *reinterpret_cast<const uint4*>(p.q + (long long)(s.row0 + t) * p.q_stride +
-                                                        (long long)(s.head * p.group + r - t * p.group) * HD + b * 8);
+                                                        (long long)(s.head * p.group + s.skip + r - t * p.group) * HD + b * 8);
                 const uint32_t* y = &x.x;
                 uint32_t top = 0;               // largest finite magnitude
 #pragma unroll
@@ -768,29 +944,27 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.q_full[qr.at]);
-                mbar_arrive(&sh.r_full[par]);
-            }
+            arrive_if(BAR(q_full, qr.at), lane == 0);
+            arrive_if(BAR(r_full, par), lane == 0);
             qr.step();
-            return ok;
         };
         int i = 0;                              // the segment's first unit
-        Seg next = take(false);
-        bool gone = bar_any(kResultBar, 128, *deadp != 0);
+        Seg next = take();
+        bool gone = bar_any(kResultBar, 128, *dead != 0);
         if (!gone && next.units) split_queries(next, 0);
 #pragma unroll 1
         for (int seg = 0; !gone && next.units; ++seg) {
             const Seg w = next;
-            next = take(false);
-            gone = bar_any(kResultBar, 128, *deadp != 0);
+            next = take();
+            gone = bar_any(kResultBar, 128, *dead != 0);
             if (gone) break;
             if (next.units) split_queries(next, (seg + 1) & 1);
             const int par = seg & 1, last0 = w.last0;
-            const int ga = kStream ? i & 1 : 0; // the warpgroup of the first unit; the other has none in a segment of one
+            const int ga = kStream ? i & 1 : 0; // the team of the first unit; the other has none in a segment of one
             const bool two = kStream && w.units > 1, whole = w.slot < 0;
             i += w.units;
-            bool ok = wait(&sh.l_full[par], (seg >> 1) & 1, deadp, plan::wait_rounds(w.units));
+            if (qd == 0) wait(BAR(l_full, par), (seg >> 1) & 1, dead, plan8::wait_rounds(w.units));
+            named_bar_sync(kResultBar, 128);
             if (d < w.R) {
                 const int r = d;
                 auto sum = [&](int g) { return sh.xl[par][g][0][r] + sh.xl[par][g][1][r] + sh.xl[par][g][2][r] + sh.xl[par][g][3][r]; };
@@ -812,88 +986,69 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
                 } else {
                     p.part_ml[(size_t)w.slot * RP + r] = make_float2(ma, la);
                 }
-                // O^T is in units of 2^(r - 8), r the warpgroup's that formed the row's weights
-                fa = fa * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][kStream ? ga : r / NC]);
-                if (two) fb = fb * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][ga ^ 1]);
+                // O^T is in units of 2^(r - 3), r the warpgroup's that formed the row's weights
+                fa = fa * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][ga * kTeam + r / NC]);
+                if (two) fb = fb * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][(ga ^ 1) * kTeam + r / NC]);
                 sh.weight[par][r] = {fa, fb};
             }
+            if (qd == 0) wait(BAR(o_full, par), (seg >> 1) & 1, dead);
             named_bar_sync(kResultBar, 128);
             const bool bad = sh.poison[par] == seg + 1;
-            ok = ok && wait(&sh.o_full[par], (seg >> 1) & 1, deadp);
             tc_fence_after();
-            uint16_t* const out = p.out + (long long)w.row0 * p.out_stride + (long long)w.head * p.group * HD + d;
+            uint16_t* const out = p.out + (long long)w.row0 * p.out_stride + ((long long)w.head * p.group + w.skip) * HD + d;
             float* const part = p.part_o + (size_t)(whole ? 0 : w.slot) * RP * HD + d;
-            // rows whose O^T is in flight together (more would be more instructions than the cache likes)
-            constexpr int kStep = kStack ? 8 : 16;
 #pragma unroll 1
-            for (int j0 = 0; j0 < w.R; j0 += kStep) {
-                // the rows' O^T of the first warpgroup, and of the other
-                float o[kStep], y[kStep];
-                const uint32_t at = lanes + 2 * RP + (kStream ? par * 2 + ga : par) * L::kO + j0;
-                const uint32_t bt = lanes + 2 * RP + (par * 2 + (ga ^ 1)) * L::kO + j0;
-                auto ld = [](uint32_t a, float* r) {
-                    if constexpr (kStack) {     // its three parts
-                        float u[kStep], v[kStep];
-                        tmem_ld8_async(a, r);
-                        tmem_ld8_async(a + RP, u);
-                        tmem_ld8_async(a + 2 * RP, v);
-                        tmem_wait_ld();
+            for (int j0 = 0; j0 < w.R; j0 += 8) {
+                // 8 rows' O^T of the first team (its three parts), and of the other
+                float o[8], y[8];
+                auto ld = [&](int g, float* r) {
+                    const uint32_t at = lanes + NS * RP + (kStream ? par * 2 + g : par) * L::kO + j0;
+                    float u[8], v[8];
+                    tmem_ld8_async(at, r);
+                    tmem_ld8_async(at + RP, u);
+                    tmem_ld8_async(at + 2 * RP, v);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < kStep; ++e) r[e] += u[e] + v[e];
-                    } else {
-                        tmem_ld16_async(a, r);
-                        tmem_wait_ld();
-                    }
+                    for (int e = 0; e < 8; ++e) r[e] += (u[e] + v[e] * (1.f / kPart3)) * (1.f / kPart2);
                 };
-                ld(at, o);
-                if (two) ld(bt, y);
+                ld(ga, o);
+                if (two) ld(ga ^ 1, y);
 #pragma unroll
-                for (int e = 0; e < kStep; ++e) {
-                    const plan::Pair f = sh.weight[par][j0 + e];
+                for (int e = 0; e < 8; ++e) {
+                    const plan8::Pair f = sh.weight[par][j0 + e];
                     o[e] *= f.x;
                     if (two) o[e] += y[e] * f.y;
                 }
                 if (d < HD) {
                     if (bad)                    // of the positions that some row of the block sees and some does not
 #pragma unroll 1
-                        for (int t = max(last0 + 1, w.c0 * kChunk); t < min(last0 + sh.tok[w.R - 1] + 1, (w.c0 + w.units) * kChunk); ++t) {
+                        for (int t = max(last0 + 1, w.c0 * kChunk); t < min(last0 + token(w, w.R - 1) + 1, (w.c0 + w.units) * kChunk); ++t) {
                             const int page = p.tables[(size_t)w.q * p.table_pages + t / SPEC_PAGE];
                             if (page < 0 || page >= p.num_pages) continue;
                             const int code = p.vpool[(((size_t)page * p.hkv + w.head) * SPEC_PAGE + t % SPEC_PAGE) * HD + d];
                             if ((code & 0x7F) == 0x7F)
 #pragma unroll
-                                for (int e = 0; e < kStep; ++e)
-                                    if (t <= last0 + sh.tok[j0 + e]) o[e] = __uint_as_float(0x7FC00000u);
+                                for (int e = 0; e < 8; ++e)
+                                    if (t <= last0 + token(w, j0 + e)) o[e] = __uint_as_float(0x7FC00000u);
                         }
                     if (whole) {
-                        if (last0 < 0) {        // rows without a position
 #pragma unroll
-                            for (int e = 0; e < kStep; ++e)
-                                if (last0 + sh.tok[j0 + e] < 0) o[e] = 0.f;
-                        }
-                        // (the offsets first: a guard around each load would wait for each)
-#pragma unroll
-                        for (int e0 = 0; e0 < kStep; e0 += 8) {
-                            long long off[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) off[e] = sh.col_off[j0 + e0 + e];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (j0 + e0 + e < w.R) out[off[e]] = f2bf(o[e0 + e]);
+                        for (int e = 0; e < 8; ++e) {
+                            const int t = token(w, j0 + e);
+                            if (j0 + e < w.R)       // (a row without a position: zeros)
+                                out[t * p.out_stride + (long long)(j0 + e - t * p.group) * HD] = last0 + t < 0 ? (uint16_t)0 : f2bf(o[e]);
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < kStep; ++e)
+                        for (int e = 0; e < 8; ++e)
                             if (j0 + e < w.R) part[(j0 + e) * HD] = o[e];
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.o_empty[par]);
-                mbar_arrive(&sh.l_empty[par]);
-            }
+            arrive_if(BAR(o_empty, par), lane == 0);
+            arrive_if(BAR(l_empty, par), lane == 0);
         }
     }
     tc_fence_before();
@@ -903,6 +1058,7 @@ __global__ void __block_size__((kThreads, 1, 1)) __maxnreg__(128) paged_attn8_ke
         tc_fence_after();
         tmem_dealloc(tmem, L::kCols);
     }
+#undef BAR
 }
 
 spec_status bad8(const char* what) {
@@ -936,7 +1092,7 @@ cudaError_t run8(Paged8Params& p, int ctas, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<HD, RP>::kBytes);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
-    if ((e = launch(fn, dim3((unsigned)ctas), kThreads, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess || p.whole) return e;
+    if ((e = launch(fn, dim3((unsigned)ctas), 32 * Plan<HD, RP>::kWarps, Plan<HD, RP>::kBytes, s, args)) != cudaSuccess || p.whole) return e;
     int rp = RP;
     void* jargs[] = {static_cast<PagedCommon*>(&p), &rp};
     return launch((const void*)paged_join_kernel<HD>, dim3((unsigned)ctas, 2 * (RP <= 16 ? 1 : RP / 16)), 32 * kJoinWarps, 0, s, jargs);
@@ -963,7 +1119,7 @@ spec_status spec_paged_attention_fp8_workspace(int32_t n_heads, int32_t n_kv_hea
         set_last_error("spec_paged_attention_fp8_workspace: no current CUDA device");
         return SPEC_ERR_CUDA;
     }
-    *out_bytes = Work(sms, split::tile_rows(n_heads / n_kv_heads, max_new), head_dim).bytes;
+    *out_bytes = Work(sms, split8::tile_height(n_heads / n_kv_heads, max_new), head_dim).bytes;
     return SPEC_OK;
 }
 
@@ -993,10 +1149,10 @@ spec_status spec_paged_attention_fp8(const void* d_q, int64_t q_stride, const in
     if (misaligned(d_row_start, 4) || misaligned(d_len, 4) || misaligned(d_tables, 4) || misaligned(d_error_opt, 4))
         return bad8("an int32 pointer is not 4-byte aligned");
     if (misaligned(d_work, 256)) return bad8("d_work is not 256-byte aligned");
-    const int group = n_heads / n_kv_heads, rp = split::tile_rows(group, max_new), tokens = rp / group;
+    const int group = n_heads / n_kv_heads, rp = split8::tile_height(group, max_new), tile = split8::tile_rows(rp, group);
     // every unit has to fit int32, whatever the lengths on the device
-    const int64_t pairs = ((int64_t)nseq + rows / tokens) * n_kv_heads;
-    if (pairs > 0x7fffffffll / ((table_pages + 1) / 2))
+    const int64_t pairs = ((int64_t)nseq + (int64_t)rows * group / tile) * n_kv_heads;
+    if (pairs > 0x7fffffffll / ((table_pages + 1) / 2 + split8::kHead))
         return bad8("too much work for one call ((nseq + rows / tile) * n_kv_heads * table_pages / 2)");
     if (!whole && work_bytes < Work(1, rp, head_dim).bytes) return bad8("work_bytes is less than these heads need");
     const int sms = current_sms();
@@ -1028,7 +1184,8 @@ spec_status spec_paged_attention_fp8(const void* d_q, int64_t q_stride, const in
     p.rows = rows;
     p.hkv = n_kv_heads;
     p.group = group;
-    p.tokens = tokens;
+    p.tokens = 0;
+    p.tile = tile;
     p.whole = whole;
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.num_pages = num_pages;
@@ -1042,11 +1199,9 @@ spec_status spec_paged_attention_fp8(const void* d_q, int64_t q_stride, const in
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     cudaError_t e;
     if (head_dim == 128)
-        e = rp == 16 ? run8<128, 16>(p, sms, s) : rp == 32 ? run8<128, 32>(p, sms, s) : rp == 64 ? run8<128, 64>(p, sms, s)
-                                                                                            : run8<128, 128>(p, sms, s);
+        e = rp == 16 ? run8<128, 16>(p, sms, s) : rp == 32 ? run8<128, 32>(p, sms, s) : run8<128, 64>(p, sms, s);
     else
-        e = rp == 16 ? run8<64, 16>(p, sms, s) : rp == 32 ? run8<64, 32>(p, sms, s) : rp == 64 ? run8<64, 64>(p, sms, s)
-                                                                                          : run8<64, 128>(p, sms, s);
+        e = rp == 16 ? run8<64, 16>(p, sms, s) : rp == 32 ? run8<64, 32>(p, sms, s) : run8<64, 64>(p, sms, s);
     return e == cudaSuccess ? SPEC_OK : failed(e);
 }
 

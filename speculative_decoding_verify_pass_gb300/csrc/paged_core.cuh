@@ -9,25 +9,16 @@
 #include <math.h>
 
 #include "internal.h"
-#include "paged_plan.h"
 #include "paged_split.h"
 #include "spec.h"
 
 namespace sv {
 namespace {
 
-using plan::kFewSeqs;
-using plan::kSegs;
-using plan::kWarps;
-using plan::Seg;
 using split::kChunk;
 
-constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
-constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference
 constexpr float kNone = -FLT_MAX;       // reference of a row that has seen no key: no score lies below it
-constexpr int kSoftBar = 1, kResultBar = 3; // named barriers: one per softmax warpgroup, the results' warpgroup
 
 // A split pair, as the join kernel sees it from one of its CTAs.
 struct Meta {
@@ -38,7 +29,7 @@ struct Meta {
     int head;                   // first query head
     int row0;                   // first row of the call
     int last0;                  // last visible position of the first token
-    int pad;
+    int skip;                   // query heads of the first token in front of the first row
 };
 
 // What a call is about, apart from the tensor maps of its operands.
@@ -204,86 +195,12 @@ struct Ring {
     }
 };
 
-// A CTA's segments in order.
-struct Walk {
-    const PagedCommon& p;
-    const int* first;           // [nseq + 1] in shared memory
-    const int *start, *lens;    // row starts and lengths: in shared memory when they are few
-    int u, end;                 // next unit, end of the CTA's range
-    int q = 0, q1 = 0;          // sequence, the end of its units
-    int rows = 0, len = 0, row_base = 0, chunks = 1;
-    // the segment
-    int head = 0, block = 0, c0 = 0, c1 = 0, R = 0, seg = -1;
-
-    __device__ Walk(const PagedCommon& pp, const int* f, const int* s, const int* n, int begin, int e)
-        : p(pp), first(f), start(s), lens(n), u(begin), end(e) {}
-    __device__ __forceinline__ void sequence() {
-        q1 = first[q + 1];
-        row_base = start[q];
-        rows = start[q + 1] - row_base;
-        len = lens[q];
-        chunks = split::chunks_of(len);
-    }
-    __device__ __forceinline__ bool next() {
-        if (u >= end) return false;
-        if (seg < 0) {                          // where the range begins
-            q = split::sequence_of(first, p.nseq, u);
-            sequence();
-            const int at = u - first[q], pair = at / chunks;
-            block = pair / p.hkv;
-            head = pair - block * p.hkv;
-            c0 = at - pair * chunks;
-            if (p.whole && c0 > 0) {            // this pair begins in another CTA's range, which takes it
-                u += chunks - c0;
-                if (u >= end) return false;
-                step();
-            }
-        } else {
-            step();
-        }
-        c1 = p.whole ? chunks : min(chunks, c0 + end - u);
-        R = min(p.tokens, rows - block * p.tokens) * p.group;
-        u += c1 - c0;
-        ++seg;
-        return true;
-    }
-    // the pair after the current one
-    __device__ __forceinline__ void step() {
-        c0 = 0;
-        if (u >= q1) {
-            do ++q;
-            while (first[q + 1] <= u);          // sequences without units
-            sequence();
-            block = head = 0;
-        } else if (++head == p.hkv) {
-            head = 0;
-            ++block;
-        }
-    }
-    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
-    // last position that the block's first token sees
-    __device__ __forceinline__ int last0() const { return len - rows + block * p.tokens; }
-    // the segment's pair, for the join
-    __device__ Meta meta(const split::Deal& deal) const {
-        const int pair_begin = u - c1, owner = deal.cta(pair_begin);
-        Meta m;
-        m.count = deal.parts(owner, pair_begin + chunks);
-        m.owner = owner;
-        m.slot = 2 * owner + (pair_begin == deal.begin(owner) ? 0 : 1);
-        m.rows = R;
-        m.head = head * p.group;
-        m.row0 = row_base + block * p.tokens;
-        m.last0 = last0();
-        m.pad = 0;
-        return m;
-    }
-};
-
 // The pages of a segment's chunks, looked up 32 chunks at a time, one a lane.
 struct PageWalk {
     int y0 = -1, y1 = -1;       // the lane's chunk: tensor-map rows of its two pages
     int z0 = -1, z1 = -1;       // the current chunk's (a bad page's -1 lies outside the pool and reads as zeros)
     int count = 0;              // and how many of them exist
+    template <class Seg>
     __device__ __forceinline__ void at(const PagedCommon& p, const Seg& s, int k, int lane) {
         const int held = (s.len + SPEC_PAGE - 1) / SPEC_PAGE, c = s.c0 + k;
         if ((k & 31) == 0) {
@@ -328,9 +245,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
         // partial t of the pair: the owner's slot, then the first slots of the CTAs after it
         auto at = [&](int r, int t) { return (size_t)(t ? 2 * (m.owner + t) : m.slot) * rp + r; };
         auto store = [&](int r, const float* o, float sum) {
-            const int t = r / p.group;
+            const int t = (m.skip + r) / p.group;
             const bool any = m.last0 + t >= 0;
-            uint16_t* out = p.out + (long long)(m.row0 + t) * p.out_stride + (long long)(m.head + r - t * p.group) * HD + lane * V;
+            uint16_t* out = p.out + (long long)(m.row0 + t) * p.out_stride + (long long)(m.head + m.skip + r - t * p.group) * HD + lane * V;
             const float inv = any ? 1.f / sum : 0.f;
             if constexpr (V == 4)
                 *reinterpret_cast<uint2*>(out) = any ? make_uint2(cvt_bf16x2(o[0] * inv, o[1] * inv), cvt_bf16x2(o[2] * inv, o[3] * inv))

@@ -5,31 +5,53 @@
 
 #include <stdint.h>
 
-#include "paged_plan.h"
+#include "paged_split8.h"
 
 namespace sv {
 namespace plan8 {
 
-using plan::kFewSeqs;
-using plan::kSegs;
-using plan::kSmem;
-using plan::kWarps;
-using plan::Pair;
-using plan::Seg;
-using split::kChunk;
+using split8::kChunk;
 
+constexpr int kSmem = 227 * 1024;           // of a CTA
 constexpr int kSlots = 8;                   // at most, of K and of V
 constexpr int kScaleSlots = 8;              // chunks whose scales are loaded ahead
 constexpr int kParts = 3;                   // parts of a weight
+constexpr int kSegs = 4;                    // segments listed ahead
+constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
 
-// Tile height of a plan: which warpgroups work how, and how many buffers they take.
+// Limits of one wait (2^31 cycles each) that the results of a segment are waited for:
+// the other waits last a few chunks at most, this one all of them, up to 2^19.
+constexpr int wait_rounds(int units) { return 1 + (units >> 15); }
+
+// A segment, as the roles need it.
+struct alignas(16) Seg {
+    int c0, units;              // first chunk, number of chunks (0: the list ends)
+    int R;                      // rows
+    int last0;                  // last position that the first row's token sees
+    int len;                    // of the sequence
+    int q, head;                // sequence, kv head
+    int row0;                   // the first row's row of the call
+    int skip;                   // query heads of that row in front of the first row
+    int slot;                   // where its partial goes; -1: it covers its pair
+    int pad[2];
+};
+
+struct alignas(8) Pair {
+    float x, y;
+};
+
+// Tile height of a plan: how the softmax warpgroups share the work.  A thread handles
+// one key and NC rows.
 template <int RP>
 struct Rows {
-    static constexpr bool kStream = RP <= 64;               // warpgroups take alternate chunks
-    static constexpr bool kStack = RP <= 32;                // P^T's parts in one product
-    static constexpr int NQ = RP <= 64 ? 2 : 1;             // query tiles
-    static constexpr int NP = kStream ? 2 : 1;              // P^T's
+    static constexpr int NC = 16;                           // rows of a thread
+    static constexpr int kSoftGroups = RP <= 16 ? 2 : 4;    // softmax warpgroups
+    static constexpr int kTeam = RP / NC;                   // warpgroups of a chunk
+    static constexpr bool kStream = kTeam < kSoftGroups;    // two teams take alternate chunks
     static constexpr int kGroups = kStream ? 2 : 1;         // O^T's (and references) of a segment
+    static constexpr int NS = RP <= 32 ? 4 : 2;             // S^T's: two ahead of each team, where tensor memory has room
+    static constexpr int kWarps = 4 * kSoftGroups + 8;
+    static_assert(kTeam * kGroups == kSoftGroups, "every warpgroup has its share");
 };
 
 // Everything but the tiles.
@@ -40,18 +62,19 @@ struct Fixed {
     alignas(16) Seg segs[kSegs];
     alignas(16) float nref[2][T::kGroups][RP];      // by segment parity: minus each row's reference
     alignas(16) float qmul[2][RP];                  // by segment parity: log2 units per unit of S^T
+    alignas(16) float shrink[T::kGroups][RP];       // while references move: what the old weights shrink by,
+    alignas(16) float oshrink[T::kGroups][RP];      // and O^T, in which the values' scales are too
     alignas(16) float xl[2][T::kGroups][4][RP];     // per lane quadrant: sums (and, while a reference moves, maxima)
-    alignas(16) int tok[RP];                        // token of each row
+    alignas(16) int tok[RP];                        // token of each row of a block that begins with a token
     Pair weight[2][RP];                             // what the two O^T's of a row are multiplied with
-    long long col_off[RP];                          // a row's offset in the output
-    long long warp_sum[kWarps];
-    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], c_full[kScaleSlots], c_empty[kScaleSlots],
-        q_full[T::NQ], q_empty[T::NQ], r_full[2], s_full[2], s_empty[2], p_full[T::NP], p_empty[T::NP], o_full[2], o_empty[2],
-        l_full[2], l_empty[2], seg_full[kSegs], seg_empty[kSegs], fin[2];
+    long long warp_sum[T::kWarps];
+    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], c_full[kScaleSlots], c_empty[kScaleSlots], q_full[2],
+        q_empty[2], r_full[2], s_full[T::NS], s_empty[T::NS], p_full[2], p_empty[2], o_full[2], o_empty[2], l_full[2], l_empty[2],
+        seg_full[kSegs], seg_empty[kSegs], fin[2];
     int first[split::kMaxSeqs + 1];
     int few_start[kFewSeqs + 1], few_len[kFewSeqs]; // a batch this small is not read from memory twice
-    int vtop[2][4];                                 // by softmax warpgroup and quadrant: largest value scale of a chunk
-    int vref[2][2];                                 // by segment parity and softmax warpgroup: the value scale that its weights are in
+    int vtop[T::kSoftGroups][4];                       // by softmax warpgroup and quadrant: largest value scale of a chunk
+    int vref[2][T::kSoftGroups];                       // by segment parity and softmax warpgroup: the value scale that its weights are in
     int poison[2];                                  // 1 + the last segment (by parity) that silenced a value
     uint32_t tmem_base;
     int dead, total;
@@ -65,17 +88,20 @@ struct Plan : Rows<RP> {
     static constexpr int kQ = 2 * kQPart;
     static constexpr int kP = kChunk * RP;                  // one part of P^T
     static constexpr int kPad = 1024;                       // an M = 128 product over 64 dimensions reads past its slot
-    static constexpr int kOther = T::NQ * kQ + T::NP * kParts * kP + 1024 + kPad;   // 1024: alignment
+    static constexpr int kOther = 2 * kQ + 2 * kParts * kP + 1024 + kPad;   // two query tiles, two P^T's; 1024: alignment
     static constexpr int kMost = kSmem - (int)sizeof(Fixed<RP>) - kOther;
     static constexpr int kFit = kMost / kSlot / 2;
     static constexpr int NK = kFit < kSlots ? kFit : kSlots, NV = NK;
     static constexpr int kBytes = kOther + (NK + NV) * kSlot;
-    static constexpr int kO = T::kStack ? kParts * RP : RP; // tensor-memory columns of one O^T
-    static constexpr int kUsed = 2 * RP + 2 * T::kGroups * kO;      // S^T x 2, O^T x 2 (per warpgroup)
+    static constexpr int kO = kParts * RP;                  // tensor-memory columns of one O^T: its parts side by side
+    static constexpr int kUsed = T::NS * RP + 2 * T::kGroups * kO;  // S^T's, O^T x 2 (per team)
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
-    // registers of a thread, by role: 128 each at launch, moved to where S^T and P^T live
-    static constexpr int kSoftRegs = RP <= 32 ? 160 : 184, kIssueRegs = 64, kResultRegs = RP <= 32 ? 128 : 80;
-    static_assert(2 * kSoftRegs + kIssueRegs + kResultRegs <= 4 * 128, "more registers than the block was launched with");
+    // registers of a thread, by role: the same for all at launch, moved to where S^T and P^T live
+    static constexpr int kLaunchRegs = T::kSoftGroups == 2 ? 128 : 80, kSoftRegs = T::kSoftGroups == 2 ? 160 : 88, kIssueRegs = 56,
+                         kResultRegs = T::kSoftGroups == 2 ? 112 : 72;
+    static_assert(T::kSoftGroups * kSoftRegs + kIssueRegs + kResultRegs <= (T::kSoftGroups + 2) * kLaunchRegs,
+                  "more registers than the block was launched with");
+    static_assert(T::kWarps * 32 * kLaunchRegs <= 65536, "more registers than an SM has");
     static_assert(NK >= 2 && kUsed <= 512, "a K and a V beyond those in use");
     static_assert(kBytes + (int)sizeof(Fixed<RP>) <= kSmem, "more shared memory than a CTA has");
 };

@@ -3,21 +3,24 @@ and attention against 64 bits.
 
 Attention's tolerance, per output: half a bf16 step of the value (2^-8 |o|), plus
 
- - E * sum_i w_i |v_i|.  The weights enter the second product as three e5m2 parts, each
-   the rounding to 3 significant bits of what is left (2^-3 of it): off by 2^-9; exp2's
-   own error (2^-22); the sums of n terms in 32 bits (n * 2^-24 each, weights and
-   values); and scores off by d, which move each weight and the sum by at most e^d - 1
-   < 2 d each: a dot product of hd products summed in fp32, for each of the two e4m3
-   parts of q (2 hd * 2^-24 * scale * sum |q||k|), roundings of the scaled score (2^-22
-   |s|: the query row's and the key's powers of two are exact, scale * log2 e, the
-   product and the difference round), and what the two parts leave of q: nothing of an
-   element within 2^-8 of the row's largest (8 significant bits are two e4m3's), else
-   half of e4m3's smallest step, 2^-10, where the largest is at least 2^7: 2^-17 of it.
+ - E * sum_i w_i |v_i|.  The weights enter the second product as a half (off by 2^-11)
+   in three e5m2 parts of 3 significant bits: the first is cut (it leaves less than 2^-2
+   of the weight's power of two), the second rounded (2^-6), the third rounded (2^-10):
+   off by less than 2^-9; exp2's own error (2^-22); the sums of n terms in 32 bits
+   (n * 2^-24 each, weights and values); and scores off by d, which move each weight and
+   the sum by at most e^d - 1 < 2 d each: a dot product of hd products summed in fp32, for
+   each of the two e4m3 parts of q (2 hd * 2^-24 * scale * sum |q||k|), roundings of the
+   scaled score (2^-22 |s|: the query row's and the key's powers of two are exact, scale *
+   log2 e, the product and the difference round), and what the two parts leave of q:
+   nothing of an element within 2^-8 of the row's largest (8 significant bits are two
+   e4m3's), else half of e4m3's smallest step, 2^-10, where the largest is at least 2^7:
+   2^-17 of it.
    E = 2^-9 + 2^-21 + 4 d + 2 n 2^-24.
  - F * vmax, vmax the largest |v| of the sequence: a weight is kept relative to the
-   largest that is known, times 2^8 at least, and a part smaller than half of e5m2's
-   smallest number, 2^-17, is lost: n * 2^-25, times 2, since values are at most twice
-   their row's largest after scaling by a power of two, and 2 for the sum that divides:
+   largest that is known, times 2^3 at least, and its third part times 4 * 8 more; what
+   is smaller than half of e5m2's smallest number, 2^-17, is lost, 2^-25 of the weight:
+   n * 2^-25, times 2, since values are at most twice their row's largest after scaling
+   by a power of two, and 2 for the sum that divides:
    F = n * 2^-23."""
 import random
 
@@ -535,6 +538,25 @@ def test_attention_same_call_same_bits():
     a = c.run().view(torch.int16)
     for _ in range(5):
         assert torch.equal(a, c.run().view(torch.int16))
+
+
+@pytest.mark.parametrize("heads,new", [((12, 2, 64), 8), ((32, 4, 128), 8), ((8, 2, 128), 8)])
+def test_attention_of_ragged_blocks_in_many_calls(heads, new):
+    """Short sequences whose blocks leave some of the softmax's warpgroups without rows, segment
+    by segment: no wait gives up, and every call gives the same bits."""
+    torch = torch_cuda()
+    rng = random.Random(19)
+    lens = [rng.randint(8, 400) for _ in range(120)]
+    c = Case8(lens, [rng.randint(1, new) for _ in lens], *heads, seed=20)
+    err, outs = i32([0]), [torch.empty_like(c.d["q"]) for _ in range(2)]
+    first = c.run(max_new=new, d_error=err)
+    c.check(first)
+    for _ in range(40):
+        for k in range(100):
+            c.run(max_new=new, d_error=err, d_out=outs[k & 1])
+        assert err.item() == 0
+        live = c.start[-1]
+        assert all(torch.equal(o[:live].view(torch.int16), first[:live].view(torch.int16)) for o in outs)
 
 
 def test_refusals_of_the_binding():
