@@ -121,7 +121,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         tmp = BINDING + ".tmp%d" % os.getpid()
         torch_lib = os.path.join(torch_dir, "lib")
         link = ["g++", "-shared", "-o", tmp, bobj, "-L" + HERE, "-l:libspecverify.so", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
-                "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+                "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
         r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))

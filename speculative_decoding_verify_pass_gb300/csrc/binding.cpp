@@ -9,6 +9,7 @@
 //
 // Every function returns what the C ABI returned, or -1 for arguments that the
 // kernels could not read; the Python side then says which and why.
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -30,6 +31,11 @@ const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariab
 
 bool on(const at::Tensor& t, int dev, at::ScalarType type) {
     return t.is_cuda() && t.get_device() == dev && t.scalar_type() == type;
+}
+
+// A new tensor, straight from the allocator (0.4 us sooner than by way of at::empty).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev) {
+    return at::Tensor(at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
 }
 
 // A contiguous int32 tensor of at least `need` entries.
@@ -224,8 +230,8 @@ PyObject* paged_read_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (a[1] != Py_None && !int32(count, dev, 1)) || (a[7] != Py_None && !int32(err, dev, 1)))
         return status(kBadArgs);
     at::Tensor nk, nv;
-    if (!k) nk = at::empty({m, hkv, hd}, kp->options().dtype(at::kBFloat16));
-    if (!v) nv = at::empty({m, hkv, hd}, kp->options().dtype(at::kBFloat16));
+    if (!k) nk = fresh({m, hkv, hd}, at::kBFloat16, dev);
+    if (!v) nv = fresh({m, hkv, hd}, at::kBFloat16, dev);
     const spec_status st = spec_paged_read_fp8(i32(slots), count ? i32(count) : nullptr, (int32_t)m, (int32_t)hkv, (int32_t)hd,
                                                kp->data_ptr(), vp->data_ptr(), sc->data_ptr(), (int32_t)kp->size(0),
                                                (k ? *k : nk).data_ptr(), ks, (v ? *v : nv).data_ptr(), vs,
@@ -273,7 +279,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double gain = PyFloat_AsDouble(a[7]);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor result;
-    if (!out) result = at::empty({m, heads, hd}, x->options());
+    if (!out) result = fresh({m, heads, hd}, type, dev);
     const spec_status st = spec_rope(x->data_ptr(), xs, out ? out->data_ptr() : result.data_ptr(), os, kind, (int32_t)m, (int32_t)heads,
                                      (int32_t)hd, (int32_t)(2 * turns->numel()), interleaved, inverse, (float)gain,
                                      static_cast<const uint64_t*>(turns->data_ptr()), start ? i32(start) : nullptr,

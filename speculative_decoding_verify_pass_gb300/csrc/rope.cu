@@ -8,10 +8,13 @@
 // position; its upper 32 bits, as a signed fraction, go to sincospi.  (In fp32 the
 // angle of position 500000 would be off by 2^-6.)
 //
-// Memory bounds it: x once in, once out.  A CTA takes a few rows: its warps find the
-// rows' positions, its threads fill a table of cos and sin in shared memory that
-// all heads of the row share, then every thread turns 8 pairs (two 16-byte loads)
-// at a time.
+// Memory bounds it: x once in, once out.  A warp takes a row: it loads its first heads,
+// finds the row's position, fills a table of cos and sin in shared memory, and then goes
+// over the heads, a lane's pairs the same in each, so that their cos and sin stay in
+// registers.  16001 rows of 40 heads of 128, 64 of them rotated, take 51.7 us (328 MB: 6.3
+// TB/s); a CTA of 8 rows with one table that every piece looked up took 62.2.  2 heads
+// in flight a lane: 1 took 57.5, 4 (and their registers) 61.1.  Few rows (at most 4 per
+// SM) have 8 warps each, which all find the position and fill a table: 2.5 us for 8 rows.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -21,8 +24,8 @@
 namespace sv {
 namespace {
 
-constexpr int kThreads = 256, kMostRows = 8;    // rows of a CTA: at most one a warp
-static_assert(kMostRows <= kThreads / 32, "one warp a row");
+constexpr int kWarps = 8;       // of a CTA
+constexpr int kBatch = 2;       // heads that a lane has in flight
 
 struct RopeParams {
     const void* x;
@@ -31,7 +34,7 @@ struct RopeParams {
     const unsigned long long* turns;
     const int *row_start, *len, *pos;
     int nseq, rows, heads, hd, pairs;           // pairs: r/2
-    int per_cta;                                // rows of a CTA
+    int split;                                  // 2^split warps share a row
     float gain;
     int inverse, copy;                          // copy: elements behind the rotated part go to another buffer
 };
@@ -73,94 +76,111 @@ __device__ __forceinline__ int sequence(const int* start, int nseq, int r, int l
     return start[lo] <= r && r < *end ? lo : -1;
 }
 
+// What a lane takes at a time: VEC pairs of kBatch heads, as one piece (INTER) or two.
 template <class T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    extern __shared__ float2 turn[];            // [rows of the CTA][pairs] cos, sin
-    __shared__ long long where[kMostRows];      // position of each row
-    __shared__ int live[kMostRows];
+struct Batch {
+    static constexpr int N = INTER ? 2 * VEC : VEC, kPieces = INTER ? 1 : 2;
+    Piece<T, N> a[kBatch][kPieces];
+    __device__ __forceinline__ void load(const T* x, const RopeParams& p, int h, int step, int j) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (h + u * step < p.heads)
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k)
+                    a[u][k] = *reinterpret_cast<const Piece<T, N>*>(x + (h + u * step) * p.hd + (INTER ? 2 * j : j + k * p.pairs));
+    }
+    __device__ __forceinline__ void turn_store(T* out, const RopeParams& p, int h, int step, int j, const float2* cs) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (h + u * step >= p.heads) continue;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                T &v = a[u][0].v[INTER ? 2 * e : e], &w = a[u][kPieces - 1].v[INTER ? 2 * e + 1 : e];
+                const float m = up(v), n = up(w);
+                v = down<T>(m * cs[e].x - n * cs[e].y);
+                w = down<T>(n * cs[e].x + m * cs[e].y);
+            }
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                *reinterpret_cast<Piece<T, N>*>(out + (h + u * step) * p.hd + (INTER ? 2 * j : j + k * p.pairs)) = a[u][k];
+        }
+    }
+};
+
+template <class T, int VEC, bool INTER>
+__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const __grid_constant__ RopeParams p) {
+    extern __shared__ float2 tables[];          // [warps][pairs] cos, sin
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r0 = blockIdx.x * p.per_cta, count = min(p.per_cta, p.rows - r0);
+    const int r = (int)(((long long)blockIdx.x * kWarps + warp) >> p.split), part = warp & ((1 << p.split) - 1);
+    // lanes: pieces of VEC pairs, over as many heads as there are lanes for
+    const int pieces = p.pairs / VEC, across = min(pieces, 32), heads = 32 / across;
+    const int j0 = lane % across * VEC, step = heads << p.split;
+    const int h0 = lane / across < heads ? part * heads + lane / across : p.heads;
     pdl_wait();
     pdl_launch_dependents();
-    if (warp < count) {
-        const int r = r0 + warp;
-        long long t = 0;
-        int in = 1;
-        if (p.pos) {
-            t = p.pos[r];
-        } else {
-            int end;
-            const int q = sequence(p.row_start, p.nseq, r, lane, &end);
-            in = q >= 0;
-            if (in) t = (long long)p.len[q] - (end - r);
-        }
-        if (lane == 0) {
-            where[warp] = t;
-            live[warp] = in;
-        }
+    if (r >= p.rows) return;
+    const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
+    T* out = static_cast<T*>(p.out) + r * p.out_stride;
+    Batch<T, VEC, INTER> batch;
+    batch.load(x, p, h0, step, j0);         // (also of a row that is no sequence's)
+    long long t = 0;
+    if (p.pos) {
+        t = p.pos[r];
+    } else {
+        int end;
+        const int q = sequence(p.row_start, p.nseq, r, lane, &end);
+        if (q < 0) return;
+        t = (long long)p.len[q] - (end - r);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < count * p.pairs; i += kThreads) {
-        const int k = i / p.pairs, j = i - k * p.pairs;
-        const unsigned long long phase = (unsigned long long)where[k] * p.turns[j];
+    float2* turn = tables + warp * p.pairs;
+    for (int j = lane; j < p.pairs; j += 32) {
+        const unsigned long long phase = (unsigned long long)t * p.turns[j];
         float s, c;
         sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s, &c);
-        turn[i] = make_float2(c * p.gain, (p.inverse ? -s : s) * p.gain);
+        turn[j] = make_float2(c * p.gain, (p.inverse ? -s : s) * p.gain);
     }
-    __syncthreads();
-
-    const int per_head = p.pairs / VEC, per_row = p.heads * per_head;
-    for (int i = threadIdx.x; i < count * per_row; i += kThreads) {
-        const int k = i / per_row, u = i - k * per_row, h = u / per_head, j = (u - h * per_head) * VEC;
-        if (!live[k]) continue;
-        const T* x = static_cast<const T*>(p.x) + (r0 + k) * p.x_stride + (long long)h * p.hd;
-        T* out = static_cast<T*>(p.out) + (r0 + k) * p.out_stride + (long long)h * p.hd;
-        const float2* cs = turn + k * p.pairs + j;
-        if constexpr (INTER) {
-            Piece<T, 2 * VEC> a = *reinterpret_cast<const Piece<T, 2 * VEC>*>(x + 2 * j);
+    __syncwarp();
+#pragma unroll 1
+    for (int j = j0; j < p.pairs; j += 32 * VEC) {
+        float2 cs[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float2 f = cs[e];
-                const float m = up(a.v[2 * e]), n = up(a.v[2 * e + 1]);
-                a.v[2 * e] = down<T>(m * f.x - n * f.y);
-                a.v[2 * e + 1] = down<T>(n * f.x + m * f.y);
-            }
-            *reinterpret_cast<Piece<T, 2 * VEC>*>(out + 2 * j) = a;
-        } else {
-            Piece<T, VEC> a = *reinterpret_cast<const Piece<T, VEC>*>(x + j);
-            Piece<T, VEC> b = *reinterpret_cast<const Piece<T, VEC>*>(x + p.pairs + j);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float2 f = cs[e];
-                const float m = up(a.v[e]), n = up(b.v[e]);
-                a.v[e] = down<T>(m * f.x - n * f.y);
-                b.v[e] = down<T>(n * f.x + m * f.y);
-            }
-            *reinterpret_cast<Piece<T, VEC>*>(out + j) = a;
-            *reinterpret_cast<Piece<T, VEC>*>(out + p.pairs + j) = b;
+        for (int e = 0; e < VEC; ++e) cs[e] = turn[j + e];
+#pragma unroll 1
+        for (int h = h0; h < p.heads; h += kBatch * step) {
+            if (j != j0 || h != h0) batch.load(x, p, h, step, j);
+            batch.turn_store(out, p, h, step, j, cs);
         }
     }
-    if (p.copy) {
-        constexpr int PV = VEC >= 4 ? 16 / sizeof(T) : 1;   // r is then a multiple of 8
-        const int rest = (p.hd - 2 * p.pairs) / PV, rest_row = p.heads * rest;
-        for (int i = threadIdx.x; i < count * rest_row; i += kThreads) {
-            const int k = i / rest_row, u = i - k * rest_row, h = u / rest, j = 2 * p.pairs + (u - h * rest) * PV;
-            if (!live[k]) continue;
-            const long long from = (r0 + k) * p.x_stride + (long long)h * p.hd + j;
-            const long long to = (r0 + k) * p.out_stride + (long long)h * p.hd + j;
-            *reinterpret_cast<Piece<T, PV>*>(static_cast<T*>(p.out) + to) =
-                *reinterpret_cast<const Piece<T, PV>*>(static_cast<const T*>(p.x) + from);
+    if (p.copy) {                               // the elements behind the rotated ones
+        constexpr int N = 2 * VEC * sizeof(T) < 16 ? 2 * VEC : 16 / sizeof(T);   // rotary_dim is a multiple of 2 * VEC
+        const int rest = (p.hd - 2 * p.pairs) / N, beside = min(rest, 32), rows = 32 / beside, stride = rows << p.split;
+        if (lane / beside >= rows) return;
+        for (int j = lane % beside; j < rest; j += 32) {
+            const int at = 2 * p.pairs + j * N;
+#pragma unroll 1
+            for (int h = part * rows + lane / beside; h < p.heads; h += 2 * kBatch * stride) {
+                Piece<T, N> a[2 * kBatch];
+#pragma unroll
+                for (int u = 0; u < 2 * kBatch; ++u)
+                    if (h + u * stride < p.heads) a[u] = *reinterpret_cast<const Piece<T, N>*>(x + (h + u * stride) * p.hd + at);
+#pragma unroll
+                for (int u = 0; u < 2 * kBatch; ++u)
+                    if (h + u * stride < p.heads) *reinterpret_cast<Piece<T, N>*>(out + (h + u * stride) * p.hd + at) = a[u];
+            }
         }
     }
 }
 
+// Pairs a lane takes: 16 bytes' worth where the pairs allow it.
+template <class T, bool INTER>
+const void* variant(int pairs) {
+    constexpr int kMost = 16 / sizeof(T) / (INTER ? 2 : 1), kSome = kMost / 2;
+    return pairs % kMost == 0   ? (const void*)rope_kernel<T, kMost, INTER>
+           : pairs % kSome == 0 ? (const void*)rope_kernel<T, kSome, INTER>
+                                : (const void*)rope_kernel<T, 1, INTER>;
+}
 template <class T>
-const void* variant(int pairs, bool inter) {
-    constexpr int kMost = sizeof(T) == 4 ? 4 : 8;
-    if (pairs % kMost == 0) return inter ? (const void*)rope_kernel<T, kMost, true> : (const void*)rope_kernel<T, kMost, false>;
-    if (pairs % 4 == 0) return inter ? (const void*)rope_kernel<T, 4, true> : (const void*)rope_kernel<T, 4, false>;
-    return inter ? (const void*)rope_kernel<T, 1, true> : (const void*)rope_kernel<T, 1, false>;
-}
+const void* variant(int pairs, bool inter) { return inter ? variant<T, true>(pairs) : variant<T, false>(pairs); }
 
 spec_status bad(const char* msg) {
     set_last_error(msg);
@@ -251,14 +271,14 @@ spec_status spec_rope(const void* d_x, int64_t x_stride, void* d_out, int64_t ou
     p.gain = gain;
     p.inverse = inverse != 0;
     p.copy = d_x != d_out && rotary_dim < head_dim;
-    p.per_cta = rows <= 4 * 152 ? 1 : kMostRows;
+    p.split = rows <= 4 * 152 ? 3 : 0;
     const void* fn = type == SPEC_BF16   ? variant<__nv_bfloat16>(p.pairs, interleaved != 0)
                      : type == SPEC_FP16 ? variant<__half>(p.pairs, interleaved != 0)
                                          : variant<float>(p.pairs, interleaved != 0);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + p.per_cta - 1) / p.per_cta));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)p.per_cta * p.pairs * sizeof(float2);    // at most 32 KB
+    cfg.gridDim = dim3((unsigned)((((int64_t)rows << p.split) + kWarps - 1) / kWarps));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = (size_t)kWarps * p.pairs * sizeof(float2);       // at most 32 KB
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
