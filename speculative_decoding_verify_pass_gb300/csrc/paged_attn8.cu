@@ -91,17 +91,16 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 // The lanes may leave it apart: they join (__syncwarp, a vote, a named barrier) before
 // one of them does what lets the barrier's next phase end.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* dead, int rounds = 1) {
-    if (try_wait(bar, parity)) return true;
     uint32_t t0 = cycles();
 #pragma unroll 1
-    while (!*dead) {
-        if (try_wait(bar, parity)) return true;
+    while (!try_wait(bar, parity)) {
+        if (*dead) return false;
         if (cycles() - t0 > 0x7fffffffu) {
             if (--rounds <= 0) *dead = 1;
             t0 = cycles();
         }
     }
-    return false;
+    return true;
 }
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -175,6 +174,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // Largest of the warp's values; a NaN counts only among NaN.
 __device__ __forceinline__ float warp_max(float x) {
     float r;
@@ -234,8 +238,9 @@ struct Walk {
     int q = 0, q1 = 0;          // sequence, the end of its units
     int rows = 0, len = 0, row_base = 0, chunks = 1;
     // the segment
-    int head = 0, block = 0, c0 = 0, c1 = 0, seg = -1;
+    int head = 0, c0 = 0, c1 = 0, seg = -1;
     int pair0 = 0;              // first unit of its pair
+    split8::Place at = {0, 0};  // where its block begins
 
     __device__ Walk(const Paged8Params& pp, const int* f, const int* s, const int* n, int begin, int e)
         : p(pp), first(f), start(s), lens(n), u(begin), end(e) {}
@@ -254,10 +259,10 @@ struct Walk {
             if (q1 == 0) {                          // where the range begins
                 q = split::sequence_of(first, p.nseq, u);
                 sequence();
-                const int span = chunks + split8::kHead, at = u - first[q], pair = at / span;
-                block = pair / p.hkv;
+                const unsigned span = chunks + split8::kHead, v = u - first[q], pair = v / span, block = pair / (unsigned)p.hkv;
                 head = pair - block * p.hkv;
-                u0 = at - pair * span;
+                u0 = v - pair * span;
+                at.at(block, p.group, p.tokens);
             } else {
                 step();
             }
@@ -279,35 +284,33 @@ struct Walk {
             do ++q;
             while (first[q + 1] <= u);              // sequences without units
             sequence();
-            block = head = 0;
+            at = {0, 0};
+            head = 0;
         } else if (++head == p.hkv) {
             head = 0;
-            ++block;
+            at.step(p.group, p.tokens);
         }
     }
     __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
     __device__ __forceinline__ Seg segment() const {
-        const long long row = (long long)block * p.tile;    // of the sequence's rows and query heads
-        const int t = (int)(row / p.group);
         Seg s = {};
         s.c0 = c0;
         s.units = c1 - c0;
-        s.R = (int)min((long long)p.tile, (long long)rows * p.group - row);
-        s.last0 = len - rows + t;
+        s.R = min(p.tile, min(rows - at.token, p.tile) * p.group - at.skip);
+        s.last0 = len - rows + at.token;
         s.len = len;
         s.q = q;
         s.head = head;
-        s.row0 = row_base + t;
-        s.skip = (int)(row - (long long)t * p.group);
+        s.row0 = row_base + at.token;
+        s.skip = at.skip;
         s.slot = whole() ? -1 : 2 * (int)blockIdx.x + (c0 > 0 ? 0 : 1);
         return s;
     }
     // the segment's pair, for the join
-    __device__ Meta meta(const split::Deal& deal) const {
-        const Seg s = segment();
+    __device__ __forceinline__ Meta meta(const split::Deal& deal, const Seg& s) const {
         Meta m;
-        m.count = split8::parts_of(deal, pair0, chunks);
         m.owner = split8::owner_of(deal, pair0);
+        m.count = split8::parts_of(deal, m.owner, pair0, chunks);
         m.slot = 2 * m.owner + 1;
         m.rows = s.R;
         m.head = head * p.group;
@@ -339,43 +342,45 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
     uint8_t* ps = qs + 2 * L::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        for (int i = 0; i < NK; ++i) {
-            mbar_init(&sh.k_full[i], 1);
-            mbar_init(&sh.k_empty[i], 1);
+    if (tid < 32) {                             // the lanes share the barriers
+        if (lane < NK) {
+            mbar_init(&sh.k_full[lane], 1);
+            mbar_init(&sh.k_empty[lane], 1);
         }
-        for (int i = 0; i < NV; ++i) {
-            mbar_init(&sh.v_full[i], 1);
-            mbar_init(&sh.v_empty[i], 1);
+        if (lane < NV) {
+            mbar_init(&sh.v_full[lane], 1);
+            mbar_init(&sh.v_empty[lane], 1);
         }
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_empty[i], kArrive);
+        if (lane < NS) {
+            mbar_init(&sh.s_full[lane], 1);
+            mbar_init(&sh.s_empty[lane], kArrive);
         }
-        for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(&sh.c_full[i], 1);
-            mbar_init(&sh.c_empty[i], kArrive);
+        if (lane < kScaleSlots) {
+            mbar_init(&sh.c_full[lane], 1);
+            mbar_init(&sh.c_empty[lane], kArrive);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.q_full[i], 4);
-            mbar_init(&sh.q_empty[i], 1);
-            mbar_init(&sh.r_full[i], 4);
-            mbar_init(&sh.o_full[i], 1);
-            mbar_init(&sh.o_empty[i], 4);
-            mbar_init(&sh.l_full[i], kSoftWarps);
-            mbar_init(&sh.l_empty[i], 4);
-            mbar_init(&sh.p_full[i], kArrive);
-            mbar_init(&sh.p_empty[i], 1);
-            mbar_init(&sh.fin[i], 1);
-            sh.poison[i] = 0;
+        if (lane < 2) {
+            mbar_init(&sh.q_full[lane], 4);
+            mbar_init(&sh.q_empty[lane], 1);
+            mbar_init(&sh.r_full[lane], 4);
+            mbar_init(&sh.o_full[lane], 1);
+            mbar_init(&sh.o_empty[lane], 4);
+            mbar_init(&sh.l_full[lane], kSoftWarps);
+            mbar_init(&sh.l_empty[lane], 4);
+            mbar_init(&sh.p_full[lane], kArrive);
+            mbar_init(&sh.p_empty[lane], 1);
+            mbar_init(&sh.fin[lane], 1);
+            sh.poison[lane] = 0;
         }
-        for (int i = 0; i < kSegs; ++i) {
-            mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], kReaders);
+        if (lane < kSegs) {
+            mbar_init(&sh.seg_full[lane], 1);
+            mbar_init(&sh.seg_empty[lane], kReaders);
         }
         fence_barrier_init();
-        sh.dead = 0;
-        sh.first[0] = 0;
+        if (lane == 0) {
+            sh.dead = 0;
+            sh.first[0] = 0;
+        }
     }
 #pragma unroll 1
     for (int i = tid; i < RP; i += kThreads) sh.tok[i] = i / p.group;
@@ -403,7 +408,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 if (bad_rows || bad_len) {
                     if (blockIdx.x == 0 && p.err) atomicCAS(p.err, 0, bad_rows ? SPEC_PAGED_BAD_ROWS : SPEC_PAGED_BAD_LENGTH);
                 } else {
-                    v[k] = split8::units_of(r1 - r0, n, p.group, p.tile, p.hkv);
+                    v[k] = split8::units_of(r1 - r0, n, p.group, p.tokens, p.hkv);
                 }
             }
             sum += v[k];
@@ -460,7 +465,8 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             // ---------------- the list of segments, K and scale copies, and what the join kernel has to do here ----------------
             const bool few = p.nseq <= kFewSeqs;
             Walk w(p, sh.first, few ? sh.few_start : p.row_start, few ? sh.few_len : p.len, begin, end);
-            Meta into = {}, from = {};
+            Meta* const meta = p.meta + 2 * blockIdx.x;     // of the pair that goes on here, and of the one that goes on behind
+            if (lane == 0 && !p.whole) meta[0] = meta[1] = {};
             Ring<NK> kr;
             Ring<kScaleSlots> cr;
             const uint32_t ka = kept(smem_u32(kslots));
@@ -469,7 +475,10 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             for (bool more = true; more && ok;) {
                 more = w.next();
                 Seg s = {};                     // no units: the list ends
-                if (more) s = w.segment();
+                if (more) {
+                    s = w.segment();
+                    if (lane == 0 && !p.whole && !w.whole()) meta[w.c0 == 0] = w.meta(deal, s);
+                }
                 ok = wait(BAR(seg_empty, sr.at), sr.round ^ 1, dead);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 if (lane == 0) {
@@ -509,12 +518,6 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     kr.step();
                     cr.step();
                 }
-                if (w.seg == 0 && w.c0 > 0) into = w.meta(deal);
-            }
-            if (lane == 0 && !p.whole) {
-                if (w.seg >= 0 && w.c0 == 0 && w.c1 > 0 && w.c1 < w.chunks) from = w.meta(deal);
-                p.meta[2 * blockIdx.x] = into;
-                p.meta[2 * blockIdx.x + 1] = from;
             }
             if (lane == 0 && *dead) {          // every buffer's last copy, as far as one was issued
 #pragma unroll 1
@@ -949,16 +952,17 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             qr.step();
         };
         int i = 0;                              // the segment's first unit
-        Seg next = take();
-        bool gone = bar_any(kResultBar, 128, *dead != 0);
-        if (!gone && next.units) split_queries(next, 0);
+        Seg next = {};
 #pragma unroll 1
-        for (int seg = 0; !gone && next.units; ++seg) {
+        for (int seg = -1;; ++seg) {
             const Seg w = next;
             next = take();
-            gone = bar_any(kResultBar, 128, *dead != 0);
-            if (gone) break;
+            if (bar_any(kResultBar, 128, *dead != 0)) break;
             if (next.units) split_queries(next, (seg + 1) & 1);
+            if (seg < 0) {
+                if (next.units == 0) break;
+                continue;
+            }
             const int par = seg & 1, last0 = w.last0;
             const int ga = kStream ? i & 1 : 0; // the team of the first unit; the other has none in a segment of one
             const bool two = kStream && w.units > 1, whole = w.slot < 0;
@@ -979,8 +983,9 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     la = la * fa + lb * fb;
                     ma = m;
                 }
-                if (whole) {
-                    const float inv = 1.f / la;
+                const int t = token(w, r);
+                if (whole) {                    // (a row without a position: zeros)
+                    const float inv = last0 + t < 0 ? 0.f : rcp_approx(la);
                     fa *= inv;
                     fb *= inv;
                 } else {
@@ -989,7 +994,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 // O^T is in units of 2^(r - 3), r the warpgroup's that formed the row's weights
                 fa = fa * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][ga * kTeam + r / NC]);
                 if (two) fb = fb * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][(ga ^ 1) * kTeam + r / NC]);
-                sh.weight[par][r] = {fa, fb};
+                sh.row[par][r] = {{fa, fb}, whole ? t * p.out_stride + (long long)(r - t * p.group) * HD : (long long)r * HD};
             }
             if (qd == 0) wait(BAR(o_full, par), (seg >> 1) & 1, dead);
             named_bar_sync(kResultBar, 128);
@@ -1000,24 +1005,20 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
 #pragma unroll 1
             for (int j0 = 0; j0 < w.R; j0 += 8) {
                 // 8 rows' O^T of the first team (its three parts), and of the other
-                float o[8], y[8];
-                auto ld = [&](int g, float* r) {
-                    const uint32_t at = lanes + NS * RP + (kStream ? par * 2 + g : par) * L::kO + j0;
-                    float u[8], v[8];
-                    tmem_ld8_async(at, r);
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll 1
+                for (int g = 0; g < (two ? 2 : 1); ++g) {
+                    const uint32_t at = lanes + NS * RP + (kStream ? par * 2 + (ga ^ g) : par) * L::kO + j0;
+                    float x[8], u[8], v[8];
+                    tmem_ld8_async(at, x);
                     tmem_ld8_async(at + RP, u);
                     tmem_ld8_async(at + 2 * RP, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] += (u[e] + v[e] * (1.f / kPart3)) * (1.f / kPart2);
-                };
-                ld(ga, o);
-                if (two) ld(ga ^ 1, y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const plan8::Pair f = sh.weight[par][j0 + e];
-                    o[e] *= f.x;
-                    if (two) o[e] += y[e] * f.y;
+                    for (int e = 0; e < 8; ++e)
+                        o[e] += (x[e] + (u[e] + v[e] * (1.f / kPart3)) * (1.f / kPart2)) * sh.row[par][j0 + e].f[g];
                 }
                 if (d < HD) {
                     if (bad)                    // of the positions that some row of the block sees and some does not
@@ -1031,24 +1032,20 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                                 for (int e = 0; e < 8; ++e)
                                     if (t <= last0 + token(w, j0 + e)) o[e] = __uint_as_float(0x7FC00000u);
                         }
-                    if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int t = token(w, j0 + e);
-                            if (j0 + e < w.R)       // (a row without a position: zeros)
-                                out[t * p.out_stride + (long long)(j0 + e - t * p.group) * HD] = last0 + t < 0 ? (uint16_t)0 : f2bf(o[e]);
+                    for (int e = 0; e < 8; ++e)
+                        if (j0 + e < w.R) {
+                            const long long at = sh.row[par][j0 + e].at;
+                            if (whole) out[at] = f2bf(o[e]);
+                            else part[at] = o[e];
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (j0 + e < w.R) part[(j0 + e) * HD] = o[e];
-                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
             arrive_if(BAR(o_empty, par), lane == 0);
             arrive_if(BAR(l_empty, par), lane == 0);
+            if (next.units == 0) break;
         }
     }
     tc_fence_before();
@@ -1184,7 +1181,7 @@ spec_status spec_paged_attention_fp8(const void* d_q, int64_t q_stride, const in
     p.rows = rows;
     p.hkv = n_kv_heads;
     p.group = group;
-    p.tokens = 0;
+    p.tokens = split8::tile_tokens(tile, group);
     p.tile = tile;
     p.whole = whole;
     p.scale_log2 = scale * 1.44269504088896340736f;

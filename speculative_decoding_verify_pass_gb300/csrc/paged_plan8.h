@@ -36,8 +36,9 @@ struct alignas(16) Seg {
     int pad[2];
 };
 
-struct alignas(8) Pair {
-    float x, y;
+struct alignas(16) Out {
+    float f[2];                 // what the row is multiplied with in each team's O^T
+    long long at;               // where the row goes, in elements behind the segment's first
 };
 
 // Tile height of a plan: how the softmax warpgroups share the work.  A thread handles
@@ -66,7 +67,7 @@ struct Fixed {
     alignas(16) float oshrink[T::kGroups][RP];      // and O^T, in which the values' scales are too
     alignas(16) float xl[2][T::kGroups][4][RP];     // per lane quadrant: sums (and, while a reference moves, maxima)
     alignas(16) int tok[RP];                        // token of each row of a block that begins with a token
-    Pair weight[2][RP];                             // what the two O^T's of a row are multiplied with
+    Out row[2][RP];                                 // by segment parity: for the results
     long long warp_sum[T::kWarps];
     uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], c_full[kScaleSlots], c_empty[kScaleSlots], q_full[2],
         q_empty[2], r_full[2], s_full[T::NS], s_empty[T::NS], p_full[2], p_empty[2], o_full[2], o_empty[2], l_full[2], l_empty[2],

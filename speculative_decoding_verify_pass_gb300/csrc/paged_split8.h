@@ -34,10 +34,35 @@ SPLIT_HD int tile_height(int group, int max_new) {
 }
 SPLIT_HD int tile_rows(int height, int group) { return group <= height ? height / group * group : height; }
 
-SPLIT_HD int blocks_of(int rows, int group, int tile) { return (int)(((int64_t)rows * group + tile - 1) / tile); }
-SPLIT_HD int64_t units_of(int rows, int len, int group, int tile, int hkv) {
-    return (int64_t)blocks_of(rows, group, tile) * hkv * (chunks_of(len) + kHead);
+// Whole tokens of a block; 0: a token's heads fill more than one (kMostRows at a time).
+SPLIT_HD int tile_tokens(int tile, int group) { return group <= tile ? tile / group : 0; }
+
+SPLIT_HD int blocks_of(int rows, int group, int tokens) {
+    if (tokens) return rows > 0 ? (int)((unsigned)(rows - 1) / (unsigned)tokens) + 1 : 0;
+    return (int)(((int64_t)rows * group + kMostRows - 1) / kMostRows);
 }
+SPLIT_HD int64_t units_of(int rows, int len, int group, int tokens, int hkv) {
+    return (int64_t)blocks_of(rows, group, tokens) * hkv * (chunks_of(len) + kHead);
+}
+
+// Where a block begins: a token, and a query head of it.
+struct Place {
+    int token, skip;
+    SPLIT_HD void at(int block, int group, int tokens) {
+        if (tokens) {
+            token = block * tokens;
+            skip = 0;
+        } else {                        // block * kMostRows / group, in 32 bits
+            const int whole = block / group, rest = (block - whole * group) * kMostRows;
+            token = whole * kMostRows + rest / group;
+            skip = rest % group;
+        }
+    }
+    SPLIT_HD void step(int group, int tokens) {     // to the next block
+        token += tokens;
+        if (!tokens && (skip += kMostRows) >= group) skip -= group, ++token;
+    }
+};
 
 // The part of a pair that units [u0, u1) of it (counted from its first one) cover.
 struct Part {
@@ -52,7 +77,7 @@ SPLIT_HD Part part_of(int u0, int u1) {
 // The CTA that holds the first chunk of a pair whose first unit is `begin`, and how
 // many CTAs work on it.
 SPLIT_HD int owner_of(const Deal& d, int begin) { return d.cta(begin + kHead); }
-SPLIT_HD int parts_of(const Deal& d, int begin, int chunks) { return d.parts(owner_of(d, begin), begin + kHead + chunks); }
+SPLIT_HD int parts_of(const Deal& d, int owner, int begin, int chunks) { return d.parts(owner, begin + kHead + chunks); }
 
 }  // namespace split8
 }  // namespace sv

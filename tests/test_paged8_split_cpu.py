@@ -16,13 +16,15 @@ using namespace sv::split8;
 extern "C" {
 int head() { return kHead; }
 int chunks(int len) { return chunks_of(len); }
-int blocks(int rows, int group, int tile) { return blocks_of(rows, group, tile); }
-long long units(int rows, int len, int group, int tile, int hkv) { return units_of(rows, len, group, tile, hkv); }
+int blocks(int rows, int group, int tile) { return blocks_of(rows, group, tile_tokens(tile, group)); }
+long long units(int rows, int len, int group, int tile, int hkv) { return units_of(rows, len, group, tile_tokens(tile, group), hkv); }
 int begin(int c, int total, int ctas) { return Deal(total, ctas).begin(c); }
 int c0(int u0, int u1) { return part_of(u0, u1).c0; }
 int c1(int u0, int u1) { return part_of(u0, u1).c1; }
 int owner(int total, int ctas, int begin) { return owner_of(Deal(total, ctas), begin); }
-int parts(int total, int ctas, int begin, int chunks) { return parts_of(Deal(total, ctas), begin, chunks); }
+int parts(int total, int ctas, int begin, int chunks) { Deal d(total, ctas); return parts_of(d, owner_of(d, begin), begin, chunks); }
+void place(int block, int group, int tile, int* out) { Place p; p.at(block, group, tile_tokens(tile, group)); out[0] = p.token; out[1] = p.skip; }
+void step(int group, int tile, int* out) { Place p = {out[0], out[1]}; p.step(group, tile_tokens(tile, group)); out[0] = p.token; out[1] = p.skip; }
 int height(int group, int max_new) { return tile_height(group, max_new); }
 int tile(int height, int group) { return tile_rows(height, group); }
 }
@@ -131,3 +133,17 @@ def test_tiles_and_blocks_cover_the_rows(split, group):
                     assert t == (int(skip + r >= group) if group > h else r // group)
                     seen.append((r0 // group + t, skip + r - t * group))
             assert seen == [(t, g) for t in range(rows) for g in range(group)]
+
+
+@pytest.mark.parametrize("group", [1, 3, 4, 16, 33, 63, 64, 65, 100, 127, 128])
+@pytest.mark.parametrize("hint", [1, 4, 1000])
+def test_blocks_begin_where_the_flattened_rows_say(split, group, hint):
+    tile = split.tile(split.height(group, hint), group)
+    at, walked = (ctypes.c_int * 2)(), (ctypes.c_int * 2)(0, 0)
+    for block in range(500):
+        split.place(block, group, tile, at)
+        assert tuple(at) == divmod(block * tile, group) == tuple(walked)
+        split.step(group, tile, walked)
+    for block in (10 ** 6, 2 ** 24 - 1, 2 ** 31 // max(1, tile // group) - 1):
+        split.place(block, group, tile, at)
+        assert tuple(at) == divmod(block * tile, group)
