@@ -85,18 +85,26 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
                  : "memory");
     return ok != 0;
 }
+// The word at `dead`, which a wait that gave up sets.
+__device__ __forceinline__ bool raised(uint32_t dead) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(dead) : "memory");
+    return v != 0;
+}
+__device__ __forceinline__ void raise(uint32_t dead) { asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(1u) : "memory"); }
 // Wait bounded in time (2^31 cycles, about a second, `rounds` of them): one that gives
 // up raises dead, and no wait lasts once that is raised.  For whole warps: a try by
 // part of a warp does not suspend it, and a spinning warp takes its neighbours' turns.
 // The lanes may leave it apart: they join (__syncwarp, a vote, a named barrier) before
-// one of them does what lets the barrier's next phase end.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* dead, int rounds = 1) {
+// one of them does what lets the barrier's next phase end, or the others could look after
+// that, and wait for a phase that is over.  (Joining in here costs 1 to 5 %.)
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t dead, int rounds = 1) {
     uint32_t t0 = cycles();
 #pragma unroll 1
     while (!try_wait(bar, parity)) {
-        if (*dead) return false;
+        if (raised(dead)) return false;
         if (cycles() - t0 > 0x7fffffffu) {
-            if (--rounds <= 0) *dead = 1;
+            if (--rounds <= 0) raise(dead);
             t0 = cycles();
         }
     }
@@ -446,7 +454,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
     using F = plan8::Fixed<RP>;
     const uint32_t shb = kept(smem_u32(&sh));
 #define BAR(x, i) (shb + (uint32_t)offsetof(F, x) + (uint32_t)(i) * 8u)
-    volatile int* const dead = &sh.dead;
+    const uint32_t dead = shb + (uint32_t)offsetof(F, dead);
     // token of row r of a block, counted from its first row's (which the block may begin in the middle of)
     auto token = [&](const Seg& s, int r) { return p.group > RP ? (int)(s.skip + r >= p.group) : sh.tok[r]; };
     Ring<kSegs> sr;                             // every role's place in the list of segments
@@ -519,7 +527,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     cr.step();
                 }
             }
-            if (lane == 0 && *dead) {          // every buffer's last copy, as far as one was issued
+            if (lane == 0 && raised(dead)) {          // every buffer's last copy, as far as one was issued
 #pragma unroll 1
                 for (int i = 0; i < NK; ++i) give_up(BAR(k_full, i), i < kr.at ? kr.round : kr.round ^ 1);
 #pragma unroll 1
@@ -533,7 +541,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
 #pragma unroll 1
             for (;;) {
                 const Seg s = take();
-                ok = __all_sync(0xffffffffu, !*dead);
+                ok = __all_sync(0xffffffffu, !raised(dead));
                 if (!ok || s.units == 0) break;
                 PageWalk pages;
 #pragma unroll 1
@@ -553,7 +561,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 }
                 if (!ok) break;
             }
-            if (lane == 0 && *dead) {
+            if (lane == 0 && raised(dead)) {
 #pragma unroll 1
                 for (int i = 0; i < NV; ++i) give_up(BAR(v_full, i), i < vr.at ? vr.round : vr.round ^ 1);
             }
@@ -567,7 +575,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
 #pragma unroll 1
             while (ok) {
                 const Seg s = take();
-                ok = __all_sync(0xffffffffu, !*dead);
+                ok = __all_sync(0xffffffffu, !raised(dead));
                 if (!ok || s.units == 0) break;
                 ok = wait(BAR(q_full, qr.at), qr.round, dead);
                 const uint32_t id = idesc8(128, (s.R + 15) & ~15, 0, 0);
@@ -597,7 +605,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 }
                 qr.step();
             }
-            if (*dead) {
+            if (raised(dead)) {
                 if (elect_one()) commit(BAR(fin, 0));
                 __syncwarp();
                 give_up(BAR(fin, 0), 0);
@@ -612,7 +620,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
 #pragma unroll 1
             for (int seg = 0; ok; ++seg) {
                 const Seg s = take();
-                ok = __all_sync(0xffffffffu, !*dead);
+                ok = __all_sync(0xffffffffu, !raised(dead));
                 if (!ok || s.units == 0) break;
                 ok = wait(BAR(o_empty, seg & 1), ((seg >> 1) & 1) ^ 1, dead);
                 // A = V^T and B = P^T, both MN-major
@@ -644,7 +652,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     pr.step();
                 }
             }
-            if (*dead) {
+            if (raised(dead)) {
                 if (elect_one()) commit(BAR(fin, 1));
                 __syncwarp();
                 give_up(BAR(fin, 1), 0);
@@ -662,11 +670,11 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
         const int bar = kSoftBar + wg;
         const uint32_t scales = kept(shb + (uint32_t)offsetof(F, scale) + (key >> 6) * 2 * SPEC_PAGE + (key & 63));
         const uint32_t weights = kept(smem_u32(ps) + (col0 >> 4) * (kChunk * 16) + key * 16);
-        int unit = 0;                           // the segment's first unit
+        uint32_t unit = 0;                      // the segment's first unit
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
             const Seg w = take();
-            if (bar_any(bar, 128, *dead != 0) || w.units == 0) break;   // after a wait that gave up, all of the warpgroup leaves
+            if (bar_any(bar, 128, raised(dead)) || w.units == 0) break;   // after a wait that gave up, all of the warpgroup leaves
             const int par = seg & 1, last0 = w.last0, rows = w.R - col0;   // live rows of this thread
             const int active = min((w.R + NC - 1) / NC, kTeam);     // warpgroups of the team with rows
             const bool speaks = key == 0;       // for the warpgroup
@@ -680,12 +688,11 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             bool fresh = true;
             int vref = 0;                       // scale byte that O^T is relative to
 #pragma unroll 1
-            for (int i = unit + (kStream ? (unit ^ gi) & 1 : 0); i < unit + w.units; i += kGroups) {
+            for (uint32_t i = unit + (kStream ? (unit ^ gi) & 1u : 0u); i < unit + w.units; i += kGroups) {
                 const uint32_t b = i & 1, use = (i >> 1) & 1;       // P^T buffer, its round
                 if (rows <= 0) {
                     // No rows here: one warp keeps up with the team's barriers (a barrier's
-                    // parity is only sound for one that sees every phase: its lanes join
-                    // before one arrives, or the phase is over before the last has looked).
+                    // parity is only sound for one that sees every phase).
                     if (qd == 0) {
                         wait(BAR(s_full, i % NS), (i / NS) & 1, dead);
                         __syncwarp();
@@ -698,12 +705,13 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     continue;
                 }
                 const uint32_t st = lanes + i % NS * RP + col0;
-                const int kp = (w.c0 + i - unit) * kChunk + key;
+                const int kp = (w.c0 + (int)(i - unit)) * kChunk + key;
                 const bool masked = kp - key + kChunk - 1 > last0;  // some row does not see all of the chunk
                 // One warp waits for the warpgroup.
                 if (qd == 0) {
                     wait(BAR(c_full, i % kScaleSlots), (i / kScaleSlots) & 1, dead);
                     wait(BAR(s_full, i % NS), (i / NS) & 1, dead);
+                    if (!kStream) wait(BAR(p_empty, b), use ^ 1, dead);
                 }
                 named_bar_sync(bar, 128);
                 tc_fence_after();
@@ -805,7 +813,9 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                         for (int j = 0; j < NC; ++j)
                             if (j < hidden) x[j] = -INFINITY;
                     }
-                    wait(BAR(p_empty, b), use ^ 1, dead);       // this P^T buffer's last product is done
+                    // This P^T buffer's last product is done.  (Of one team: the chunk before the
+                    // last one's, which has been waited for above; of two, the team's last.)
+                    if (kStream) wait(BAR(p_empty, b), use ^ 1, dead);
                     uint32_t top = 0;           // the largest halves
                     static_assert(NC == 16, "a thread's rows are one 16-byte piece of each part");
                     uint32_t c1[4], c2[4], c3[4];
@@ -903,20 +913,31 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
         regs_down<L::kResultRegs>();
         const int qd = warp & 3, d = qd * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
+        constexpr int kRowThreads = HD / 8, kPass = 128 / kRowThreads;     // 8 elements a thread; rows that the warpgroup splits at once
+        constexpr int kAhead = RP / kPass < 2 ? RP / kPass : 2;            // and how many times that much is in flight
+        const int b = d & (kRowThreads - 1), qrow = d / kRowThreads;
         Ring<2> qr;
-        // Queries in two e4m3 parts with a power of two for each row, 8 elements a thread.
-        auto split_queries = [&](const Seg& s, int par) {
-            constexpr int kRowThreads = HD / 8, kPass = 128 / kRowThreads;
+        uint4 ahead[kAhead];
+        auto fetch = [&](const Seg& s, int r0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int r = r0 + k * kPass + qrow;
+                if (r >= s.R) continue;
+                const int t = token(s, r);
+                ahead[k] = *reinterpret_cast<const uint4*>(p.q + (long long)(s.row0 + t) * p.q_stride +
+                                                           (long long)(s.head * p.group + s.skip + r - t * p.group) * HD + b * 8);
+            }
+        };
+        // Queries in two e4m3 parts with a power of two for each row.
+        auto split_queries = [&](const Seg s, int par) {
+            fetch(s, 0);
             wait(BAR(q_empty, qr.at), qr.round ^ 1, dead);
             uint8_t* const tile = qs + qr.at * L::kQ;
-            const int b = d & (kRowThreads - 1);
 #pragma unroll 1
-            for (int r0 = 0; r0 < s.R; r0 += kPass) {
-                const int r = r0 + d / kRowThreads, t = token(s, min(r, s.R - 1));
-                uint4 x = {};
-                if (r < s.R)
-                    x = *reinterpret_cast<const uint4*>(p.q + (long long)(s.row0 + t) * p.q_stride +
-                                                        (long long)(s.head * p.group + s.skip + r - t * p.group) * HD + b * 8);
+            for (int r = qrow, k = 0; r - qrow < s.R; r += kPass) {
+                const uint4 x = ahead[0];
+#pragma unroll
+                for (int e = 0; e + 1 < kAhead; ++e) ahead[e] = ahead[e + 1];
                 const uint32_t* y = &x.x;
                 uint32_t top = 0;               // largest finite magnitude
 #pragma unroll
@@ -944,6 +965,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     *reinterpret_cast<uint2*>(at + L::kQPart) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
                     if (b == 0) sh.qmul[par][r] = __uint_as_float((f - 7u) << 23) * p.scale_log2;
                 }
+                if (RP > kAhead * kPass && ++k == kAhead) k = 0, fetch(s, r - qrow + kPass);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -952,17 +974,20 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             qr.step();
         };
         int i = 0;                              // the segment's first unit
-        Seg next = {};
 #pragma unroll 1
-        for (int seg = -1;; ++seg) {
-            const Seg w = next;
-            next = take();
-            if (bar_any(kResultBar, 128, *dead != 0)) break;
-            if (next.units) split_queries(next, (seg + 1) & 1);
+        for (int seg = -1;; ++seg) {            // the next segment's queries, then this one's results
+            wait(BAR(seg_full, sr.at), sr.round, dead);
+            __syncwarp();
+            if (bar_any(kResultBar, 128, raised(dead))) break;
+            const bool more = sh.segs[sr.at].units != 0;
+            if (more) split_queries(sh.segs[sr.at], (seg + 1) & 1);
+            const int here = (sr.at + kSegs - 1) % kSegs;
+            sr.step();
             if (seg < 0) {
-                if (next.units == 0) break;
+                if (!more) break;
                 continue;
             }
+            const Seg w = sh.segs[here];
             const int par = seg & 1, last0 = w.last0;
             const int ga = kStream ? i & 1 : 0; // the team of the first unit; the other has none in a segment of one
             const bool two = kStream && w.units > 1, whole = w.slot < 0;
@@ -994,7 +1019,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 // O^T is in units of 2^(r - 3), r the warpgroup's that formed the row's weights
                 fa = fa * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][ga * kTeam + r / NC]);
                 if (two) fb = fb * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][(ga ^ 1) * kTeam + r / NC]);
-                sh.row[par][r] = {{fa, fb}, whole ? t * p.out_stride + (long long)(r - t * p.group) * HD : (long long)r * HD};
+                sh.row[par][r] = {{fa, fb}, t * p.out_stride + (long long)(r - t * p.group) * HD};
             }
             if (qd == 0) wait(BAR(o_full, par), (seg >> 1) & 1, dead);
             named_bar_sync(kResultBar, 128);
@@ -1032,20 +1057,23 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                                 for (int e = 0; e < 8; ++e)
                                     if (t <= last0 + token(w, j0 + e)) o[e] = __uint_as_float(0x7FC00000u);
                         }
+                    if (whole) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (j0 + e < w.R) {
-                            const long long at = sh.row[par][j0 + e].at;
-                            if (whole) out[at] = f2bf(o[e]);
-                            else part[at] = o[e];
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            if (j0 + e < w.R) out[sh.row[par][j0 + e].at] = f2bf(o[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (j0 + e < w.R) part[(j0 + e) * HD] = o[e];
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
             arrive_if(BAR(o_empty, par), lane == 0);
             arrive_if(BAR(l_empty, par), lane == 0);
-            if (next.units == 0) break;
+            arrive_if(BAR(seg_empty, here), lane == 0);
+            if (!more) break;
         }
     }
     tc_fence_before();

@@ -16,7 +16,7 @@ constexpr int kSmem = 227 * 1024;           // of a CTA
 constexpr int kSlots = 8;                   // at most, of K and of V
 constexpr int kScaleSlots = 8;              // chunks whose scales are loaded ahead
 constexpr int kParts = 3;                   // parts of a weight
-constexpr int kSegs = 4;                    // segments listed ahead
+constexpr int kSegs = 8;                    // segments in the list: those ahead, and those whose results are not written
 constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
 
 // Limits of one wait (2^31 cycles each) that the results of a segment are waited for:

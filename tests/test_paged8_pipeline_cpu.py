@@ -12,7 +12,7 @@ import subprocess
 
 import pytest
 
-from test_paged_pipeline_cpu import SEGS, Barrier, Model
+from test_paged_pipeline_cpu import Barrier, Model
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = r"""
@@ -21,14 +21,14 @@ SRC = r"""
 using namespace sv::plan8;
 template <int HD, int RP> void line() {
     using L = Plan<HD, RP>;
-    printf("%d %d %d %d %d %d %d %d %d %d %d\n", HD, RP, (int)sizeof(Fixed<RP>), L::kBytes, L::NK, L::NV, kScaleSlots, L::kTeam, (int)L::kStream, L::NS, L::kUsed);
+    printf("%d %d %d %d %d %d %d %d %d %d %d %d\n", HD, RP, (int)sizeof(Fixed<RP>), L::kBytes, L::NK, L::NV, kScaleSlots, L::kTeam, (int)L::kStream, L::NS, L::kUsed, kSegs);
 }
 int main() {
     line<64, 16>(); line<64, 32>(); line<64, 64>();
     line<128, 16>(); line<128, 32>(); line<128, 64>();
 }
 """
-NAMES = ["HD", "RP", "fixed", "bytes", "NK", "NV", "NC", "team", "stream", "NS", "columns"]
+NAMES = ["HD", "RP", "fixed", "bytes", "NK", "NV", "NC", "team", "stream", "NS", "columns", "SEGS"]
 
 
 @pytest.fixture(scope="module")
@@ -74,10 +74,24 @@ class Model8(Model):
         self.s_full, self.s_empty = n(pl["NS"]), n(pl["NS"], team)
         self.groups = team * (2 if pl["stream"] else 1)
         self.p_full, self.l_full = n(2, team), n(2, 4 * self.groups)
-        self.seg_empty = n(SEGS, 4 * self.groups + 3 + 4)
+        self.segs = [None] * pl["SEGS"]
+        self.seg_full, self.seg_empty = n(pl["SEGS"]), n(pl["SEGS"], 4 * self.groups + 3 + 4)
         self.active = [rng.randint(1, team) for _ in segments]
         self.place = [-1] * self.groups                           # segment of each warpgroup
         self.passed = [[0, 0] for _ in range(self.groups)]        # waits that the arriving lane and the others have left
+
+    def listed(self, g):
+        """The list's entry g, not let go yet."""
+        n = self.pl["SEGS"]
+        yield from self.wait(self.seg_full[g % n], g // n)
+        s = self.segs[g % n]
+        assert s is None or s[0] == g
+        return s
+
+    def take(self, g):
+        s = yield from self.listed(g)
+        self.seg_empty[g % self.pl["SEGS"]].arrive()
+        return s
 
     def take4(self, g):
         """A warpgroup's four warps take a segment."""
@@ -89,9 +103,10 @@ class Model8(Model):
     def load_k(self):
         u, nk, nc = 0, self.pl["NK"], self.pl["NC"]
         for g in range(len(self.segments) + 1):
-            yield from self.free(self.seg_empty[g % SEGS], g // SEGS)
-            self.segs[g % SEGS] = (g, self.segments[g]) if g < len(self.segments) else None
-            self.seg_full[g % SEGS].arrive()
+            n = self.pl["SEGS"]
+            yield from self.free(self.seg_empty[g % n], g // n)
+            self.segs[g % n] = (g, self.segments[g]) if g < len(self.segments) else None
+            self.seg_full[g % n].arrive()
             if g == len(self.segments):
                 return
             for _ in range(self.segments[g][0]):
@@ -178,6 +193,8 @@ class Model8(Model):
                 yield from self.wait(self.s_full[i % ns], i // ns)
                 assert self.buf[("s", i % ns)] == i and self.buf[("r", g % 2)] == g
                 b, use = i % 2, i // 2
+                if not self.pl["stream"]:
+                    yield from self.free(self.p_empty[b], use)
                 if k >= (2 if self.pl["stream"] else 1) and self.rng.random() < 0.2:          # a reference moves
                     j = i - (2 if self.pl["stream"] else 1)    # the last product into this O^T
                     yield from self.wait(self.p_empty[j % 2], j // 2)
@@ -185,7 +202,8 @@ class Model8(Model):
                 for _ in range(1 if not self.absent or wg % team else 1 + team - active):
                     self.s_empty[i % ns].arrive()
                     self.c_empty[i % nc].arrive()
-                yield from self.free(self.p_empty[b], use)
+                if self.pl["stream"]:
+                    yield from self.free(self.p_empty[b], use)
                 if self.buf.setdefault(("p", b), set()) != {i}:
                     self.buf[("p", b)] = {i}
                 if k >= s[1][0] - s[1][1] and wg % team == active - 1:
@@ -213,24 +231,27 @@ class Model8(Model):
         self.r_full[g % 2].arrive()
 
     def results(self, warp):
-        s = yield from self.take(0)
-        if s is not None:
-            yield from self.split(warp, 0)
-        g = 0
-        while s is not None:
-            s = yield from self.take(g + 1)
-            if s is not None:
+        g, n = -1, self.pl["SEGS"]
+        while True:
+            nxt = yield from self.listed(g + 1)
+            if nxt is not None:
                 yield from self.split(warp, g + 1)
-            yield from self.wait(self.l_full[g % 2], g // 2)
-            assert all(self.refs[(g % 2, w)] == g for w in range(self.groups))
             yield
-            yield from self.wait(self.o_full[g % 2], g // 2)
-            yield
-            assert all(self.refs[(g % 2, w)] == g for w in range(self.groups))
-            self.o_empty[g % 2].arrive()
-            self.l_empty[g % 2].arrive()
-            if warp == 0:
-                self.done_results.append(g)
+            if g >= 0:
+                assert self.segs[g % n][0] == g                   # still there
+                yield from self.wait(self.l_full[g % 2], g // 2)
+                assert all(self.refs[(g % 2, w)] == g for w in range(self.groups))
+                yield
+                yield from self.wait(self.o_full[g % 2], g // 2)
+                yield
+                assert all(self.refs[(g % 2, w)] == g for w in range(self.groups)) and self.segs[g % n][0] == g
+                self.o_empty[g % 2].arrive()
+                self.l_empty[g % 2].arrive()
+                self.seg_empty[g % n].arrive()
+                if warp == 0:
+                    self.done_results.append(g)
+            if nxt is None:
+                return
             g += 1
 
     def schedule(self, roles):
