@@ -642,8 +642,28 @@ spec_status spec_paged_read_fp8(const int32_t* d_slots, const int32_t* d_row_cou
 
 /* spec_paged_attention over such pools: out[row][h] = sum_i softmax_i(scale *
  * q[row][h] . k_i) v_i with k_i and v_i as the codes and scales give them.
- * Arguments, layouts, limits and errors as there, with d_scales (16-byte
- * aligned) beside the pools, and a workspace of its own. */
+ * Arguments, layouts, rows, skipped sequences, bad pages and errors as there,
+ * with d_scales (16-byte aligned) beside the pools, and a workspace of its own.
+ * The codes enter the products as they are.  Queries are split into two e4m3
+ * parts with a power of two for each row: exact but for elements below 2^-8 of
+ * the row's largest, of which 2^-17 of the largest is lost.  Scores, softmax
+ * and sums are fp32; a weight enters the second product off by at most 2^-9 of
+ * it, and what lies below 2^-25 of the largest weight times the largest value
+ * scale among the chunks that the sequence's rows were dealt with so far (a
+ * finite later draft's scale counts there too) is lost.
+ * Values behind a sequence's length are never used, nor is a position that a
+ * row may not see, whatever codes and scales are there.  A visible NaN value
+ * makes that dimension of the rows that see it NaN; a visible scale byte of
+ * 255, or a NaN key, makes the whole row NaN, and an infinite or NaN query
+ * element its own row.
+ * A score is formed as (the sum over the codes) * (the key's scale) * (the
+ * query row's power of two * scale * log2(e)), each product in fp32: exact in
+ * range as long as a key's scale lies within 2^-100 .. 2^100 and a query row's
+ * largest element above 2^-119.
+ * The limit on the work: with T the smallest of 16, 32 and 64 that holds
+ * max_new tokens' rows, else 64, and t the multiple of (query heads per kv
+ * head) next below T (T itself if there is none), (nseq + rows * (query heads
+ * per kv head) / t) * n_kv_heads * (ceil(table_pages / 2) + 4) below 2^31. */
 spec_status spec_paged_attention_fp8_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
                                                int32_t table_pages, size_t* out_bytes);
 spec_status spec_paged_attention_fp8(const void* d_q, int64_t q_stride, const int32_t* d_row_start, const int32_t* d_len,

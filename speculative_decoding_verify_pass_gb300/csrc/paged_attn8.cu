@@ -360,13 +360,10 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             mbar_init(&sh.v_empty[lane], 1);
         }
         if (lane < NS) {
-            mbar_init(&sh.s_full[lane], 1);
+            mbar_init(&sh.s_full[lane], 2);     // the product, and the warp that saw its K's scales arrive
             mbar_init(&sh.s_empty[lane], kArrive);
         }
-        if (lane < kScaleSlots) {
-            mbar_init(&sh.c_full[lane], 1);
-            mbar_init(&sh.c_empty[lane], kArrive);
-        }
+        if (lane < kScaleSlots) mbar_init(&sh.c_empty[lane], kArrive);
         if (lane < 2) {
             mbar_init(&sh.q_full[lane], 4);
             mbar_init(&sh.q_empty[lane], 1);
@@ -504,7 +501,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (elect_one()) {
-                        const uint32_t cf = BAR(c_full, cr.at), full = BAR(k_full, kr.at);
+                        const uint32_t full = BAR(k_full, kr.at);    // of K and its scales
                         const uint32_t to = shb + (uint32_t)offsetof(F, scale) + cr.at * 4 * SPEC_PAGE, dst = ka + kr.at * L::kSlot;
                         // a bad page (it reads as zeros) has no scales: ones
                         const bool c0 = pages.count > 0 && pages.z0 >= 0, c1 = pages.count > 1 && pages.z1 >= 0;
@@ -515,10 +512,9 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                                 if (i < 8 ? !c0 : !c1) sts4(to + i * 16, kOnes, kOnes, kOnes, kOnes);
                             fence_proxy_async_smem();
                         }
-                        arrive_expect_tx(cf, (c0 ? 2 * SPEC_PAGE : 0) + (c1 ? 2 * SPEC_PAGE : 0));
-                        if (c0) bulk_load(to, p.scales + (size_t)pages.z0 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, cf);
-                        if (c1) bulk_load(to + 2 * SPEC_PAGE, p.scales + (size_t)pages.z1 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, cf);
-                        arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD));
+                        arrive_expect_tx(full, (uint32_t)(pages.count * SPEC_PAGE * HD) + (c0 ? 2 * SPEC_PAGE : 0) + (c1 ? 2 * SPEC_PAGE : 0));
+                        if (c0) bulk_load(to, p.scales + (size_t)pages.z0 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, full);
+                        if (c1) bulk_load(to + 2 * SPEC_PAGE, p.scales + (size_t)pages.z1 * 2 * SPEC_PAGE, 2 * SPEC_PAGE, full);
                         if (pages.count > 0) tile_load(dst, &p.mk, pages.z0, full);
                         if (pages.count > 1) tile_load(dst + SPEC_PAGE * HD, &p.mk, pages.z1, full);
                     }
@@ -530,8 +526,6 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             if (lane == 0 && raised(dead)) {          // every buffer's last copy, as far as one was issued
 #pragma unroll 1
                 for (int i = 0; i < NK; ++i) give_up(BAR(k_full, i), i < kr.at ? kr.round : kr.round ^ 1);
-#pragma unroll 1
-                for (int i = 0; i < kScaleSlots; ++i) give_up(BAR(c_full, i), i < cr.at ? cr.round : cr.round ^ 1);
             }
         } else if (warp == kLoadVWarp) {
             // ---------------- V copies ----------------
@@ -596,6 +590,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                             for (int e = 0; e < HD / 32; ++e)
                                 umma8_lo(tmem + sb.at * RP, dk + e * 2, kHi, dq + part * (L::kQPart >> 4) + e * 2, kHi, id, (part | e) != 0);
                         commit(BAR(s_full, sb.at));
+                        arrive(BAR(s_full, sb.at));             // (after K's barrier: the softmax reads scales that came with K)
                         commit(BAR(k_empty, ks.at));
                         if (k == s.units - 1) commit(BAR(q_empty, qr.at));
                     }
@@ -709,7 +704,6 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 const bool masked = kp - key + kChunk - 1 > last0;  // some row does not see all of the chunk
                 // One warp waits for the warpgroup.
                 if (qd == 0) {
-                    wait(BAR(c_full, i % kScaleSlots), (i / kScaleSlots) & 1, dead);
                     wait(BAR(s_full, i % NS), (i / NS) & 1, dead);
                     if (!kStream) wait(BAR(p_empty, b), use ^ 1, dead);
                 }

@@ -69,7 +69,7 @@ struct Fixed {
     alignas(16) int tok[RP];                        // token of each row of a block that begins with a token
     Out row[2][RP];                                 // by segment parity: for the results
     long long warp_sum[T::kWarps];
-    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], c_full[kScaleSlots], c_empty[kScaleSlots], q_full[2],
+    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], c_empty[kScaleSlots], q_full[2],
         q_empty[2], r_full[2], s_full[T::NS], s_empty[T::NS], p_full[2], p_empty[2], o_full[2], o_empty[2], l_full[2], l_empty[2],
         seg_full[kSegs], seg_empty[kSegs], fin[2];
     int first[split::kMaxSeqs + 1];

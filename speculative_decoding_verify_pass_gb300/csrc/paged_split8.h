@@ -13,6 +13,12 @@
 // segments would end late (64 ragged decodes: 104 us with one such unit, 95 with four;
 // 24 sequences of 16 new rows: 206 and 154).  A CTA whose range holds only such units of a pair does
 // not work on it; the CTA that holds its first chunk owns it.
+//
+// Pairs of short tables are left whole by the bf16 calls' rule (split::whole_pairs, up to
+// 1024 positions), which holds here too: 8 kv heads of 128, decode, every sequence
+// full, split against whole in us with 1, 16 and 64 sequences: 512 positions 7.7 / 6.7,
+// 11.7 / 8.5, 22.6 / 18.3; 1024 8.5 / 8.1, 13.8 / 10.2, 31.2 / 29.1; 2048 9.2 / 11.2,
+// 15.6 / 13.2, 50.2 / 49.7; 4096 9.6 / 17.3, 29.6 / 26.0, 89.5 / 90.0.
 #pragma once
 
 #include "paged_split.h"
@@ -25,7 +31,7 @@ using split::Deal;
 using split::kChunk;
 
 constexpr int kHead = 4;                // units in front of a pair's chunks
-constexpr int kMostRows = 64;           // of a tile
+constexpr int kMostRows = 64;           // of a tile: 128 rows' S^T, O^T and their parts do not fit tensor memory
 
 // Tile height that the kernel is compiled for, and the rows of a block in it.
 SPLIT_HD int tile_height(int group, int max_new) {

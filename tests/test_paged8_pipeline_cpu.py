@@ -70,8 +70,8 @@ class Model8(Model):
         n = lambda k, c=1: [Barrier(c) for _ in range(k)]  # noqa: E731
         team = pl["team"]
         self.q_full, self.r_full = n(2, 4), n(2, 4)
-        self.c_full, self.c_empty = n(pl["NC"]), n(pl["NC"], team)
-        self.s_full, self.s_empty = n(pl["NS"]), n(pl["NS"], team)
+        self.c_empty = n(pl["NC"], team)
+        self.s_full, self.s_empty = n(pl["NS"], 2), n(pl["NS"], team)
         self.groups = team * (2 if pl["stream"] else 1)
         self.p_full, self.l_full = n(2, team), n(2, 4 * self.groups)
         self.segs = [None] * pl["SEGS"]
@@ -112,8 +112,7 @@ class Model8(Model):
             for _ in range(self.segments[g][0]):
                 yield from self.free(self.c_empty[u % nc], u // nc)
                 yield from self.free(self.k_empty[u % nk], u // nk)
-                self.async_("tk", lambda u=u: (self.put(("c", u % nc), u), self.c_full[u % nc].arrive()))
-                self.async_("tma", lambda u=u: (self.put(("k", u % nk), u), self.k_full[u % nk].arrive()))
+                self.async_("tk", lambda u=u: (self.put(("c", u % nc), u), self.put(("k", u % nk), u), self.k_full[u % nk].arrive()))
                 u += 1
                 yield
 
@@ -136,6 +135,7 @@ class Model8(Model):
                     if last:
                         self.q_empty[g % 2].arrive()
                 self.async_("score", mma)
+                self.s_full[u % ns].arrive()
                 u += 1
                 yield
 
@@ -188,9 +188,8 @@ class Model8(Model):
                     continue
                 if wg % team >= active:
                     continue
-                yield from self.wait(self.c_full[i % nc], i // nc)
-                assert self.buf[("c", i % nc)] == i
                 yield from self.wait(self.s_full[i % ns], i // ns)
+                assert self.buf[("c", i % nc)] == i                 # the scales came with K
                 assert self.buf[("s", i % ns)] == i and self.buf[("r", g % 2)] == g
                 b, use = i % 2, i // 2
                 if not self.pl["stream"]:
