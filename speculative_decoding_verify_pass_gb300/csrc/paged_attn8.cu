@@ -35,11 +35,14 @@
 // 8 heads a kv head: 206 against 210 us then, 200 short ones 62 and 62), and one code
 // serves every tile.
 //
-// What bounds it: long caches memory (100003 positions of 8 kv heads: 39.6 us, 30.3 at
-// the copy rate; 64 ragged decodes 95, of 83), short sequences a segment's way through the
-// roles (200 of them 61 us: about 8 go to the results, 10 to the weights), many rows the
-// softmax's issue (24 x 16 new rows 154 us: a weight costs 8 instructions beside its
-// exp2, and the conversions to halves share its pipe).
+// What bounds it: long caches memory (100003 positions of 8 kv heads of 128: 39.7 us, 30.3
+// at the copy rate; 64 ragged decodes 94.8, of 83), short sequences a segment's way through
+// the roles (2.1 us a segment of one chunk at 16 rows, 0.4 a further chunk of 64-wide
+// heads; 200 ragged blocks 46 us), many rows a chunk's way through the softmax (64 rows:
+// 2300 cycles, of which 1000 issue; 24 sequences of 16 new at 8 heads a kv head 127 us).
+// The roles share one instruction cache, so that code costs time wherever it stands: the
+// last two were 62 and 154 us when the kernel had 86 KB, with divisions in the walk over the
+// segments, each wait's loop twice, and rows' addresses formed where they are written.
 #include <stddef.h>
 #include <stdio.h>
 

@@ -4,8 +4,9 @@ test_paged_pipeline_cpu.py runs the bf16 kernel's.
 
 What is new against that model: the results' warps split the next segment's queries
 before they write a segment's results (q_full, and r_full for what the softmax needs
-of the rows), scales have a ring of their own, and a warpgroup frees its chunk's
-scales with its S^T."""
+of the rows) and let a segment's entry in the list go when its results are written,
+scales arrive with K but have a ring of their own, which a chunk's warpgroups free with
+its S^T."""
 import os
 import random
 import subprocess
