@@ -35,8 +35,8 @@
 // 8 heads a kv head: 206 against 210 us then, 200 short ones 62 and 62), and one code
 // serves every tile.
 //
-// What bounds it: long caches memory (100003 positions of 8 kv heads of 128: 39.7 us, 30.3
-// at the copy rate; 64 ragged decodes 94.8, of 83), short sequences a segment's way through
+// What bounds it: long caches memory (100003 positions of 8 kv heads of 128: 39.4 us, 30.3
+// at the copy rate; 64 ragged decodes 91.8, of 83), short sequences a segment's way through
 // the roles (2.1 us a segment of one chunk at 16 rows, 0.4 a further chunk of 64-wide
 // heads; 200 ragged blocks 46 us), many rows a chunk's way through the softmax (64 rows:
 // 2300 cycles, of which 1000 issue; 24 sequences of 16 new at 8 heads a kv head 127 us).
@@ -456,7 +456,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
 #define BAR(x, i) (shb + (uint32_t)offsetof(F, x) + (uint32_t)(i) * 8u)
     const uint32_t dead = shb + (uint32_t)offsetof(F, dead);
     // token of row r of a block, counted from its first row's (which the block may begin in the middle of)
-    auto token = [&](const Seg& s, int r) { return p.group > RP ? (int)(s.skip + r >= p.group) : sh.tok[r]; };
+    auto token = [&](const Seg& s, int r) { return RP == split8::kMostRows && p.group > RP ? (int)(s.skip + r >= p.group) : sh.tok[r]; };
     Ring<kSegs> sr;                             // every role's place in the list of segments
     auto take = [&]() {                         // the next segment
         wait(BAR(seg_full, sr.at), sr.round, dead);
@@ -927,11 +927,12 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
         };
         // Queries in two e4m3 parts with a power of two for each row.
         auto split_queries = [&](const Seg s, int par) {
-            fetch(s, 0);
             wait(BAR(q_empty, qr.at), qr.round ^ 1, dead);
             uint8_t* const tile = qs + qr.at * L::kQ;
 #pragma unroll 1
             for (int r = qrow, k = 0; r - qrow < s.R; r += kPass) {
+                if (k == 0) fetch(s, r - qrow);
+                if (++k == kAhead) k = 0;
                 const uint4 x = ahead[0];
 #pragma unroll
                 for (int e = 0; e + 1 < kAhead; ++e) ahead[e] = ahead[e + 1];
@@ -962,7 +963,6 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     *reinterpret_cast<uint2*>(at + L::kQPart) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
                     if (b == 0) sh.qmul[par][r] = __uint_as_float((f - 7u) << 23) * p.scale_log2;
                 }
-                if (RP > kAhead * kPass && ++k == kAhead) k = 0, fetch(s, r - qrow + kPass);
             }
             fence_proxy_async_smem();
             __syncwarp();

@@ -13,7 +13,11 @@ namespace plan8 {
 using split8::kChunk;
 
 constexpr int kSmem = 227 * 1024;           // of a CTA
-constexpr int kSlots = 8;                   // at most, of K and of V
+// K and V that a CTA has in flight or in use, 64 KB of each: 8 slots of 64-wide heads, 4
+// of 128-wide ones, where there is room for 6, but 64 ragged decodes take 94.0 us with
+// 6, 92.9 with 5, 91.7 with 4, 93.3 with 3 (of 64-wide ones fewer than 8 cost up to 15 %).
+constexpr int kAhead = 64 * 1024;
+constexpr int kSlots = kAhead / (kChunk * 64);
 constexpr int kScaleSlots = 8;              // chunks whose scales are loaded ahead
 constexpr int kParts = 3;                   // parts of a weight
 constexpr int kSegs = 8;                    // segments in the list: those ahead, and those whose results are not written
@@ -92,7 +96,7 @@ struct Plan : Rows<RP> {
     static constexpr int kOther = 2 * kQ + 2 * kParts * kP + 1024 + kPad;   // two query tiles, two P^T's; 1024: alignment
     static constexpr int kMost = kSmem - (int)sizeof(Fixed<RP>) - kOther;
     static constexpr int kFit = kMost / kSlot / 2;
-    static constexpr int NK = kFit < kSlots ? kFit : kSlots, NV = NK;
+    static constexpr int NK = kFit < kAhead / kSlot ? kFit : kAhead / kSlot, NV = NK;
     static constexpr int kBytes = kOther + (NK + NV) * kSlot;
     static constexpr int kO = kParts * RP;                  // tensor-memory columns of one O^T: its parts side by side
     static constexpr int kUsed = T::NS * RP + 2 * T::kGroups * kO;  // S^T's, O^T x 2 (per team)
