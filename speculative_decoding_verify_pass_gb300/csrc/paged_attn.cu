@@ -63,6 +63,7 @@ using plan::kWarps;
 using plan::Plan;
 using plan::Seg;
 
+constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
 constexpr int kSoftWarps = 8, kScoreWarp = 8, kLoadVWarp = 10, kLoadKWarp = 11, kResultWarp = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLimit = 40.f;          // log2 by which a score may exceed its row's reference

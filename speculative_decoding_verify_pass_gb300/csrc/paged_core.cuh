@@ -1,7 +1,6 @@
 // What the attention kernels over a paged cache share, whatever its pages hold:
-// waits, tensor-memory and matrix-descriptor helpers, the walk over a CTA's
-// segments and their pages, the join of pairs that CTAs shared, and the host's part
-// of a launch.
+// waits, tensor-memory and matrix-descriptor helpers, the walk over a segment's
+// pages, the join of pairs that CTAs shared, and the host's part of a launch.
 #pragma once
 
 #include <cuda.h>
@@ -17,7 +16,6 @@ namespace {
 
 using split::kChunk;
 
-constexpr float kWide = 1 << 24;        // size of a reference from which its own rounding counts
 constexpr float kNone = -FLT_MAX;       // reference of a row that has seen no key: no score lies below it
 
 // A split pair, as the join kernel sees it from one of its CTAs.
