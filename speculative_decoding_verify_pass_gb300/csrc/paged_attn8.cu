@@ -39,7 +39,7 @@
 // at the copy rate; 64 ragged decodes 91.8, of 83), short sequences a segment's way through
 // the roles (2.1 us a segment of one chunk at 16 rows, 0.4 a further chunk of 64-wide
 // heads; 200 ragged blocks 46 us), many rows a chunk's way through the softmax (64 rows:
-// 2300 cycles, of which 1000 issue; 24 sequences of 16 new at 8 heads a kv head 127 us).
+// 2200 cycles, of which 1000 issue; 24 sequences of 16 new at 8 heads a kv head 124 us).
 // The roles share one instruction cache, so that code costs time wherever it stands: the
 // last two were 62 and 154 us when the kernel had 86 KB, with divisions in the walk over the
 // segments, each wait's loop twice, and rows' addresses formed where they are written.
@@ -911,7 +911,7 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
         const int qd = warp & 3, d = qd * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(qd * 32) << 16);
         constexpr int kRowThreads = HD / 8, kPass = 128 / kRowThreads;     // 8 elements a thread; rows that the warpgroup splits at once
-        constexpr int kAhead = RP / kPass < 2 ? RP / kPass : 2;            // and how many times that much is in flight
+        constexpr int kAhead = RP / kPass < 4 ? RP / kPass : 4;            // and how many times that much is in flight
         const int b = d & (kRowThreads - 1), qrow = d / kRowThreads;
         Ring<2> qr;
         uint4 ahead[kAhead];

@@ -101,9 +101,11 @@ struct Plan : Rows<RP> {
     static constexpr int kO = kParts * RP;                  // tensor-memory columns of one O^T: its parts side by side
     static constexpr int kUsed = T::NS * RP + 2 * T::kGroups * kO;  // S^T's, O^T x 2 (per team)
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
-    // registers of a thread, by role: the same for all at launch, moved to where S^T and P^T live
-    static constexpr int kLaunchRegs = T::kSoftGroups == 2 ? 128 : 80, kSoftRegs = T::kSoftGroups == 2 ? 160 : 88, kIssueRegs = 56,
-                         kResultRegs = T::kSoftGroups == 2 ? 112 : 72;
+    // Registers of a thread, by role: the same for all at launch, moved to where S^T and P^T
+    // live.  (Four softmax warpgroups leave 480 to share out: 88, 48 and 80 spill least
+    // and take 24 sequences of 16 new at 8 heads a kv head from 127 us, with 88, 56 and 72, to 124.)
+    static constexpr bool kTwo = T::kSoftGroups == 2;
+    static constexpr int kLaunchRegs = kTwo ? 128 : 80, kSoftRegs = kTwo ? 160 : 88, kIssueRegs = kTwo ? 56 : 48, kResultRegs = kTwo ? 112 : 80;
     static_assert(T::kSoftGroups * kSoftRegs + kIssueRegs + kResultRegs <= (T::kSoftGroups + 2) * kLaunchRegs,
                   "more registers than the block was launched with");
     static_assert(T::kWarps * 32 * kLaunchRegs <= 65536, "more registers than an SM has");
