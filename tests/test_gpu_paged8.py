@@ -449,6 +449,50 @@ def test_attention_queries_of_any_size(exponent):
     c.check(c.run(scale=2.0 ** (-exponent - 3)), rows=[1] if exponent > 0 else [], scale=2.0 ** (-exponent - 3))
 
 
+@pytest.mark.parametrize("exponent", [90, -90])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (32, 2, 128)])
+def test_attention_keys_of_any_size(exponent, heads):
+    """Keys whose scales lie far from 1, queries that bring the scores back."""
+    torch = torch_cuda()
+    c = Case8([700, 130], [3, 2], *heads, seed=23)
+    for q, n in enumerate(c.lens):
+        c.k[q] = (c.k[q].float() * 2.0 ** exponent).bfloat16()
+        c.place(q, torch.arange(n))
+    c.q = (c.q.float() * 2.0 ** -exponent).bfloat16()
+    c.d["q"] = c.q.cuda()
+    c.upload()
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (32, 2, 128), (65, 1, 128), (4, 4, 64)])
+@pytest.mark.parametrize("seed", range(4))
+def test_attention_nan_codes_and_scales_reach_the_rows_that_see_them(heads, seed):
+    """NaN codes of either sign and scale bytes of 255 anywhere in the cache: a value's NaN in its
+    dimension, a key's and a scale's in the whole row of every query head of its kv head."""
+    c = Case8([300, 1, 129, 2100, 64], [8, 1, 3, 2, 1], *heads, seed=24 + seed)
+    rng = random.Random(seed)
+    for _ in range(6):
+        q = rng.randrange(len(c.lens))
+        n, h, d, nan = c.lens[q], rng.randrange(c.hkv), rng.randrange(c.hd), rng.choice([127, 255])
+        t = n - 1 - rng.randint(0, min(n - 1, rng.choice([1, 9, n])))
+        page, o = int(c.tables_cpu[q, t // PAGE]), t % PAGE
+        kind = rng.choice(["value", "key", "values' scale", "keys' scale"])
+        if kind == "value":
+            c.vp8[page, h, o, d] = nan
+            c.v[q][t, h, d] = float("nan")
+        elif kind == "key":
+            c.kp8[page, h, o, d] = nan
+            c.k[q][t, h, d] = float("nan")
+        else:
+            c.sc[page, h, int(kind[0] == "v"), o] = 255
+            c.k[q][t, h] = float("nan")
+    c.upload()
+    got = c.run().double().cpu().numpy()[:c.start[-1]]
+    out, bound = (x[:c.start[-1]] for x in c.reference())
+    seen = np.isnan(out)
+    assert np.array_equal(np.isnan(got), seen) and (np.abs(got - out)[~seen] <= bound[~seen]).all()
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("n", [130, 136, 128, 300])
