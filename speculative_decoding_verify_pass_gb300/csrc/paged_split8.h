@@ -10,7 +10,7 @@
 //
 // A pair begins with kHead units that are no chunk: a segment costs about as much
 // beside its chunks (queries, references, sums, results), and CTAs with many short
-// segments would end late (64 ragged decodes: 104 us with one such unit, 95 with four;
+// segments would end late (64 ragged decodes: 104 us with one such unit, 95 with four then;
 // 24 sequences of 16 new rows: 206 and 154).  A CTA whose range holds only such units of a pair does
 // not work on it; the CTA that holds its first chunk owns it.
 //
