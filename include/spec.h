@@ -647,10 +647,10 @@ spec_status spec_paged_read_fp8(const int32_t* d_slots, const int32_t* d_row_cou
  * The codes enter the products as they are.  Queries are split into two e4m3
  * parts with a power of two for each row: exact but for elements below 2^-8 of
  * the row's largest, of which 2^-17 of the largest is lost.  Scores, softmax
- * and sums are fp32; a weight enters the second product off by at most 2^-9 of
- * it, and what lies below 2^-25 of the largest weight times the largest value
- * scale among the chunks that the sequence's rows were dealt with so far (a
- * finite later draft's scale counts there too) is lost.
+ * and sums are fp32; a weight enters the second product off by at most 2^-10 of
+ * it, and by 2^-26 of the largest weight times the largest value scale among the
+ * chunks that the sequence's rows were dealt with so far (a finite later draft's
+ * scale counts there too), whatever its own size: smaller ones may be lost.
  * Values behind a sequence's length are never used, nor is a position that a
  * row may not see, whatever codes and scales are there.  A visible NaN value
  * makes that dimension of the rows that see it NaN; a visible scale byte of

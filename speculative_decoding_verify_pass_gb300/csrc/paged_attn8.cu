@@ -15,13 +15,18 @@
 // A value's scale goes into its weight, relative to r, the largest scale seen, so
 // that the codes enter the product as they are.  Weights need more range than bits
 // (a key far down still counts when there are 100000 like it), so their parts are
-// e5m2, a half's upper byte: 3 significant bits each, which is cheap to cut a half into
-// (an and, a subtraction, a byte permutation).  What a part leaves is kept times 4, then
-// times 8 more, so that together they end at 2^-25 of the reference's weight.  The parts
+// e5m2, a half's upper byte: 3 significant bits each, which is cheap to round a half to
+// (an addition, an and, a subtraction, a byte permutation).  What a part leaves is at most
+// half of its last bit, so that it can be kept times 8, then times 16 more, without passing
+// the weight: off by 2^-11 of the weight's power of two (and 2^-11 by the half), and by
+// 2^-24 where e5m2 and halves end (2^-17 / 128, and 2^-25), 1.5 * 2^-27 of the reference's
+// weight.  (Parts that are cut and kept times 4 and 8 left 2^-10 and 2^-22; 24 sequences of
+// 16 new at 8 heads a kv head took 125.4 us with them, 128.8 so.)  A NaN may get lost in the
+// parts, not in its row's sum, by which the row is divided.  The parts
 // lie side by side in the product's N (3 RP columns of O^T, joined by the results): one
 // product for all costs as much as one part's as long as N is this small.
 //
-// A half overflows 2^13 above the references.  So a segment's first chunk gives them (the
+// A half's first part overflows 2^13 above the references.  So a segment's first chunk gives them (the
 // rows' maxima, the largest value scale), and a later chunk in which some half is
 // infinite makes its warpgroup move references, sums and O^T up to its maxima, and is
 // taken again; the vote on it rides on the barrier that the P^T buffer needs anyway.
@@ -53,14 +58,15 @@ namespace sv {
 namespace {
 
 using plan8::kFewSeqs;
+using plan8::kPart2;
+using plan8::kPart3;
 using plan8::kParts;
 using plan8::kScaleSlots;
 using plan8::kSegs;
+using plan8::kShift8;
 using plan8::Plan;
 using plan8::Seg;
 
-constexpr int kShift8 = 3;              // weights are kept times 2^3, so that they overflow a half 2^13 above the references
-constexpr float kPart2 = 4.f, kPart3 = 8.f;     // the second part is kept times 4, the third times 4 * 8
 constexpr int kNearScale = 12;          // where references move, the values' does if a scale is more than this above it
 constexpr int kFarScale = 100;          // and a scale this far above it moves it in any case (powers of two end there)
 constexpr int kLowScale = -60;          // one further below counts as that: 2^-60 of a value that counts is nothing
@@ -225,8 +231,8 @@ __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {    // a 
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-constexpr uint32_t kHalves2 = 0x44004400u, kHalves3 = 0x48004800u;  // kPart2 and kPart3 twice
-static_assert(kPart2 == 4.f && kPart3 == 8.f, "as halves");
+constexpr uint32_t kHalves2 = 0x48004800u, kHalves3 = 0x4C004C00u;  // kPart2 and kPart3 twice
+static_assert(kPart2 == 8 && kPart3 == 16, "as halves");
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, 0x7531;" : "=r"(r) : "r"(a), "r"(b));
@@ -826,9 +832,9 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                             v = ex2_approx(v);
                             h[k] = cvt_f16x2(mul2(F2(u, v), vm2));
                             top = max_f16x2(top, h[k]);
-                            t1[k] = h[k] & 0xFF00FF00u;                                     // cut to e5m2
+                            t1[k] = (h[k] + 0x00800080u) & 0xFF00FF00u;                     // rounded to e5m2
                             h[k] = mul_f16x2(sub_f16x2(h[k], t1[k]), kHalves2);
-                            t2[k] = (h[k] + 0x00800080u) & 0xFF00FF00u;                     // rounded to it
+                            t2[k] = (h[k] + 0x00800080u) & 0xFF00FF00u;
                             h[k] = mul_f16x2(sub_f16x2(h[k], t2[k]), kHalves3) + 0x00800080u;   // the last part's upper bytes, rounded
                         }
                         c1[e] = upper_bytes(t1[0], t1[1]);
@@ -872,8 +878,8 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     }
                     fence_proxy_async_smem();
                     tc_fence_before();
-                    // Weights that overflow a half: the references move, and the chunk is taken again.
-                    const bool over = ((top + 0x04000400u) & 0x80008000u) != 0 || dv > kFarScale;
+                    // Weights whose first part overflows (from 61440 on): the references move, and the chunk is taken again.
+                    const bool over = ((top + 0x04800480u) & 0x80008000u) != 0 || dv > kFarScale;
                     if (!bar_any(bar, 128, over && !move) || move) break;
                 }
 #pragma unroll

@@ -20,6 +20,8 @@ constexpr int kAhead = 64 * 1024;
 constexpr int kSlots = kAhead / (kChunk * 64);
 constexpr int kScaleSlots = 8;              // chunks whose scales are loaded ahead
 constexpr int kParts = 3;                   // parts of a weight
+constexpr int kShift8 = 3;                  // weights are kept times 2^3, so that they overflow a half 2^13 above the references
+constexpr int kPart2 = 8, kPart3 = 16;      // the second part is kept times 8, the third times 8 * 16
 constexpr int kSegs = 8;                    // segments in the list: those ahead, and those whose results are not written
 constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
 
