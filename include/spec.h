@@ -648,14 +648,17 @@ spec_status spec_paged_read_fp8(const int32_t* d_slots, const int32_t* d_row_cou
  * parts with a power of two for each row: exact but for elements below 2^-8 of
  * the row's largest, of which 2^-17 of the largest is lost.  Scores, softmax
  * and sums are fp32; a weight enters the second product off by at most 2^-10 of
- * it, and by 2^-26 of the largest weight times the largest value scale among the
- * chunks that the sequence's rows were dealt with so far (a finite later draft's
- * scale counts there too), whatever its own size: smaller ones may be lost.
+ * it, and, whatever its own size, by so much that its contribution (weight times
+ * value scale) is off by at most 2^-21 of the largest contribution among the
+ * positions that the row sees (2^-24 where the rows of a block have
+ * contributions of one size): smaller ones may be lost.
  * Values behind a sequence's length are never used, nor is a position that a
- * row may not see, whatever codes and scales are there.  A visible NaN value
+ * row may not see, whatever codes and scales are there: what a row's result is
+ * does not depend on later drafts (its last bits may).  A visible NaN value
  * makes that dimension of the rows that see it NaN; a visible scale byte of
  * 255, or a NaN key, makes the whole row NaN, and an infinite or NaN query
- * element its own row.
+ * element its own row.  Weights are summed as in spec_paged_attention: visible
+ * values should stay below 2^62 in magnitude, and contributions above 2^-110.
  * A score is formed as (the sum over the codes) * (the key's scale) * (the
  * query row's power of two * scale * log2(e)), each product in fp32: exact in
  * range as long as a key's scale lies within 2^-100 .. 2^100 and a query row's

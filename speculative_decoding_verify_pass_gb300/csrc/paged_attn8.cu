@@ -11,24 +11,33 @@
 //                       q is lost but below 2^-17 of the row's largest element.  The
 //                       parts are two products into the same S^T.
 //     P^T = exp2(2^(a + ek) scale log2e S^T - m)    ek: the key's scale
-//     O^T += V8^T P'^T  P' = 2^(ev - r + 3) P as a half, in three e5m2 parts; ev: the value's scale
-// A value's scale goes into its weight, relative to r, the largest scale seen, so
-// that the codes enter the product as they are.  Weights need more range than bits
+//     O^T += V8^T P'^T  P' = g 2^ev P as a half, in three e5m2 parts; ev: the value's scale
+// A value's scale goes into its weight, so that the codes enter the product as they are.
+// The row's gain g, a power of two, brings the largest contribution P 2^ev among the keys
+// that the row sees to 2 .. 4: what counts is what a position adds to the result, so that
+// a value that the row does not see or gives next to no weight sets nothing, however large it is,
+// and neither does a key that takes all weight and has no value.  (The sums are of P, in 32
+// bits; the results divide by g.)  Weights need more range than bits
 // (a key far down still counts when there are 100000 like it), so their parts are
 // e5m2, a half's upper byte: 3 significant bits each, which is cheap to round a half to
 // (an addition, an and, a subtraction, a byte permutation).  What a part leaves is at most
 // half of its last bit, so that it can be kept times 8, then times 16 more, without passing
 // the weight: off by 2^-11 of the weight's power of two (and 2^-11 by the half), and by
-// 2^-24 where e5m2 and halves end (2^-17 / 128, and 2^-25), 1.5 * 2^-27 of the reference's
-// weight.  (Parts that are cut and kept times 4 and 8 left 2^-10 and 2^-22; 24 sequences of
+// 2^-24 where e5m2 and halves end (2^-17 / 128, and 2^-25), 1.5 * 2^-25 of the largest
+// contribution.  (Parts that are cut and kept times 4 and 8 left 2^-10 and 2^-22; 24 sequences of
 // 16 new at 8 heads a kv head took 125.4 us with them, 128.8 so.)  A NaN may get lost in the
 // parts, not in its row's sum, by which the row is divided.  The parts
 // lie side by side in the product's N (3 RP columns of O^T, joined by the results): one
 // product for all costs as much as one part's as long as N is this small.
 //
-// A half's first part overflows 2^13 above the references.  So a segment's first chunk gives them (the
-// rows' maxima, the largest value scale), and a later chunk in which some half is
-// infinite makes its warpgroup move references, sums and O^T up to its maxima, and is
+// The 16 rows of a thread whose largest contributions lie within 2^3 of one another, as rows
+// of one size of values do, share the largest's gain, which then is one factor a key: a
+// multiplication for every two weights less (the same case 139 us without sharing, 131 with).
+// It costs the smallest of them 3 bits at the lower end.
+//
+// A half's first part overflows 2^14 above the references.  So a segment's first chunk gives
+// them (by row, the largest score and contribution), and a later chunk in which some half
+// overflows makes its warpgroup move references, gains, sums and O^T up to its own, and is
 // taken again; the vote on it rides on the barrier that the P^T buffer needs anyway.
 //
 // Roles, by warpgroup: softmax (thread = key, 16 rows; 2 of them for tiles of 16 rows,
@@ -67,9 +76,15 @@ using plan8::kShift8;
 using plan8::Plan;
 using plan8::Seg;
 
-constexpr int kNearScale = 12;          // where references move, the values' does if a scale is more than this above it
-constexpr int kFarScale = 100;          // and a scale this far above it moves it in any case (powers of two end there)
-constexpr int kLowScale = -60;          // one further below counts as that: 2^-60 of a value that counts is nothing
+// A row's largest contribution (weight times value scale) is kept as an exponent byte, top;
+// its gain is 2^(kShift8 + 127 - top).
+constexpr int kGainBytes = 254 + kShift8;   // exponent byte of a gain, plus top
+constexpr int kLeastTop = 1 + kShift8;      // the gain stays below 2^127
+constexpr int kSpread = 3;                  // rows of a thread whose tops lie this close share the largest
+constexpr int kMostBytes = 127 - kShift8;   // a value scale further above a shared top has no factor
+constexpr int kApart = -512;                // (in place of one: rows that share none)
+constexpr int kFarScale = 40;               // a value scale this far below every top: its weight overflows no half before sums might,
+constexpr float kFarWeight = 1ull << (16 - kShift8 + kFarScale);    // so it is looked at itself (one that halves let pass is no larger)
 
 struct Paged8Params : PagedCommon {
     CUtensorMap mk, mv;
@@ -689,8 +704,9 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
             F2 l[NC / 2];                       // the rows' sums over this thread's keys
 #pragma unroll
             for (int j = 0; j < NC / 2; ++j) l[j] = F2(0.f, 0.f);
+            const uint32_t gains = kept(shb + (uint32_t)offsetof(F, gain) + ((par * kGroups + gi) * RP + col0) * 4);
             bool fresh = true;
-            int vref = 0;                       // scale byte that O^T is relative to
+            int most = 0, shared = 0;           // the rows' largest top, and the one that they share
 #pragma unroll 1
             for (uint32_t i = unit + (kStream ? (unit ^ gi) & 1u : 0u); i < unit + w.units; i += kGroups) {
                 const uint32_t b = i & 1, use = (i >> 1) & 1;       // P^T buffer, its round
@@ -736,41 +752,59 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     if (move) {
                         // The references move up to the chunk's maxima (a first chunk's become
                         // them), the sums and O^T with them.
-                        float (*const mx)[RP] = sh.xl[par][gi];
+                        float (*const mx)[RP] = sh.xl[par][gi], (*const cx)[RP] = sh.xc[gi];
+                        const float ev = (float)vb;
 #pragma unroll 1
                         for (int j = 0; j < NC && j < rows; j += 8) {
-                            float v[8], keep = 0.f;
+                            float v[8], m[8], keep = 0.f, keep2 = 0.f;
                             tmem_ld8_async(st + j, v);
                             const float4 f = lds4(qmul + j * 4), g = lds4(qmul + j * 4 + 16);
                             const float fs[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
                             tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const float m = warp_max(j + e < hidden ? -INFINITY : v[e] * km * fs[e]);
-                                if (lane == e) keep = m;
+                                v[e] = j + e < hidden ? -INFINITY : __fmul_rn(__fmul_rn(v[e], km), fs[e]);
+                                m[e] = warp_max(v[e]);
+                                if (lane == e) keep = m[e];
                             }
-                            if (lane < 8) mx[qd][col0 + j + lane] = keep;
+                            // Contributions, beside the warp's largest weight: a difference of scores is
+                            // exact where it counts, whatever their size.
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float c = warp_max(v[e] - m[e] + ev);
+                                if (lane == e) keep2 = c;
+                            }
+                            if (lane < 8) mx[qd][col0 + j + lane] = keep, cx[qd][col0 + j + lane] = keep2;
                         }
-                        const int vt = __reduce_max_sync(0xffffffffu, vb);
-                        if (lane == 0) sh.vtop[wg][qd] = vt;
                         // the last product into this O^T: of this team's chunk before
                         if (!fresh && qd == 0) wait(BAR(p_empty, (i - kGroups) & 1), ((i - kGroups) >> 1) & 1, dead);
                         named_bar_sync(bar, 128);
                         tc_fence_after();
-                        int vnow = max(max(sh.vtop[wg][0], sh.vtop[wg][1]), max(sh.vtop[wg][2], sh.vtop[wg][3]));
-                        if (!fresh && vnow <= vref + kNearScale) vnow = vref;
-                        const float vshrink = scale_of(max(vref - vnow + 127, 0));      // 1 or less (not used at first)
                         if (key < NC) {         // one thread per row: the new reference, and what the old weights shrink by
                             const int r = col0 + key;
+                            const bool live = key < rows;
                             const float m = fmaxf(fmaxf(mx[0][r], mx[1][r]), fmaxf(mx[2][r], mx[3][r]));
                             const float old = fresh ? kNone : -sh.nref[par][gi][r];
-                            const float now = key < rows ? fmaxf(old, m) : INFINITY;      // rows past R weigh nothing
+                            const float now = live ? fmaxf(old, m) : INFINITY;      // rows past R weigh nothing
                             sh.nref[par][gi][r] = -now;
-                            const float f = key < rows ? ex2_approx(old - now) : 0.f;
+                            // The largest contribution: this chunk's rounded up, the earlier ones' down.  (A row that
+                            // sees nothing, or NaN alone, has none.)
+                            const float c = fmaxf(fmaxf(cx[0][r] + (mx[0][r] - now), cx[1][r] + (mx[1][r] - now)),
+                                                  fmaxf(cx[2][r] + (mx[2][r] - now), cx[3][r] + (mx[3][r] - now)));
+                            const int old_top = fresh ? kLeastTop : sh.top[gi][r];
+                            int top = max(max(__float2int_ru(c), __float2int_rd((float)old_top + (old - now))), kLeastTop);
+                            sh.top[gi][r] = top;
+                            const int was = fresh ? top : kGainBytes - (int)(__float_as_uint(sh.gain[par][gi][r]) >> 23);
+                            const int high = __reduce_max_sync((1u << NC) - 1u, live ? top : 0);
+                            // (one that has seen no key moves when it does)
+                            const bool near = __all_sync((1u << NC) - 1u, !live || now == kNone || top >= high - kSpread);
+                            if (near) top = high;
+                            if (key == 0) sh.tops[wg][0] = high, sh.tops[wg][1] = near ? high : kApart;
+                            sh.gain[par][gi][r] = __uint_as_float((uint32_t)(kGainBytes - top) << 23);
+                            const float f = live ? ex2_approx(old - now) : 0.f;
                             sh.shrink[gi][r] = f;
-                            sh.oshrink[gi][r] = f * vshrink;
+                            sh.oshrink[gi][r] = f * __uint_as_float((uint32_t)(min(max(was - top, -126), 127) + 127) << 23);
                         }
-                        if (key == 0) sh.vref[par][wg] = vnow;
                         named_bar_sync(bar, 128);
                         if (!fresh) {
                             const uint32_t shrink = shb + (uint32_t)offsetof(F, shrink) + (gi * RP + col0) * 4;
@@ -796,11 +830,9 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                             }
                             tmem_wait_st();
                         }
-                        vref = vnow;
+                        most = sh.tops[wg][0];
+                        shared = sh.tops[wg][1];
                     }
-                    const int dv = vb - vref;
-                    const float vm = __uint_as_float((uint32_t)(min(max(dv, kLowScale), kFarScale) + kShift8 + 127) << 23);
-                    const F2 vm2(vm, vm);
                     // Scores less their references: rounded products, as a reference is, so that a
                     // reference and the score that it comes from cancel whatever their size (a fused
                     // product of a score past 2^24 differs from it by powers of two, past 2^31 by more
@@ -821,16 +853,29 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     if (kStream) wait(BAR(p_empty, b), use ^ 1, dead);
                     uint32_t top = 0;           // the largest halves
                     static_assert(NC == 16, "a thread's rows are one 16-byte piece of each part");
-                    uint32_t c1[4], c2[4], c3[4];
+                    uint32_t c1[4], c2[4], c3[4], halves[NC / 2];
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) x[j] = ex2_approx(x[j]);
+                    // weight times gain times value scale (a weight of zero stays zero)
+                    if (vb - shared <= kMostBytes) {
+                        const float vm = __uint_as_float((uint32_t)max(vb - shared + kGainBytes - 127, 0) << 23);
+#pragma unroll
+                        for (int j = 0; j < NC; j += 2) halves[j / 2] = cvt_f16x2(mul2(F2(x[j], x[j + 1]), F2(vm, vm)));
+                    } else {
+                        const float vm = scale_of(vb);
+#pragma unroll
+                        for (int j = 0; j < NC; j += 4) {
+                            const float4 g = lds4(gains + j * 4);
+                            halves[j / 2] = cvt_f16x2(mul2(mul2(F2(x[j], x[j + 1]), F2(g.x, g.y)), F2(vm, vm)));
+                            halves[j / 2 + 1] = cvt_f16x2(mul2(mul2(F2(x[j + 2], x[j + 3]), F2(g.z, g.w)), F2(vm, vm)));
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t h[2], t1[2], t2[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            float &u = x[4 * e + 2 * k], &v = x[4 * e + 2 * k + 1];
-                            u = ex2_approx(u);
-                            v = ex2_approx(v);
-                            h[k] = cvt_f16x2(mul2(F2(u, v), vm2));
+                            h[k] = halves[2 * e + k];
                             top = max_f16x2(top, h[k]);
                             t1[k] = (h[k] + 0x00800080u) & 0xFF00FF00u;                     // rounded to e5m2
                             h[k] = mul_f16x2(sub_f16x2(h[k], t1[k]), kHalves2);
@@ -879,7 +924,13 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                     fence_proxy_async_smem();
                     tc_fence_before();
                     // Weights whose first part overflows (from 61440 on): the references move, and the chunk is taken again.
-                    const bool over = ((top + 0x04800480u) & 0x80008000u) != 0 || dv > kFarScale;
+                    bool over = ((top + 0x04800480u) & 0x80008000u) != 0;
+                    if (vb < most - kFarScale) {        // (no value, or one that is nothing beside the others)
+                        float largest = 0.f;
+#pragma unroll
+                        for (int j = 0; j < NC; ++j) largest = fmaxf(largest, x[j]);
+                        over = over || largest > kFarWeight;
+                    }
                     if (!bar_any(bar, 128, over && !move) || move) break;
                 }
 #pragma unroll
@@ -1019,9 +1070,10 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
                 } else {
                     p.part_ml[(size_t)w.slot * RP + r] = make_float2(ma, la);
                 }
-                // O^T is in units of 2^(r - 3), r the warpgroup's that formed the row's weights
-                fa = fa * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][ga * kTeam + r / NC]);
-                if (two) fb = fb * (1.f / (1 << kShift8)) * scale_of(sh.vref[par][(ga ^ 1) * kTeam + r / NC]);
+                // the gain in O^T, a power of two, taken back
+                auto undo = [&](int g) { return __uint_as_float((254u << 23) - __float_as_uint(sh.gain[par][g][r])); };
+                fa *= undo(ga);
+                if (two) fb *= undo(ga ^ (kGroups - 1));
                 sh.row[par][r] = {{fa, fb}, t * p.out_stride + (long long)(r - t * p.group) * HD};
             }
             if (qd == 0) wait(BAR(o_full, par), (seg >> 1) & 1, dead);

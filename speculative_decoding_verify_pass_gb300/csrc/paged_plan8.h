@@ -20,7 +20,11 @@ constexpr int kAhead = 64 * 1024;
 constexpr int kSlots = kAhead / (kChunk * 64);
 constexpr int kScaleSlots = 8;              // chunks whose scales are loaded ahead
 constexpr int kParts = 3;                   // parts of a weight
-constexpr int kShift8 = 3;                  // weights are kept times 2^3, so that they overflow a half 2^13 above the references
+// A row's largest contribution (weight times value scale) is kept at 2 to 4: a half overflows
+// 2^14 above it, and small contributions end 1.5 * 2^-25 of it.  A bit more for these costs
+// references that move: 24 sequences of 16 new at 8 heads a kv head 130.9 us with 2, 133.1 with
+// 3, 136.5 with 4 (200 short ones 49.3, 50.3, 51.4).
+constexpr int kShift8 = 2;
 constexpr int kPart2 = 8, kPart3 = 16;      // the second part is kept times 8, the third times 8 * 16
 constexpr int kSegs = 8;                    // segments in the list: those ahead, and those whose results are not written
 constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
@@ -68,10 +72,13 @@ struct Fixed {
     alignas(16) uint8_t scale[kScaleSlots][2][2][64];   // of a chunk: by page, keys' and values'
     alignas(16) Seg segs[kSegs];
     alignas(16) float nref[2][T::kGroups][RP];      // by segment parity: minus each row's reference
+    alignas(16) float gain[2][T::kGroups][RP];      // and what its weights are multiplied with before their values' scales
     alignas(16) float qmul[2][RP];                  // by segment parity: log2 units per unit of S^T
     alignas(16) float shrink[T::kGroups][RP];       // while references move: what the old weights shrink by,
-    alignas(16) float oshrink[T::kGroups][RP];      // and O^T, in which the values' scales are too
+    alignas(16) float oshrink[T::kGroups][RP];      // and O^T, in which the gains are too
     alignas(16) float xl[2][T::kGroups][4][RP];     // per lane quadrant: sums (and, while a reference moves, maxima)
+    alignas(16) float xc[T::kGroups][4][RP];        // while it moves: the largest contribution beside that maximum
+    int top[T::kGroups][RP];                        // of each row: the exponent byte of its largest contribution so far
     alignas(16) int tok[RP];                        // token of each row of a block that begins with a token
     Out row[2][RP];                                 // by segment parity: for the results
     long long warp_sum[T::kWarps];
@@ -80,8 +87,7 @@ struct Fixed {
         seg_full[kSegs], seg_empty[kSegs], fin[2];
     int first[split::kMaxSeqs + 1];
     int few_start[kFewSeqs + 1], few_len[kFewSeqs]; // a batch this small is not read from memory twice
-    int vtop[T::kSoftGroups][4];                       // by softmax warpgroup and quadrant: largest value scale of a chunk
-    int vref[2][T::kSoftGroups];                       // by segment parity and softmax warpgroup: the value scale that its weights are in
+    int tops[T::kSoftGroups][2];                       // by softmax warpgroup: its rows' largest contribution, and that of all if it is one
     int poison[2];                                  // 1 + the last segment (by parity) that silenced a value
     uint32_t tmem_base;
     int dead, total;
