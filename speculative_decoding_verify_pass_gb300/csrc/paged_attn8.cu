@@ -479,9 +479,11 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
     // token of row r of a block, counted from its first row's (which the block may begin in the middle of)
     auto token = [&](const Seg& s, int r) { return RP == split8::kMostRows && p.group > RP ? (int)(s.skip + r >= p.group) : sh.tok[r]; };
     Ring<kSegs> sr;                             // every role's place in the list of segments
+    int before = 0;                             // chunks of the segment before: who has no part in them waits here for all
     auto take = [&]() {                         // the next segment
-        wait(BAR(seg_full, sr.at), sr.round, dead);
+        wait(BAR(seg_full, sr.at), sr.round, dead, plan8::wait_rounds(before));
         const Seg s = sh.segs[sr.at];
+        before = s.units;
         __syncwarp();
         arrive_if(BAR(seg_empty, sr.at), lane == 0);
         sr.step();
@@ -1030,10 +1032,11 @@ __global__ void __block_size__((32 * Plan<HD, RP>::kWarps, 1, 1)) __maxnreg__((P
         int i = 0;                              // the segment's first unit
 #pragma unroll 1
         for (int seg = -1;; ++seg) {            // the next segment's queries, then this one's results
-            wait(BAR(seg_full, sr.at), sr.round, dead);
+            wait(BAR(seg_full, sr.at), sr.round, dead, plan8::wait_rounds(before));
             __syncwarp();
             if (bar_any(kResultBar, 128, raised(dead))) break;
-            const bool more = sh.segs[sr.at].units != 0;
+            before = sh.segs[sr.at].units;
+            const bool more = before != 0;
             if (more) split_queries(sh.segs[sr.at], (seg + 1) & 1);
             const int here = (sr.at + kSegs - 1) % kSegs;
             sr.step();

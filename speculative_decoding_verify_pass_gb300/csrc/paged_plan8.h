@@ -29,8 +29,10 @@ constexpr int kPart2 = 8, kPart3 = 16;      // the second part is kept times 8, 
 constexpr int kSegs = 8;                    // segments in the list: those ahead, and those whose results are not written
 constexpr int kFewSeqs = 64;                // a batch whose lengths are kept in shared memory
 
-// Limits of one wait (2^31 cycles each) that the results of a segment are waited for:
-// the other waits last a few chunks at most, this one all of them, up to 2^19.
+// Limits of one wait (2^31 cycles each) for what comes when a segment's chunks are through:
+// the next entry of the list, which follows the last copy of K (the results' warps and softmax
+// warps without rows wait for it from the segment's start), and the sums.  The other waits
+// last a few chunks at most, these all of them, up to 2^19.
 constexpr int wait_rounds(int units) { return 1 + (units >> 15); }
 
 // A segment, as the roles need it.
