@@ -243,7 +243,8 @@ spec_status spec_rope(const void* d_x, int64_t x_stride, void* d_out, int64_t ou
     const int64_t row = (int64_t)heads * head_dim, whole = type == SPEC_FP32 ? 4 : 8;
     if (x_stride < row || out_stride < row || x_stride % whole || out_stride % whole || x_stride >= (1ll << 38) || out_stride >= (1ll << 38))
         return bad("spec_rope: row strides must be multiples of 16 bytes, at least heads * head_dim and below 2^38");
-    if ((d_pos_opt != nullptr) == (d_row_start_opt != nullptr) || (d_row_start_opt != nullptr) != (d_len_opt != nullptr)) {
+    // (no lengths may be a null pointer)
+    if (d_pos_opt ? d_row_start_opt || d_len_opt : !d_row_start_opt || (!d_len_opt && nseq != 0)) {
         if (rows) return bad("spec_rope: positions come from d_pos, or from d_row_start and d_len (one of the two)");
     }
     if (!d_pos_opt && (nseq < 0 || nseq > SPEC_MAX_SEQS)) return bad("spec_rope: nseq must be in 0..1024");

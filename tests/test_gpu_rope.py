@@ -191,3 +191,14 @@ def test_graph_other_stream_and_refusals():
         with pytest.raises(sv.SpecError):
             bad()
     assert sv.spec_rope(x[:0], turns, d_pos=p[:0]).shape == (0, 2, 64)
+
+
+def test_a_batch_of_no_sequences():
+    torch = torch_cuda()
+    sv = sv_()
+    turns, _ = sv.spec_rope_table(64)
+    x, out = torch.randn((5, 3, 64), device="cuda").bfloat16(), torch.full((5, 3, 64), 7.0, device="cuda").bfloat16()
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert sv.spec_rope(x, turns, i32([0]), none, d_out=out) is out
+    assert (out == 7.0).all()
+    assert sv.spec_rope(x, turns, i32([0]), none).shape == x.shape

@@ -131,6 +131,13 @@ def test_nothing_to_turn_is_no_error(sv):
     assert call(sv, dict(nseq=0, x=None, out=None)) == 0
 
 
+def test_a_batch_of_no_sequences_is_no_error(sv):
+    """Lengths of no sequences may be a null pointer, which is what an empty tensor has."""
+    assert call(sv, dict(nseq=0, len=None)) == 0
+    for over in (dict(nseq=0, start=None), dict(nseq=0, start=None, len=None), dict(nseq=0, len=None, pos=P)):
+        assert call(sv, over) == sv.SPEC_ERR_INVALID_ARG and "one of the two" in sv.library().spec_last_error().decode()
+
+
 def test_binding_refuses_host_tensors(sv):
     torch = pytest.importorskip("torch")
     x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
