@@ -144,6 +144,13 @@ namespace {
 
 void sv::set_last_error(const char* msg) { g_err = msg ? msg : ""; }
 
+int sv::current_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
 namespace {
 
 spec_status dalloc(spec_model* h, void** p, size_t bytes, std::vector<void*>* owner = nullptr) {

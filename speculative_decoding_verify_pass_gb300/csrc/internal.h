@@ -234,5 +234,7 @@ cudaError_t launch_sample_accept(const SampleParams& p, cudaStream_t s, bool pdl
 
 // Sets the thread-local message returned by spec_last_error (api.cu).
 void set_last_error(const char* msg);
+// SMs of the current device, its index checked; 0 on an error (api.cu).
+int current_sms();
 
 }  // namespace sv

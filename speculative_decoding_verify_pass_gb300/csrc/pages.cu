@@ -348,7 +348,12 @@ spec_status spec_paged_append(const void* d_k, int64_t k_stride, const void* d_v
                    static_cast<uint16_t*>(d_vpool), num_pages, d_error_opt};
     const int64_t pieces = (int64_t)rows * n_kv_heads * (head_dim / 8);
     const int64_t want = (pieces + 255) / 256;
-    const unsigned grid = (unsigned)(want < 8 * 152 ? want : 8 * 152);
+    const int sms = current_sms();
+    if (!sms) {
+        set_last_error("spec_paged_append: no current CUDA device");
+        return SPEC_ERR_CUDA;
+    }
+    const unsigned grid = (unsigned)(want < 8 * sms ? want : 8 * sms);
     void* args[] = {&p};
     return done(launch((const void*)paged_append_kernel, grid, 256, static_cast<cudaStream_t>(cuda_stream), args));
 }

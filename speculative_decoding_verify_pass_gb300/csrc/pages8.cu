@@ -27,11 +27,11 @@ namespace sv {
 namespace {
 
 constexpr int kThreads = 256, kElems = 8;       // of a CTA; of a key row, and of a value row, that a thread takes
-constexpr int kGrid = 152 * 8;                  // CTAs at most
+constexpr int kCtas = 8;                        // of an SM, at most
 
 struct Pools8 {
     uint8_t *k, *v, *scales;    // [page][hkv][64][hd] twice, [page][hkv][2][64]
-    int num_pages, hkv, hd;
+    int num_pages, hkv;
 };
 
 struct Rows8Params {
@@ -219,11 +219,15 @@ spec_status run(const char* call, const void* fn, const void* d_k, int64_t k_str
     p.pool.scales = static_cast<uint8_t*>(const_cast<void*>(d_scales));
     p.pool.num_pages = num_pages;
     p.pool.hkv = n_kv_heads;
-    p.pool.hd = head_dim;
     p.err = d_error_opt;
-    const int64_t want = ((int64_t)rows * n_kv_heads * (head_dim / kElems) + kThreads - 1) / kThreads;
+    const int sms = current_sms();
+    if (!sms) {
+        bad(call, "no current CUDA device");
+        return SPEC_ERR_CUDA;
+    }
+    const int64_t most = (int64_t)kCtas * sms, want = ((int64_t)rows * n_kv_heads * (head_dim / kElems) + kThreads - 1) / kThreads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(want < kGrid ? want : kGrid));
+    cfg.gridDim = dim3((unsigned)(want < most ? want : most));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     cudaLaunchAttribute attr[1];

@@ -255,6 +255,11 @@ spec_status spec_rope(const void* d_x, int64_t x_stride, void* d_out, int64_t ou
     if (misaligned(d_row_start_opt, 4) || misaligned(d_len_opt, 4) || misaligned(d_pos_opt, 4))
         return bad("spec_rope: an int32 pointer is not 4-byte aligned");
     if (d_x == d_out && x_stride != out_stride) return bad("spec_rope: in place, both strides must be the same");
+    const int sms = current_sms();
+    if (!sms) {
+        set_last_error("spec_rope: no current CUDA device");
+        return SPEC_ERR_CUDA;
+    }
     RopeParams p;
     p.x = d_x;
     p.out = d_out;
@@ -272,7 +277,7 @@ spec_status spec_rope(const void* d_x, int64_t x_stride, void* d_out, int64_t ou
     p.gain = gain;
     p.inverse = inverse != 0;
     p.copy = d_x != d_out && rotary_dim < head_dim;
-    p.split = rows <= 4 * 152 ? 3 : 0;
+    p.split = rows <= 4 * sms ? 3 : 0;
     const void* fn = type == SPEC_BF16   ? variant<__nv_bfloat16>(p.pairs, interleaved != 0)
                      : type == SPEC_FP16 ? variant<__half>(p.pairs, interleaved != 0)
                                          : variant<float>(p.pairs, interleaved != 0);

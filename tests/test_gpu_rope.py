@@ -202,3 +202,15 @@ def test_a_batch_of_no_sequences():
     assert sv.spec_rope(x, turns, i32([0]), none, d_out=out) is out
     assert (out == 7.0).all()
     assert sv.spec_rope(x, turns, i32([0]), none).shape == x.shape
+
+
+@pytest.mark.parametrize("over", [-1, 0, 1])
+def test_rows_on_both_sides_of_where_a_row_gets_one_warp(over):
+    """Up to 4 rows an SM of the device have 8 warps each."""
+    torch = torch_cuda()
+    sv = sv_()
+    rows = 4 * torch.cuda.get_device_properties(0).multi_processor_count + over
+    turns, _ = sv.spec_rope_table(48, 1e4)
+    x = torch.randn((rows, 9, 64), device="cuda").bfloat16()
+    pos = torch.randint(0, 100000, (rows,), dtype=torch.int32, device="cuda")
+    check(sv.spec_rope(x, turns, d_pos=pos), x, pos.tolist(), frequencies(turns), 1.0, False, False)

@@ -155,3 +155,13 @@ def test_step_model_affine_fit():
     resid = [abs(t - t0 - x / bw) / t for x, t in zip(b, [1.0e-3, 1.7e-3, 2.0e-3, 2.6e-3])]
     assert abs(err - max(resid)) < 1e-12 and err > 0.01
     assert abs(sm.model_time(1e-4, 1e12, [1e9, 3e9]) - (2e-4 + 4e-3)) < 1e-15
+
+
+def test_launches_without_a_handle_ask_the_device_for_its_size():
+    """No number of SMs is written into their dispatch (comments state what was measured on how many)."""
+    csrc = os.path.join(ROOT, "speculative_decoding_verify_pass_gb300", "csrc")
+    for name in ("pages.cu", "pages8.cu", "rope.cu", "paged_attn.cu", "paged_attn8.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"\b152\b", code), name
+        assert "current_sms()" in code, name
