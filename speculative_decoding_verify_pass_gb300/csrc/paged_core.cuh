@@ -1,6 +1,6 @@
 // What the attention kernels over a paged cache share, whatever its pages hold:
-// waits, tensor-memory and matrix-descriptor helpers, the walk over a segment's
-// pages, the join of pairs that CTAs shared, and the host's part of a launch.
+// tensor-memory helpers, the walk over a segment's pages, the join of pairs that CTAs
+// shared, and the host's part of a launch.
 #pragma once
 
 #include <cuda.h>
@@ -45,26 +45,7 @@ struct PagedCommon {
     Meta* meta;                 // [ctas][2]: the pair that goes on into the CTA, the pair that begins in it and goes on
 };
 
-__device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// Shared-memory matrix descriptor with the 128-byte swizzle.  K-major: 8-row
-// groups sbo apart (lbo unused).  MN-major: 64-element column blocks lbo apart,
-// 8-row (k) groups sbo apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-
-// The upper half of such a descriptor (stride, version, swizzle).
-constexpr uint32_t hi_sw128(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
-
-// 8, 16 or 32 consecutive fp32 columns of this warp's 32 lanes, not waited for.
+// 8 or 16 consecutive fp32 columns of this warp's 32 lanes, not waited for.
 __device__ __forceinline__ void tmem_ld8_async(uint32_t t, float* v) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -84,20 +65,6 @@ __device__ __forceinline__ void tmem_ld16_async(uint32_t t, float* v) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld32_async(uint32_t t, float* v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(t)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st8(uint32_t t, const float* v) {
@@ -123,11 +90,6 @@ struct F2 {
     __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
     __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
 };
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -154,33 +116,11 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Wait bounded in time (2^31 cycles, about a second, whatever one poll takes; more
-// rounds of that while nothing else has given up); one that gives up raises `dead`.  Inline (a call would fix the registers that
-// setmaxnreg moves) and short: the roles' loops share one instruction cache.
-// A role whose wait failed waits no more.
+// The SM's clock: waits are bounded in time, by 2^31 cycles (about a second).
 __device__ __forceinline__ uint32_t cycles() {
     uint32_t c;
     asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
     return c;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead, int rounds = 1) {
-    uint32_t t0 = cycles();
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (cycles() - t0 > 0x7fffffffu) {
-            if (--rounds > 0 && !*dead) {
-                t0 = cycles();
-                continue;
-            }
-            *dead = 1;
-            return false;
-        }
-    return true;
-}
-// After a failed wait: let what is in flight finish before the CTA ends.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) __nanosleep(64);
 }
 
 // Position in a ring of N buffers: index and the parity of its current round.
