@@ -562,7 +562,8 @@ enum {
     SPEC_ROPE_WAVELENGTH = 3, /* f_i / factor where it turns at most `low` times in the context, f_i from
                                  `high` times on, in between a blend linear in the number of turns         */
     SPEC_ROPE_PARTS = 4       /* the same blend, linear in i between the pairs that turn `high` and `low`
-                                 times (rounded outwards), and a gain of 0.1 ln(factor) + 1                */
+                                 times (rounded outwards, within 0 .. rotary_dim - 1: all are slowed where
+                                 none turns `low` times), and a gain of 0.1 ln(factor) + 1                 */
 };
 #define SPEC_ROPE_MAX_DIM 1024
 

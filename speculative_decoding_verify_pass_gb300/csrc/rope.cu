@@ -221,7 +221,7 @@ spec_status spec_rope_table(int32_t rotary_dim, double base, int32_t scaling, do
         double f = pow(b, -2.0 * i / rotary_dim), keep = 1.0;
         if (scaling == SPEC_ROPE_LINEAR) keep = 0.0;
         if (scaling == SPEC_ROPE_WAVELENGTH) keep = (context * f / circle - low) / (high - low);
-        if (scaling == SPEC_ROPE_PARTS) keep = 1.0 - (i - first) / (last - first > 1e-3 ? last - first : 1e-3);
+        if (scaling == SPEC_ROPE_PARTS) keep = i >= last ? 0.0 : i <= first ? 1.0 : 1.0 - (i - first) / (last - first);
         keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
         if (keep < 1.0) f = keep * f + (1.0 - keep) * f / factor;
         out_turns[i] = (uint64_t)nearbyint(f / circle * 18446744073709551616.0);    // f <= 1: below 2^62

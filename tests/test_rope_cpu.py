@@ -77,6 +77,23 @@ def test_parts_ramp_and_its_gain(sv):
         assert near(t, a * f / 16 + (1 - a) * f)
 
 
+@pytest.mark.parametrize("low,high,context", [(1.0, 32.0, 1), (1.0, 32.0, 6), (32.0, 64.0, 128), (32.0, 64.0, 200), (1.0, 32.0, 10 ** 9),
+                                              (0.5, 1.0, 40)])
+@pytest.mark.parametrize("dim,base", [(64, 1e4), (128, 5e5), (4, 1e4), (64, 1.01)])
+def test_parts_ramp_at_its_ends(sv, dim, base, low, high, context):
+    """Contexts in which no pair turns `low` times, or all turn `high` times: all slowed (pair 0 too), or all kept."""
+    got, _ = table(sv, dim, base, sv.SPEC_ROPE_PARTS, 16.0, low, high, context)
+    for i, t in enumerate(got):
+        f = base ** (-2 * i / dim)
+        turns = context * f / (2 * math.pi)
+        if turns <= low * base ** (-2 / dim):           # a whole pair past the ramp's end, as it is rounded outwards
+            assert near(t, f / 16)
+        elif turns >= high * base ** (2 / dim):
+            assert near(t, f)
+        else:
+            assert f / 16 * (1 - 2.0 ** -40) <= t / 2.0 ** 64 * 2 * math.pi <= f * (1 + 2.0 ** -40)
+
+
 def test_fixed_point_angle_of_far_positions(sv):
     """position * turns modulo 2^64 is the angle to a rounding of the frequency, whatever the position."""
     turns, _ = table(sv, 128, 5e5)
