@@ -621,9 +621,10 @@ spec_status spec_rope(const void* d_x, int64_t x_stride, void* d_out, int64_t ou
  * -126, such that every finite element of the (row, kv head) is at most 448 *
  * 2^e in magnitude, its scale byte is e + 127 and its codes are x * 2^-e
  * rounded to the nearest e4m3 (ties to even).  Infinities and NaN become NaN.
- * Arguments as spec_paged_append's; d_kpool, d_vpool and d_scales are 16-byte
- * aligned; strides below 2^38.  Errors: SPEC_ERR_INVALID_ARG, nothing
- * enqueued. */
+ * Arguments as spec_paged_append's, slots distinct (two rows with one slot may
+ * leave codes of one under the scale of the other); d_kpool, d_vpool and
+ * d_scales are 16-byte aligned; strides below 2^38.  Errors:
+ * SPEC_ERR_INVALID_ARG, nothing enqueued. */
 spec_status spec_paged_append_fp8(const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_slots,
                                   const int32_t* d_row_count_opt, int32_t rows, int32_t n_kv_heads, int32_t head_dim,
                                   void* d_kpool, void* d_vpool, void* d_scales, int32_t num_pages, int32_t* d_error_opt,
@@ -634,8 +635,8 @@ spec_status spec_paged_append_fp8(const void* d_k, int64_t k_stride, const void*
  * what that call wrote, but for elements above 1.9375 * 2^127, which round to
  * 2^128 and read as infinities).  Rows with a negative slot, from *d_row_count_opt on, or
  * with a slot outside the pool (which sets the error word) are left as they
- * were; a slot may be read twice.  Errors: SPEC_ERR_INVALID_ARG, nothing
- * enqueued. */
+ * were; a slot may be read twice.  d_k and d_v must not overlap.  Errors:
+ * SPEC_ERR_INVALID_ARG, nothing enqueued. */
 spec_status spec_paged_read_fp8(const int32_t* d_slots, const int32_t* d_row_count_opt, int32_t rows, int32_t n_kv_heads,
                                 int32_t head_dim, const void* d_kpool, const void* d_vpool, const void* d_scales,
                                 int32_t num_pages, void* d_k, int64_t k_stride, void* d_v, int64_t v_stride,

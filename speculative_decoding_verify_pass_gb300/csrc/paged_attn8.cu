@@ -49,14 +49,14 @@
 // 8 heads a kv head: 206 against 210 us then, 200 short ones 62 and 62), and one code
 // serves every tile.
 //
-// What bounds it: long caches memory (100003 positions of 8 kv heads of 128: 39.4 us, 30.3
-// at the copy rate; 64 ragged decodes 91.8, of 83), short sequences a segment's way through
-// the roles (2.1 us a segment of one chunk at 16 rows, 0.4 a further chunk of 64-wide
-// heads; 200 ragged blocks 46 us), many rows a chunk's way through the softmax (64 rows:
-// 2200 cycles, of which 1000 issue; 24 sequences of 16 new at 8 heads a kv head 124 us).
+// What bounds it: long caches memory (100003 positions of 8 kv heads of 128: 39.9 us, 30.3
+// at the copy rate; 64 ragged decodes 91.1, of 83), short sequences a segment's way through
+// the roles (2.2 us a segment of one chunk at 16 rows, 0.4 a further chunk of 64-wide
+// heads; 200 ragged blocks 49.6 us), many rows a chunk's way through the softmax (64 rows:
+// about 2300 cycles, half of them issue; 24 sequences of 16 new at 8 heads a kv head 131 us).
 // The roles share one instruction cache, so that code costs time wherever it stands: the
-// last two were 62 and 154 us when the kernel had 86 KB, with divisions in the walk over the
-// segments, each wait's loop twice, and rows' addresses formed where they are written.
+// last two were 62 and 154 us when the kernel had 86 KB (46 and 124 with 71), with divisions in
+// the walk over the segments, each wait's loop twice, and rows' addresses formed where they are written.
 #include <stddef.h>
 #include <stdio.h>
 
