@@ -666,8 +666,8 @@ spec_status spec_paged_read_fp8(const int32_t* d_slots, const int32_t* d_row_cou
  * range as long as a key's scale lies within 2^-100 .. 2^100 and a query row's
  * largest element above 2^-119.
  * The limit on the work: with T the smallest of 16, 32 and 64 that holds
- * max_new tokens' rows, else 64, and t the multiple of (query heads per kv
- * head) next below T (T itself if there is none), (nseq + rows * (query heads
+ * max_new tokens' rows, else 64, and t the largest multiple of (query heads per
+ * kv head) up to T (T itself if there is none), (nseq + rows * (query heads
  * per kv head) / t) * n_kv_heads * (ceil(table_pages / 2) + 4) below 2^31. */
 spec_status spec_paged_attention_fp8_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new,
                                                int32_t table_pages, size_t* out_bytes);
